@@ -333,6 +333,118 @@ int medusa_kv_compact(void* k_cache, void* v_cache, int32_t* kv_len, const int32
                       const void* hidden_tree, void* h_next, medusa_dtype dtype, int B, int Hkv,
                       int D, int Lmax, int N, int H, int Dmax, int32_t* src_idx, void* stream);
 
+/* ------------------------------------------------------------------------- */
+/* 6. The 8-bit paged KV cache                                                */
+/*                                                                           */
+/* Next to the dense caches of 3 and 5: half the bytes, and memory taken by   */
+/* the page.  One pool of pages serves all sequences of a batch:              */
+/*   k_pages, v_pages [n_pages,Hkv,P,D] uint8   e4m3 codes                    */
+/*   k_scale, v_scale [n_pages,Hkv]     float   one per page and KV head      */
+/*   page_table [B,M] int32   page of the tokens [j*P, j*P + P) of sequence b;*/
+/*                            -1: none                                        */
+/*   kv_len     [B]   int32   tokens that the sequence holds                  */
+/* value = code * scale.  A scale is readable in [2^-64, 2^64]; the library   */
+/* writes powers of two.  Slots of a page behind kv_len hold anything.        */
+/* Limits: D in {64, 128}; P in {16, 32, 64, 128}; B <= 1024; Hkv <= 1024;    */
+/* n_pages * Hkv * P < 2^31; M * P and B * M <= 2^30.                         */
+/* Small arrays that change (tables, lengths) are read from one buffer and    */
+/* written to another, so a captured round can be replayed on alternating     */
+/* buffers; the pools change in place.                                        */
+/* ------------------------------------------------------------------------- */
+
+/* 6a. Tree attention over the paged cache  [MH, "Tree attention and           */
+/* acceptance"].  As 3, with the prefix in the pages and the tree's own K and  */
+/* V rows (any number from one: N = 1 is plain decoding) beside them, so that  */
+/* rejected candidates never reach the cache:                                  */
+/*   q              [B,N,Hq,D]   dtype                                        */
+/*   k_tree, v_tree [B,N,Hkv,D]  dtype                                        */
+/*   mask           [N, ceil(N/64)] uint64 from medusa_tree_layout             */
+/*   out            [B,N,Hq,D]   dtype, rounded once from float32              */
+/* Scores, softmax and sums are float32; codes, q and tree rows enter the      */
+/* products exactly (bf16 q to 2^-19 of the largest |q| of a block of 64 or    */
+/* 128 query rows), the weights of the sum over V with at least 7 bits         */
+/* (dtype bf16) or in float32 (dtype float32).                                 */
+/* kv_len is clamped to [0, M*P].  Keys of a page that is not in               */
+/* [0, n_pages) or whose scale is not readable count as absent.  A row that    */
+/* sees no key is zero.  A row that sees a tree row with a non-finite V is     */
+/* NaN; rows that do not see it are not affected.                              */
+/* Limits: N <= 512, Hq % Hkv == 0, N * (Hq/Hkv) <= 4096; scale > 0, finite.   */
+size_t medusa_tree_attention_q8_workspace(int B, int N, int Hq, int Hkv, int D, medusa_dtype dtype);
+int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype,
+                             const void* k_pages, const void* v_pages, const float* k_scale,
+                             const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
+                             const uint64_t* mask, int B, int N, int Hq, int Hkv, int D, int P,
+                             int n_pages, int M, float scale, void* out, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* 6b. Append rows  [MH, "Tree attention and acceptance": keep the longest     */
+/* accepted branch; its last hidden state feeds the heads next round].         */
+/* Row rows[b,i] (or row i where rows is NULL) of sequence b goes to slot      */
+/* kv_len[b] + i, for i = 0..last[b] (all R where last is NULL); kv_len_out[b]  */
+/* = kv_len[b] + last[b] + 1.  With path_nodes for rows and accept_len for     */
+/* last this keeps a tree's accepted branch; with rows NULL it writes prompts  */
+/* (ragged through last, -1: nothing) and decoded tokens.                      */
+/*   k_rows, v_rows [B,T,Hkv,D] dtype; rows [B,R] int32; last [B] int32        */
+/*   best_node [B], hidden_rows [B,T,H] dtype, h_next [B,H] dtype: all or none; */
+/*             h_next[b] = hidden_rows[b, best_node[b]]                        */
+/*   kv_len_out [B] (not kv_len itself); appended [B] out, may be NULL: rows   */
+/*             written                                                         */
+/* The scale of a page and head is the smallest power of two 2^e (-64 <= e <=  */
+/* 64) with |x| <= 448 * 2^e for the finite values written there; rows append  */
+/* under the page's present scale while they fit it, and otherwise raise it:   */
+/* the page's earlier codes are then rounded to the new grid.  Conversion is   */
+/* to nearest even, infinities to +-448, NaN to NaN.  A page whose scale is    */
+/* not readable and that already holds rows stays as it is.                    */
+/* The pages that receive rows must be in the table and belong to one          */
+/* sequence only (6c sees to both).  A sequence whose last, rows, best_node,    */
+/* kv_len or pages are out of range is left unchanged: kv_len_out = kv_len,    */
+/* appended = -2.  Limits: R <= T where rows is NULL.                          */
+int medusa_kv_append_q8(const void* k_rows, const void* v_rows, medusa_dtype dtype, void* k_pages,
+                        void* v_pages, float* k_scale, float* v_scale, const int32_t* page_table,
+                        const int32_t* kv_len, const int32_t* rows, const int32_t* last, int B, int T,
+                        int R, int Hkv, int D, int P, int n_pages, int M, const int32_t* best_node,
+                        const void* hidden_rows, void* h_next, int H, int32_t* kv_len_out,
+                        int32_t* appended, void* stream);
+
+/* 6c. Fork, free and reserve.  Row b of the new table goes on from row src[b] */
+/* of the old one (src[b] = b: itself; -1: the row becomes empty; NULL: every  */
+/* row goes on from itself), with room for need[b] more tokens (NULL: 0).      */
+/*   - Rows that go on from the same source share its full pages.  Its open    */
+/*     page (kv_len not a multiple of P) and pages reserved behind it stay     */
+/*     with the source itself where that goes on, else with the first of the   */
+/*     rows; the others get a copy of the open page's rows in use.             */
+/*   - Pages that no row of the new table holds are free (the tables are the   */
+/*     only record).  held [n_pages] int32 or NULL: pages with held > 0 are    */
+/*     kept as well (a shared prompt between requests, say).                   */
+/*   - Pages are taken lowest first, rows in order, first the copy of the open */
+/*     page, then ceil((len + need)/P) pages in all.                           */
+/*   page_table_out [B,M], kv_len_out [B] (not the buffers read)               */
+/*   refs  [n_pages] out: rows that hold the page, plus held                   */
+/*   taken [B] out: pages newly taken; -1: too few pages free (rows after it   */
+/*         that need any find none either) or M too small: nothing taken, and  */
+/*         a fork without its copy ends at its last full page; -2: src, the    */
+/*         source's kv_len or its pages are out of range: the row is empty     */
+/* A table row holds its pages from entry 0 on; entries behind the first       */
+/* without a page are dropped.                                                 */
+size_t medusa_kv_pages_fork_workspace(int B, int n_pages);
+int medusa_kv_pages_fork(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                         const int32_t* page_table, const int32_t* kv_len, const int32_t* src,
+                         const int32_t* need, const int32_t* held, int B, int Hkv, int D, int P,
+                         int n_pages, int M, int32_t* page_table_out, int32_t* kv_len_out, int32_t* refs,
+                         int32_t* taken, void* ws, size_t ws_bytes, void* stream);
+
+/* 6d. Compact the pool.  Pages in use (in the table, or held > 0) move into   */
+/* [0, live): the k-th page in use at or above `live` to the k-th hole below   */
+/* it, in rising order; the pages from `live` on can then be given back.       */
+/*   page_table_out [B,M] (may be page_table): the table in new numbers        */
+/*   new_page [n_pages] out: new number of each page, -1 where not in use      */
+/*   live [1] out                                                              */
+size_t medusa_kv_pages_compact_workspace(int n_pages);
+int medusa_kv_pages_compact(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                            const int32_t* page_table, const int32_t* held, int B, int Hkv, int D, int P,
+                            int n_pages, int M, int32_t* page_table_out, int32_t* new_page, int32_t* live,
+                            void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,13 +16,20 @@ the C ABI of include/medusa.h); this package is its thin Python binding:
                       on the tensor cores, reduced without writing the logits
   verify_accept_chain speculative-sampling acceptance with k + 1 tokens
   kv_compact          keep the accepted branch's KV rows and hidden state
+  tree_attention_q8   tree attention over the 8-bit paged KV cache
+  kv_append_q8        quantise prompt rows, decoded tokens or the accepted branch
+                      into its pages
+  kv_pages_fork       fork, free and reserve: who holds which page
+  kv_pages_compact    move the pages in use to the front of the pool
   device_status       raises if a bounded device wait gave up (MEDUSA_ERR_TIMEOUT)
   set_wait_limit      test hook: the tensor-core kernels' wait limit
 """
 from ._native import MedusaError, lib  # noqa: F401
 from .api import (build_tree, device_status, heads_topk, heads_topk_static, heads_topk_workspace,  # noqa: F401
-                  kv_compact, set_wait_limit,
-                  sparse_tree_paths, tree_attention, tree_attention_workspace, tree_layout,
+                  kv_append_q8, kv_compact, kv_pages_compact, kv_pages_compact_workspace, kv_pages_fork,
+                  kv_pages_fork_workspace, set_wait_limit,
+                  sparse_tree_paths, tree_attention, tree_attention_q8, tree_attention_q8_workspace,
+                  tree_attention_workspace, tree_layout,
                   verify_accept_chain, verify_accept_tree, verify_accept_workspace,
                   verify_accept_tree_sample, verify_chain_workspace, verify_project_tree,
                   verify_project_workspace, verify_sample_workspace)

@@ -26,6 +26,9 @@ EXPORTS = (
     "medusa_verify_sample_workspace", "medusa_verify_accept_tree_sample",
     "medusa_verify_chain_workspace", "medusa_verify_accept_chain",
     "medusa_kv_compact",
+    "medusa_tree_attention_q8_workspace", "medusa_tree_attention_q8", "medusa_kv_append_q8",
+    "medusa_kv_pages_fork_workspace", "medusa_kv_pages_fork",
+    "medusa_kv_pages_compact_workspace", "medusa_kv_pages_compact",
 )
 
 
@@ -78,6 +81,18 @@ def lib() -> C.CDLL:
     L.medusa_verify_accept_chain.argtypes = [P, P, P, i32, i32, i32, u64, u64, P, P, P, sz, P]
     L.medusa_kv_compact.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32,
                                     P, P]
+    L.medusa_tree_attention_q8_workspace.argtypes = [i32] * 6
+    L.medusa_tree_attention_q8_workspace.restype = sz
+    L.medusa_tree_attention_q8.argtypes = [P, P, P, i32, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
+                                           i32, i32, f32, P, P, sz, P]
+    L.medusa_kv_append_q8.argtypes = [P, P, i32, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
+                                      i32, P, P, P, i32, P, P, P]
+    L.medusa_kv_pages_fork_workspace.argtypes = [i32] * 2
+    L.medusa_kv_pages_fork_workspace.restype = sz
+    L.medusa_kv_pages_fork.argtypes = [P] * 9 + [i32] * 6 + [P] * 5 + [sz, P]
+    L.medusa_kv_pages_compact_workspace.argtypes = [i32]
+    L.medusa_kv_pages_compact_workspace.restype = sz
+    L.medusa_kv_pages_compact.argtypes = [P] * 6 + [i32] * 6 + [P] * 4 + [sz, P]
     _lib = L
     return L
 

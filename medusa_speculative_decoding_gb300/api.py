@@ -321,3 +321,180 @@ def kv_compact(k_cache, v_cache, kv_len, path_nodes, accept_len, best_node, N, m
                                   _ptr(h_next), _dtype_of(k_cache), B, Hkv, D, Lmax, N, H,
                                   max_depth, _ptr(src_idx), _stream(stream)))
     return h_next, src_idx
+
+
+# ----------------------------------------------------------------------------
+# The 8-bit paged KV cache.  Pools: k_pages, v_pages [n_pages, Hkv, P, D]
+# (torch.uint8 or torch.float8_e4m3fn) and k_scale, v_scale [n_pages, Hkv]
+# float32; page_table [B, M] and kv_len [B] int32.
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len=None):
+    dev = k_pages.device
+    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _need(t, n)
+        if t.dtype not in _CODES or t.dim() != 4:
+            raise ValueError(f"{n} must be [n_pages, Hkv, P, D] e4m3 codes (uint8 or float8_e4m3fn)")
+    _need(k_scale, "k_scale", torch.float32)
+    _need(v_scale, "v_scale", torch.float32)
+    _need(page_table, "page_table", torch.int32)
+    if v_pages.shape != k_pages.shape or k_scale.shape != k_pages.shape[:2] or v_scale.shape != k_pages.shape[:2]:
+        raise ValueError("the pools' shapes do not agree")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, M]")
+    n_pages, Hkv, P, D = k_pages.shape
+    B, M = page_table.shape
+    if kv_len is not None:
+        _need_shape(kv_len, "kv_len", (B,), torch.int32, dev)
+    for n, t in (("v_pages", v_pages), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table)):
+        _same_device(t, n, dev)
+    return B, M, n_pages, Hkv, P, D
+
+
+def _same_device(t, name, dev):
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _need_shape(t, name, shape, dtype, dev):
+    _need(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _same_device(t, name, dev)
+    return t
+
+
+def tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype=torch.bfloat16):
+    return int(lib().medusa_tree_attention_q8_workspace(B, N, Hq, Hkv, D, _DT[dtype]))
+
+
+def tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, mask, scale,
+                      out=None, ws=None, stream=None):
+    """Tree attention over the 8-bit paged cache: q [B,N,Hq,D] against the pages'
+    prefix and the tree rows k_tree, v_tree [B,N,Hkv,D] under mask [N, ceil(N/64)].
+    Returns out [B,N,Hq,D] in q's type.  N = 1 with mask [[1]] is plain decoding."""
+    _need(q, "q")
+    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    dev = k_pages.device
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
+        raise ValueError(f"q must be [{B}, N, Hq, {D}], got {tuple(q.shape)}")
+    _same_device(q, "q", dev)
+    N, Hq = q.shape[1], q.shape[2]
+    _need_shape(k_tree, "k_tree", (B, N, Hkv, D), q.dtype, dev)
+    _need_shape(v_tree, "v_tree", (B, N, Hkv, D), q.dtype, dev)
+    _need_shape(mask, "mask", (N, (N + 63) // 64), torch.int64, dev)
+    with torch.cuda.device(dev):
+        o = torch.empty_like(q) if out is None else _need_shape(out, "out", q.shape, q.dtype, dev)
+        if ws is None:
+            ws = _ws(tree_attention_q8_workspace(B, N, Hq, Hkv, D, q.dtype), dev)
+        check(lib().medusa_tree_attention_q8(_ptr(q), _ptr(k_tree), _ptr(v_tree), _dtype_of(q), _ptr(k_pages),
+                                             _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                                             _ptr(kv_len), _ptr(mask), B, N, Hq, Hkv, D, P, n_pages, M,
+                                             float(scale), _ptr(o), _ptr(ws), ws.numel(), _stream(stream)))
+    return o
+
+
+def kv_append_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, rows=None, last=None,
+                 best_node=None, hidden_rows=None, out=None, stream=None):
+    """Quantises rows 0..last[b] of `rows` (tree nodes; None: rows in order) of
+    k_rows, v_rows [B,T,Hkv,D] into the pages behind kv_len.  `last` None takes
+    all.  Returns dict(kv_len, appended, h_next); the pools change in place."""
+    _need(k_rows, "k_rows")
+    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    dev = k_pages.device
+    if k_rows.dim() != 4 or k_rows.shape[0] != B or tuple(k_rows.shape[2:]) != (Hkv, D):
+        raise ValueError(f"k_rows must be [{B}, T, {Hkv}, {D}], got {tuple(k_rows.shape)}")
+    _same_device(k_rows, "k_rows", dev)
+    T = k_rows.shape[1]
+    _need_shape(v_rows, "v_rows", k_rows.shape, k_rows.dtype, dev)
+    R = T
+    if rows is not None:
+        if rows.dim() != 2:
+            raise ValueError("rows must be [B, R]")
+        R = rows.shape[1]
+        _need_shape(rows, "rows", (B, R), torch.int32, dev)
+    if last is not None:
+        _need_shape(last, "last", (B,), torch.int32, dev)
+    H = 0
+    if (hidden_rows is None) != (best_node is None):
+        raise ValueError("best_node and hidden_rows go together")
+    if hidden_rows is not None:
+        H = hidden_rows.shape[-1]
+        _need_shape(hidden_rows, "hidden_rows", (B, T, H), k_rows.dtype, dev)
+        _need_shape(best_node, "best_node", (B,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = dict(kv_len=torch.empty_like(kv_len), appended=torch.empty_like(kv_len),
+                       h_next=torch.empty((B, H), dtype=k_rows.dtype, device=dev) if H else None)
+        else:
+            _need_shape(out["kv_len"], "out kv_len", (B,), torch.int32, dev)
+            if out.get("appended") is not None:
+                _need_shape(out["appended"], "out appended", (B,), torch.int32, dev)
+            if H:
+                _need_shape(out["h_next"], "out h_next", (B, H), k_rows.dtype, dev)
+        check(lib().medusa_kv_append_q8(_ptr(k_rows), _ptr(v_rows), _dtype_of(k_rows), _ptr(k_pages),
+                                        _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                                        _ptr(kv_len), _ptr(rows), _ptr(last), B, T, R, Hkv, D, P, n_pages, M,
+                                        _ptr(best_node), _ptr(hidden_rows), _ptr(out["h_next"]) if H else None,
+                                        H, _ptr(out["kv_len"]), _ptr(out.get("appended")), _stream(stream)))
+    return out
+
+
+def kv_pages_fork_workspace(B, n_pages):
+    return int(lib().medusa_kv_pages_fork_workspace(B, n_pages))
+
+
+def kv_pages_fork(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, src=None, need=None, held=None,
+                  out=None, ws=None, stream=None):
+    """Forks, frees and reserves: row b goes on from row src[b] (-1: freed; None:
+    every row from itself) with room for need[b] more tokens.  Returns
+    dict(page_table, kv_len, refs, taken); open pages are copied in the pools."""
+    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    dev = k_pages.device
+    for n, t, shape in (("src", src, (B,)), ("need", need, (B,)), ("held", held, (n_pages,))):
+        if t is not None:
+            _need_shape(t, n, shape, torch.int32, dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = dict(page_table=torch.empty_like(page_table), kv_len=torch.empty_like(kv_len),
+                       refs=torch.empty(n_pages, dtype=torch.int32, device=dev), taken=torch.empty_like(kv_len))
+        else:
+            for n, shape in (("page_table", (B, M)), ("kv_len", (B,)), ("refs", (n_pages,)), ("taken", (B,))):
+                _need_shape(out[n], f"out {n}", shape, torch.int32, dev)
+        if ws is None:
+            ws = _ws(kv_pages_fork_workspace(B, n_pages), dev)
+        check(lib().medusa_kv_pages_fork(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                         _ptr(page_table), _ptr(kv_len), _ptr(src), _ptr(need), _ptr(held), B,
+                                         Hkv, D, P, n_pages, M, _ptr(out["page_table"]), _ptr(out["kv_len"]),
+                                         _ptr(out["refs"]), _ptr(out["taken"]), _ptr(ws), ws.numel(),
+                                         _stream(stream)))
+    return out
+
+
+def kv_pages_compact_workspace(n_pages):
+    return int(lib().medusa_kv_pages_compact_workspace(n_pages))
+
+
+def kv_pages_compact(k_pages, v_pages, k_scale, v_scale, page_table, held=None, out=None, ws=None, stream=None):
+    """Moves the pages in use into [0, live).  Returns dict(page_table, new_page,
+    live); the pools change in place."""
+    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table)
+    dev = k_pages.device
+    if held is not None:
+        _need_shape(held, "held", (n_pages,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = dict(page_table=torch.empty_like(page_table),
+                       new_page=torch.empty(n_pages, dtype=torch.int32, device=dev),
+                       live=torch.empty(1, dtype=torch.int32, device=dev))
+        else:
+            for n, shape in (("page_table", (B, M)), ("new_page", (n_pages,)), ("live", (1,))):
+                _need_shape(out[n], f"out {n}", shape, torch.int32, dev)
+        if ws is None:
+            ws = _ws(kv_pages_compact_workspace(n_pages), dev)
+        check(lib().medusa_kv_pages_compact(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                            _ptr(page_table), _ptr(held), B, Hkv, D, P, n_pages, M,
+                                            _ptr(out["page_table"]), _ptr(out["new_page"]), _ptr(out["live"]),
+                                            _ptr(ws), ws.numel(), _stream(stream)))
+    return out

@@ -1,0 +1,239 @@
+// append_q8.cu -- new K and V rows into the 8-bit paged cache.
+//
+// Rows go to the slots behind kv_len: a prompt's rows in order, a decoded token's,
+// or the rows of a tree's accepted branch picked by index ("Medusa Heads"
+// glossary page, "Tree attention and acceptance": the longest accepted branch is
+// kept) -- the tree's other rows never reach the cache, so nothing is moved or
+// undone later.
+//
+// A page's scale for one head is the smallest power of two 2^e with max|x| <=
+// 448 * 2^e over the rows it holds.  e4m3 is a floating type: a power-of-two
+// scale costs no precision, and when a later row needs a larger one the earlier
+// codes move to the new grid exactly, except those that fall into e4m3's
+// subnormal range, which round to its step.
+//
+// append_q8_kernel: one CTA per (page that receives rows, K or V, head,
+// sequence).  The rows of the page are read once, 16 bytes a load, and held in
+// registers through the maximum and the conversion; the codes leave as one
+// contiguous span.
+#include "common.cuh"
+#include "q8.cuh"
+
+namespace medusa {
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+struct AppendArgs {
+    const void* rows[2];  // K, V rows [B][T][Hkv][D]
+    uint8_t* pages[2];
+    float* scale[2];
+    const int32_t* page_table;
+    const int32_t* kv_len;
+    const int32_t* index;  // [B][R] or NULL
+    const int32_t* last;   // [B] or NULL
+    const int32_t* best_node;
+    const uint4* hidden;
+    uint4* h_next;
+    int32_t* kv_len_out;
+    int32_t* appended;
+    int B, T, R, Hkv, P, M, n_pages, h16;
+};
+
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+    const uint4 w = ld_stream16(p);
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_lo(v[i]); x[2 * i + 1] = bf16_hi(v[i]); }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const uint4 a = ld_stream16(p), b = ld_stream16(p + 4);
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
+}
+
+// the smallest 2^e with top <= 448 * 2^e, e held to [-64, 64]
+__device__ __forceinline__ float page_scale(float top) {
+    if (!(top > 0.f)) return q8::kMinScale;
+    const uint32_t u = __float_as_uint(top);
+    // 448 = 1.75 * 2^8
+    int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    if ((u >> 23) == 0) e = -64;  // subnormal
+    e = q8::clamp_int(e, -64, 64);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+template <typename T, int D, int CHUNKS>
+__global__ void __launch_bounds__(kAppendThreads) append_q8_kernel(const AppendArgs a) {
+    constexpr int C8 = D / 8;  // 8-element chunks per row
+    __shared__ float s_top[kAppendThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.z, tid = threadIdx.x;
+    const int L = a.kv_len[b], last = a.last ? a.last[b] : a.R - 1;
+    const int n = last + 1, P = a.P;
+    // The whole sequence is checked by every CTA, so that either all of its rows
+    // are written or none is.
+    bool ok = last >= -1 && last < a.R && L >= 0 && L <= a.M * P && n <= a.M * P - L;
+    const int w0 = ok ? L / P : 0;  // first page that receives a row
+    const int windows = ok && n > 0 ? (L + n - 1) / P - w0 + 1 : 0;
+    const int32_t* table = a.page_table + (size_t)b * a.M;
+    bool mine = true;
+    for (int i = tid; i < windows; i += kAppendThreads) {
+        const int p = table[w0 + i];
+        mine = mine && p >= 0 && p < a.n_pages;
+    }
+    if (a.index && ok)
+        for (int i = tid; i < n; i += kAppendThreads) {
+            const int r = a.index[(size_t)b * a.R + i];
+            mine = mine && r >= 0 && r < a.T;
+        }
+    if (a.best_node && tid == 0) mine = mine && a.best_node[b] >= 0 && a.best_node[b] < a.T;
+    ok = __syncthreads_and(ok && mine);
+
+    if (blockIdx.x == 2 * a.Hkv) {  // the sequence's bookkeeping
+        if (blockIdx.y) return;
+        if (tid == 0) {
+            a.kv_len_out[b] = ok ? L + n : L;
+            if (a.appended) a.appended[b] = ok ? n : -2;
+        }
+        if (ok && a.hidden) {
+            const uint4* src = a.hidden + ((size_t)b * a.T + a.best_node[b]) * a.h16;
+            for (int i = tid; i < a.h16; i += kAppendThreads) a.h_next[(size_t)b * a.h16 + i] = src[i];
+        }
+        return;
+    }
+    if (!ok || (int)blockIdx.y >= windows) return;
+
+    const int h = blockIdx.x >> 1, kv = blockIdx.x & 1;
+    const T* rows = static_cast<const T*>(a.rows[kv]) + ((size_t)b * a.T * a.Hkv + h) * D;
+    const size_t row_stride = (size_t)a.Hkv * D;
+    const int page = table[w0 + blockIdx.y];
+    const size_t unit = (size_t)page * a.Hkv + h;
+    uint8_t* codes = a.pages[kv] + unit * P * D;
+    const int first = (w0 + (int)blockIdx.y) * P - L;  // new row that the page's slot 0 takes
+    const int chunks = P * C8;
+
+    float x[CHUNKS][8];
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+        const int c = tid + k * kAppendThreads;
+        const int i = first + c / C8;
+        if (c < chunks && i >= 0 && i < n) {
+            const int r = a.index ? a.index[(size_t)b * a.R + i] : i;
+            load8(rows + (size_t)r * row_stride + (c % C8) * 8, x[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float m = fabsf(x[k][e]);
+                if (m < INFINITY) top = fmaxf(top, m);  // the scale is set by finite values
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((tid & 31) == 0) s_top[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAppendThreads / 32; ++i) top = fmaxf(top, s_top[i]);
+
+    const bool had = first < 0;  // the page holds earlier rows
+    const float s0 = had ? a.scale[kv][unit] : 0.f;
+    const bool readable = !had || q8::scale_ok(s0);  // an unreadable page stays one
+    const bool keep = had && (!readable || top <= q8::kE4m3Max * s0);
+    const float s1 = keep ? s0 : page_scale(top);
+    __syncthreads();  // every thread has read the scale
+    if (tid == 0 && !keep) a.scale[kv][unit] = s1;
+    if (!readable) return;
+    // 1 / s1 is exact for the powers of two written here; a caller's own scale is divided by
+    const bool pow2 = (__float_as_uint(s1) & 0x7fffffu) == 0;
+    const float inv = 1.f / s1;
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+        const int c = tid + k * kAppendThreads;
+        const int i = first + c / C8;
+        if (c >= chunks || i >= n) continue;
+        uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)c * 8);
+        if (i < 0) {
+            if (keep) continue;
+            const uint2 w = *dst;
+            const uint16_t old[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = q8::e4m3x2_to_float2(old[e]);
+                x[k][2 * e] = f.x * s0;
+                x[k][2 * e + 1] = f.y * s0;
+            }
+        }
+        uint16_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            q[e] = pow2 ? q8::float2_to_e4m3x2(x[k][2 * e] * inv, x[k][2 * e + 1] * inv)
+                        : q8::float2_to_e4m3x2(x[k][2 * e] / s1, x[k][2 * e + 1] / s1);
+        *dst = make_uint2((uint32_t)q[0] | (uint32_t)q[1] << 16, (uint32_t)q[2] | (uint32_t)q[3] << 16);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_append(const AppendArgs& a, int windows, cudaStream_t st) {
+    const dim3 grid(2 * a.Hkv + 1, windows, a.B), block(kAppendThreads);
+    switch ((a.P * D / 8 + kAppendThreads - 1) / kAppendThreads) {
+        case 1: return launch(append_q8_kernel<T, D, 1>, grid, block, 0, st, a);
+        case 2: return launch(append_q8_kernel<T, D, 2>, grid, block, 0, st, a);
+        case 4: return launch(append_q8_kernel<T, D, 4>, grid, block, 0, st, a);
+        default: return launch(append_q8_kernel<T, D, 8>, grid, block, 0, st, a);
+    }
+}
+
+}  // namespace
+}  // namespace medusa
+
+using namespace medusa;
+
+extern "C" int medusa_kv_append_q8(const void* k_rows, const void* v_rows, medusa_dtype dtype, void* k_pages,
+                                   void* v_pages, float* k_scale, float* v_scale, const int32_t* page_table,
+                                   const int32_t* kv_len, const int32_t* rows, const int32_t* last, int B, int T,
+                                   int R, int Hkv, int D, int P, int n_pages, int M, const int32_t* best_node,
+                                   const void* hidden_rows, void* h_next, int H, int32_t* kv_len_out,
+                                   int32_t* appended, void* stream) {
+    if (B < 1 || T < 1 || R < 1 || Hkv < 1 || n_pages < 1 || M < 1)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: sizes must be positive");
+    if (int rc = q8::check_pool("kv_append_q8", B, Hkv, D, P, n_pages, M)) return rc;
+    if (dtype != MEDUSA_F32 && dtype != MEDUSA_BF16)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_q8: unknown dtype %d", (int)dtype);
+    if (!k_rows || !v_rows || !k_pages || !v_pages || !k_scale || !v_scale || !page_table || !kv_len || !kv_len_out)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: null pointer");
+    if (!rows && R > T) return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: R %d above T %d without row indices", R, T);
+    const bool hid = hidden_rows != nullptr;
+    if (hid != (h_next != nullptr) || hid != (best_node != nullptr))
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: best_node, hidden_rows and h_next go together");
+    const int elem = dtype == MEDUSA_F32 ? 4 : 2;
+    if (hid && (H < 1 || ((long long)H * elem) % 16))
+        return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_q8: hidden rows must be multiples of 16 bytes");
+    if (!aligned16(k_rows) || !aligned16(v_rows) || !aligned16(k_pages) || !aligned16(v_pages) ||
+        (hid && (!aligned16(hidden_rows) || !aligned16(h_next))))
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: rows, pages and hidden states must be 16-byte aligned");
+    if (kv_len_out == kv_len)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: kv_len_out must not be kv_len");
+    const int windows = (R + P - 2) / P + 1;  // pages that R rows can touch
+    if (windows > 65535) return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_q8: %d rows span too many pages", R);
+    AppendArgs a{};
+    a.rows[0] = k_rows; a.rows[1] = v_rows;
+    a.pages[0] = (uint8_t*)k_pages; a.pages[1] = (uint8_t*)v_pages;
+    a.scale[0] = k_scale; a.scale[1] = v_scale;
+    a.page_table = page_table; a.kv_len = kv_len; a.index = rows; a.last = last;
+    a.best_node = best_node;
+    a.hidden = (const uint4*)hidden_rows; a.h_next = (uint4*)h_next;
+    a.kv_len_out = kv_len_out; a.appended = appended;
+    a.B = B; a.T = T; a.R = R; a.Hkv = Hkv; a.P = P; a.M = M; a.n_pages = n_pages;
+    a.h16 = hid ? (int)((long long)H * elem / 16) : 0;
+    cudaStream_t st = as_stream(stream);
+    cudaError_t e;
+    if (dtype == MEDUSA_F32)
+        e = D == 64 ? launch_append<float, 64>(a, windows, st) : launch_append<float, 128>(a, windows, st);
+    else
+        e = D == 64 ? launch_append<uint16_t, 64>(a, windows, st) : launch_append<uint16_t, 128>(a, windows, st);
+    if (e != cudaSuccess) return fail(MEDUSA_ERR_CUDA, "kv_append_q8: launch failed: %s", cudaGetErrorString(e));
+    return MEDUSA_OK;
+}

@@ -1,0 +1,137 @@
+// q8.cuh -- the 8-bit paged KV cache: what a page holds, which scales are
+// readable, e4m3 conversions, and the even split of attention work over CTAs.
+//
+// A pool of n_pages pages serves every sequence: codes [n_pages][Hkv][P][D] in
+// e4m3 for K and for V, one float scale per (page, KV head), value = code *
+// scale.  One (page, head) is P * D contiguous bytes: the unit that a TMA box,
+// an append and a page copy move.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace medusa {
+namespace q8 {
+
+constexpr float kE4m3Max = 448.f;
+constexpr int kMaxBatch = 1024;  // sequences a call takes (row tables fit shared memory)
+// readable scales: far from the ends of float32, so that sums of codes times
+// scales (and their inverses) over a million keys stay finite
+constexpr float kMinScale = 5.421010862427522e-20f;  // 2^-64
+constexpr float kMaxScale = 18446744073709551616.f;  // 2^64
+
+// Limits every entry point of the paged cache shares.
+inline int check_pool(const char* who, int B, int Hkv, int D, int P, int n_pages, int M) {
+    if ((D != 64 && D != 128) || (P != 16 && P != 32 && P != 64 && P != 128))
+        return fail(MEDUSA_ERR_UNSUPPORTED, "%s: head dim %d must be 64 or 128, page %d tokens 16, 32, 64 or 128", who, D, P);
+    if (B > kMaxBatch) return fail(MEDUSA_ERR_UNSUPPORTED, "%s: batch %d above %d", who, B, kMaxBatch);
+    if (Hkv > 1024) return fail(MEDUSA_ERR_UNSUPPORTED, "%s: %d KV heads above 1024", who, Hkv);
+    if ((long long)n_pages * Hkv * P > 0x7fffffffll)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "%s: a pool of %d pages x %d heads x %d rows exceeds 2^31 rows", who, n_pages,
+                    Hkv, P);
+    if ((long long)M * P > (1ll << 30) || (long long)B * M > (1ll << 30))
+        return fail(MEDUSA_ERR_UNSUPPORTED, "%s: a table of %d x %d pages is too large", who, B, M);
+    return MEDUSA_OK;
+}
+
+__host__ __device__ __forceinline__ bool scale_ok(float s) { return s >= kMinScale && s <= kMaxScale; }
+
+// two e4m3 codes (low, high byte) -> two floats, exactly
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    float2 f;
+    asm("{\n.reg .f16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}"
+        : "=f"(f.x), "=f"(f.y) : "r"(h));
+    return f;
+}
+// two floats -> two e4m3 codes (lo in the low byte): nearest even, held at 448,
+// NaN stays NaN
+__device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+    return c;
+}
+
+__device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+// ---------------------------------------------------------------------------
+// Attention work.  A unit is (sequence, KV head, block of query rows); its keys
+// are cut into tiles of T: first the prefix's, then the tree's.  The tiles of all
+// units, laid end to end, are shared out evenly over the CTAs (the lengths are
+// known on the device only, so the host cannot choose a split).  A CTA's share
+// is a run of segments, each a range of one unit's tiles; a unit that several
+// CTAs share leaves one partial result per CTA, joined by a merge kernel.
+struct Work {
+    int B, N, U, T, cap, ctas;  // U units per sequence, T keys per tile, cap slots per sequence
+    __device__ __forceinline__ int len(const int32_t* kv_len, int b) const { return clamp_int(kv_len[b], 0, cap); }
+    __device__ __forceinline__ int prefix_tiles(int L) const { return (L + T - 1) / T; }
+    __device__ __forceinline__ int tree_tiles() const { return (N + T - 1) / T; }
+    __device__ __forceinline__ int tiles(int L) const { return prefix_tiles(L) + tree_tiles(); }
+    __device__ __forceinline__ long long cta_begin(long long total, int c) const { return total * c / ctas; }
+    // the CTA whose share holds tile g: the largest c with total * c / ctas <= g
+    __device__ __forceinline__ int cta_of(long long total, long long g) const {
+        return (int)(((g + 1) * ctas - 1) / total);
+    }
+};
+
+// Fills first[b] (b <= B) with the number of tiles of sequences before b; called
+// by every thread of the block.
+__device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __restrict__ kv_len, long long* first) {
+    for (int b = threadIdx.x; b < w.B; b += blockDim.x)
+        first[b + 1] = (long long)w.U * w.tiles(w.len(kv_len, b));
+    if (threadIdx.x == 0) first[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {  // inclusive scan by one warp, 32 sequences at a time
+        long long carry = 0;
+        for (int b0 = 0; b0 < w.B; b0 += 32) {
+            const int b = b0 + (int)threadIdx.x;
+            long long v = b < w.B ? first[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if ((int)threadIdx.x >= o) v += u;
+            }
+            v += carry;
+            if (b < w.B) first[b + 1] = v;
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// The sequence whose tiles hold g (first[b] <= g < first[b + 1]).
+__device__ __forceinline__ int find_sequence(const long long* first, int B, long long g) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= g) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// A CTA's next segment: tiles [t0, t1) of unit `unit` of sequence b.
+struct Segment {
+    int b, unit, t0, t1, tiles, L;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+    // a CTA has at most one segment that begins inside a unit (its first) and one
+    // that begins a unit without ending it (its last): its two partial slots
+    __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 > 0 ? 0 : 1); }
+};
+__device__ __forceinline__ Segment segment_at(const Work& w, const long long* first, const int32_t* kv_len,
+                                              long long g, long long g_end) {
+    Segment s;
+    s.b = find_sequence(first, w.B, g);
+    s.L = w.len(kv_len, s.b);
+    s.tiles = w.tiles(s.L);
+    const long long x = g - first[s.b];
+    s.unit = (int)(x / s.tiles);
+    s.t0 = (int)(x - (long long)s.unit * s.tiles);
+    const long long left = g_end - g;
+    s.t1 = left < s.tiles - s.t0 ? s.t0 + (int)left : s.tiles;
+    return s;
+}
+
+}  // namespace q8
+}  // namespace medusa
