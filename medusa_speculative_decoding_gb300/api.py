@@ -8,6 +8,7 @@ library's kernels.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import numpy as np
 import torch
@@ -18,12 +19,12 @@ _DT = {torch.float32: MEDUSA_F32, torch.bfloat16: MEDUSA_BF16}
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _need(t, name, dtype=None, cuda=True):
@@ -326,43 +327,51 @@ def kv_compact(k_cache, v_cache, kv_len, path_nodes, accept_len, best_node, N, m
 # ----------------------------------------------------------------------------
 # The 8-bit paged KV cache.  Pools: k_pages, v_pages [n_pages, Hkv, P, D]
 # (torch.uint8 or torch.float8_e4m3fn) and k_scale, v_scale [n_pages, Hkv]
-# float32; page_table [B, M] and kv_len [B] int32.
+# float32; page_table [B, M] and kv_len [B] int32.  These calls take microseconds
+# on the device, so their checks are kept to one pass over each tensor.
+_I32, _F32 = torch.int32, torch.float32
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len=None):
-    dev = k_pages.device
-    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _need(t, n)
-        if t.dtype not in _CODES or t.dim() != 4:
-            raise ValueError(f"{n} must be [n_pages, Hkv, P, D] e4m3 codes (uint8 or float8_e4m3fn)")
-    _need(k_scale, "k_scale", torch.float32)
-    _need(v_scale, "v_scale", torch.float32)
-    _need(page_table, "page_table", torch.int32)
-    if v_pages.shape != k_pages.shape or k_scale.shape != k_pages.shape[:2] or v_scale.shape != k_pages.shape[:2]:
-        raise ValueError("the pools' shapes do not agree")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, M]")
-    n_pages, Hkv, P, D = k_pages.shape
-    B, M = page_table.shape
-    if kv_len is not None:
-        _need_shape(kv_len, "kv_len", (B,), torch.int32, dev)
-    for n, t in (("v_pages", v_pages), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table)):
-        _same_device(t, n, dev)
-    return B, M, n_pages, Hkv, P, D
-
-
-def _same_device(t, name, dev):
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-
-
 def _need_shape(t, name, shape, dtype, dev):
+    """t, a contiguous tensor of that shape and type on CUDA device number dev."""
+    if t is not None and t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
     _need(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _same_device(t, name, dev)
-    return t
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len=None):
+    _need(k_pages, "k_pages")
+    if k_pages.dtype not in _CODES or k_pages.dim() != 4:
+        raise ValueError("k_pages must be [n_pages, Hkv, P, D] e4m3 codes (uint8 or float8_e4m3fn)")
+    shape, dev = k_pages.shape, k_pages.get_device()
+    _need_shape(v_pages, "v_pages", shape, k_pages.dtype, dev)
+    _need_shape(k_scale, "k_scale", shape[:2], _F32, dev)
+    _need_shape(v_scale, "v_scale", shape[:2], _F32, dev)
+    if page_table is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, M]")
+    _need_shape(page_table, "page_table", page_table.shape, _I32, dev)
+    if kv_len is not None:
+        _need_shape(kv_len, "kv_len", page_table.shape[:1], _I32, dev)
+    return (*page_table.shape, *shape, dev)
+
+
+def _elsewhere(dev):
+    """Whether CUDA device number dev is not the current one (the library works on
+    the current device)."""
+    return dev != torch.cuda.current_device()
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_q8_bytes(dev, B, N, Hq, Hkv, D, dtype):
+    return int(lib().medusa_tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype))
 
 
 def tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype=torch.bfloat16):
@@ -374,24 +383,27 @@ def tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, pag
     """Tree attention over the 8-bit paged cache: q [B,N,Hq,D] against the pages'
     prefix and the tree rows k_tree, v_tree [B,N,Hkv,D] under mask [N, ceil(N/64)].
     Returns out [B,N,Hq,D] in q's type.  N = 1 with mask [[1]] is plain decoding."""
-    _need(q, "q")
-    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
-    dev = k_pages.device
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
-        raise ValueError(f"q must be [{B}, N, Hq, {D}], got {tuple(q.shape)}")
-    _same_device(q, "q", dev)
-    N, Hq = q.shape[1], q.shape[2]
-    _need_shape(k_tree, "k_tree", (B, N, Hkv, D), q.dtype, dev)
-    _need_shape(v_tree, "v_tree", (B, N, Hkv, D), q.dtype, dev)
+    B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, mask,
+                                     scale, out, ws, stream)
+    if q is None or q.dim() != 4:
+        raise ValueError(f"q must be [{B}, N, Hq, {D}]")
+    N, Hq, dtype = q.shape[1], q.shape[2], q.dtype
+    code = _dtype_of(q)
+    _need_shape(q, "q", (B, N, Hq, D), dtype, dev)
+    _need_shape(k_tree, "k_tree", (B, N, Hkv, D), dtype, dev)
+    _need_shape(v_tree, "v_tree", (B, N, Hkv, D), dtype, dev)
     _need_shape(mask, "mask", (N, (N + 63) // 64), torch.int64, dev)
-    with torch.cuda.device(dev):
-        o = torch.empty_like(q) if out is None else _need_shape(out, "out", q.shape, q.dtype, dev)
-        if ws is None:
-            ws = _ws(tree_attention_q8_workspace(B, N, Hq, Hkv, D, q.dtype), dev)
-        check(lib().medusa_tree_attention_q8(_ptr(q), _ptr(k_tree), _ptr(v_tree), _dtype_of(q), _ptr(k_pages),
-                                             _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
-                                             _ptr(kv_len), _ptr(mask), B, N, Hq, Hkv, D, P, n_pages, M,
-                                             float(scale), _ptr(o), _ptr(ws), ws.numel(), _stream(stream)))
+    o = torch.empty_like(q) if out is None else _need_shape(out, "out", q.shape, dtype, dev)
+    if ws is None:
+        ws = _ws(_attention_q8_bytes(dev, B, N, Hq, Hkv, D, code), q.device)
+    check(lib().medusa_tree_attention_q8(q.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), code, k_pages.data_ptr(),
+                                         v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                         page_table.data_ptr(), kv_len.data_ptr(), mask.data_ptr(), B, N, Hq, Hkv, D, P,
+                                         n_pages, M, scale, o.data_ptr(), ws.data_ptr(), ws.numel(),
+                                         _raw_stream(stream, dev)))
     return o
 
 
@@ -400,44 +412,47 @@ def kv_append_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table,
     """Quantises rows 0..last[b] of `rows` (tree nodes; None: rows in order) of
     k_rows, v_rows [B,T,Hkv,D] into the pages behind kv_len.  `last` None takes
     all.  Returns dict(kv_len, appended, h_next); the pools change in place."""
-    _need(k_rows, "k_rows")
-    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
-    dev = k_pages.device
-    if k_rows.dim() != 4 or k_rows.shape[0] != B or tuple(k_rows.shape[2:]) != (Hkv, D):
-        raise ValueError(f"k_rows must be [{B}, T, {Hkv}, {D}], got {tuple(k_rows.shape)}")
-    _same_device(k_rows, "k_rows", dev)
-    T = k_rows.shape[1]
-    _need_shape(v_rows, "v_rows", k_rows.shape, k_rows.dtype, dev)
+    B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv_append_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, rows, last,
+                                best_node, hidden_rows, out, stream)
+    if k_rows is None or k_rows.dim() != 4:
+        raise ValueError(f"k_rows must be [{B}, T, {Hkv}, {D}]")
+    T, dtype = k_rows.shape[1], k_rows.dtype
+    code = _dtype_of(k_rows)
+    _need_shape(k_rows, "k_rows", (B, T, Hkv, D), dtype, dev)
+    _need_shape(v_rows, "v_rows", (B, T, Hkv, D), dtype, dev)
     R = T
     if rows is not None:
         if rows.dim() != 2:
             raise ValueError("rows must be [B, R]")
         R = rows.shape[1]
-        _need_shape(rows, "rows", (B, R), torch.int32, dev)
+        _need_shape(rows, "rows", (B, R), _I32, dev)
     if last is not None:
-        _need_shape(last, "last", (B,), torch.int32, dev)
-    H = 0
+        _need_shape(last, "last", (B,), _I32, dev)
     if (hidden_rows is None) != (best_node is None):
         raise ValueError("best_node and hidden_rows go together")
+    H = 0
     if hidden_rows is not None:
         H = hidden_rows.shape[-1]
-        _need_shape(hidden_rows, "hidden_rows", (B, T, H), k_rows.dtype, dev)
-        _need_shape(best_node, "best_node", (B,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = dict(kv_len=torch.empty_like(kv_len), appended=torch.empty_like(kv_len),
-                       h_next=torch.empty((B, H), dtype=k_rows.dtype, device=dev) if H else None)
-        else:
-            _need_shape(out["kv_len"], "out kv_len", (B,), torch.int32, dev)
-            if out.get("appended") is not None:
-                _need_shape(out["appended"], "out appended", (B,), torch.int32, dev)
-            if H:
-                _need_shape(out["h_next"], "out h_next", (B, H), k_rows.dtype, dev)
-        check(lib().medusa_kv_append_q8(_ptr(k_rows), _ptr(v_rows), _dtype_of(k_rows), _ptr(k_pages),
-                                        _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
-                                        _ptr(kv_len), _ptr(rows), _ptr(last), B, T, R, Hkv, D, P, n_pages, M,
-                                        _ptr(best_node), _ptr(hidden_rows), _ptr(out["h_next"]) if H else None,
-                                        H, _ptr(out["kv_len"]), _ptr(out.get("appended")), _stream(stream)))
+        _need_shape(hidden_rows, "hidden_rows", (B, T, H), dtype, dev)
+        _need_shape(best_node, "best_node", (B,), _I32, dev)
+    if out is None:
+        both = torch.empty((2, B), dtype=_I32, device=kv_len.device)
+        out = dict(kv_len=both[0], appended=both[1],
+                   h_next=torch.empty((B, H), dtype=dtype, device=kv_len.device) if H else None)
+    else:
+        _need_shape(out["kv_len"], "out kv_len", (B,), _I32, dev)
+        if out.get("appended") is not None:
+            _need_shape(out["appended"], "out appended", (B,), _I32, dev)
+        if H:
+            _need_shape(out["h_next"], "out h_next", (B, H), dtype, dev)
+    check(lib().medusa_kv_append_q8(k_rows.data_ptr(), v_rows.data_ptr(), code, k_pages.data_ptr(), v_pages.data_ptr(),
+                                    k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
+                                    _ptr(rows), _ptr(last), B, T, R, Hkv, D, P, n_pages, M, _ptr(best_node),
+                                    _ptr(hidden_rows), out["h_next"].data_ptr() if H else None, H,
+                                    out["kv_len"].data_ptr(), _ptr(out.get("appended")), _raw_stream(stream, dev)))
     return out
 
 
@@ -450,25 +465,30 @@ def kv_pages_fork(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, src=No
     """Forks, frees and reserves: row b goes on from row src[b] (-1: freed; None:
     every row from itself) with room for need[b] more tokens.  Returns
     dict(page_table, kv_len, refs, taken); open pages are copied in the pools."""
-    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
-    dev = k_pages.device
-    for n, t, shape in (("src", src, (B,)), ("need", need, (B,)), ("held", held, (n_pages,))):
-        if t is not None:
-            _need_shape(t, n, shape, torch.int32, dev)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = dict(page_table=torch.empty_like(page_table), kv_len=torch.empty_like(kv_len),
-                       refs=torch.empty(n_pages, dtype=torch.int32, device=dev), taken=torch.empty_like(kv_len))
-        else:
-            for n, shape in (("page_table", (B, M)), ("kv_len", (B,)), ("refs", (n_pages,)), ("taken", (B,))):
-                _need_shape(out[n], f"out {n}", shape, torch.int32, dev)
-        if ws is None:
-            ws = _ws(kv_pages_fork_workspace(B, n_pages), dev)
-        check(lib().medusa_kv_pages_fork(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-                                         _ptr(page_table), _ptr(kv_len), _ptr(src), _ptr(need), _ptr(held), B,
-                                         Hkv, D, P, n_pages, M, _ptr(out["page_table"]), _ptr(out["kv_len"]),
-                                         _ptr(out["refs"]), _ptr(out["taken"]), _ptr(ws), ws.numel(),
-                                         _stream(stream)))
+    B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv_pages_fork(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, src, need, held, out, ws, stream)
+    if src is not None:
+        _need_shape(src, "src", (B,), _I32, dev)
+    if need is not None:
+        _need_shape(need, "need", (B,), _I32, dev)
+    if held is not None:
+        _need_shape(held, "held", (n_pages,), _I32, dev)
+    if out is None:
+        both = torch.empty((2, B), dtype=_I32, device=kv_len.device)
+        out = dict(page_table=torch.empty_like(page_table), kv_len=both[0],
+                   refs=torch.empty(n_pages, dtype=_I32, device=kv_len.device), taken=both[1])
+    else:
+        for n, shape in (("page_table", (B, M)), ("kv_len", (B,)), ("refs", (n_pages,)), ("taken", (B,))):
+            _need_shape(out[n], f"out {n}", shape, _I32, dev)
+    if ws is None:
+        ws = _ws(kv_pages_fork_workspace(B, n_pages), kv_len.device)
+    check(lib().medusa_kv_pages_fork(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                     page_table.data_ptr(), kv_len.data_ptr(), _ptr(src), _ptr(need), _ptr(held), B,
+                                     Hkv, D, P, n_pages, M, out["page_table"].data_ptr(), out["kv_len"].data_ptr(),
+                                     out["refs"].data_ptr(), out["taken"].data_ptr(), ws.data_ptr(), ws.numel(),
+                                     _raw_stream(stream, dev)))
     return out
 
 
@@ -479,22 +499,23 @@ def kv_pages_compact_workspace(n_pages):
 def kv_pages_compact(k_pages, v_pages, k_scale, v_scale, page_table, held=None, out=None, ws=None, stream=None):
     """Moves the pages in use into [0, live).  Returns dict(page_table, new_page,
     live); the pools change in place."""
-    B, M, n_pages, Hkv, P, D = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table)
-    dev = k_pages.device
+    B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv_pages_compact(k_pages, v_pages, k_scale, v_scale, page_table, held, out, ws, stream)
     if held is not None:
-        _need_shape(held, "held", (n_pages,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = dict(page_table=torch.empty_like(page_table),
-                       new_page=torch.empty(n_pages, dtype=torch.int32, device=dev),
-                       live=torch.empty(1, dtype=torch.int32, device=dev))
-        else:
-            for n, shape in (("page_table", (B, M)), ("new_page", (n_pages,)), ("live", (1,))):
-                _need_shape(out[n], f"out {n}", shape, torch.int32, dev)
-        if ws is None:
-            ws = _ws(kv_pages_compact_workspace(n_pages), dev)
-        check(lib().medusa_kv_pages_compact(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-                                            _ptr(page_table), _ptr(held), B, Hkv, D, P, n_pages, M,
-                                            _ptr(out["page_table"]), _ptr(out["new_page"]), _ptr(out["live"]),
-                                            _ptr(ws), ws.numel(), _stream(stream)))
+        _need_shape(held, "held", (n_pages,), _I32, dev)
+    if out is None:
+        out = dict(page_table=torch.empty_like(page_table),
+                   new_page=torch.empty(n_pages, dtype=_I32, device=page_table.device),
+                   live=torch.empty(1, dtype=_I32, device=page_table.device))
+    else:
+        for n, shape in (("page_table", (B, M)), ("new_page", (n_pages,)), ("live", (1,))):
+            _need_shape(out[n], f"out {n}", shape, _I32, dev)
+    if ws is None:
+        ws = _ws(kv_pages_compact_workspace(n_pages), page_table.device)
+    check(lib().medusa_kv_pages_compact(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                        page_table.data_ptr(), _ptr(held), B, Hkv, D, P, n_pages, M,
+                                        out["page_table"].data_ptr(), out["new_page"].data_ptr(),
+                                        out["live"].data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)))
     return out

@@ -7,16 +7,24 @@
 // The tree's own K and V rows are given in the model's type, next to the cache:
 // rejected candidates never reach a page.
 //
-//   tree_attn_q8_simple_kernel : float32 arithmetic on the CUDA cores
+//   tree_attn_q8_umma_kernel   : bf16, on the tensor cores
+//   tree_attn_q8_simple_kernel : float32, on the CUDA cores
 //   attn_q8_merge_kernel       : joins the partial results of units that several
 //                                CTAs share (q8.cuh, Work)
 #include <float.h>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "q8.cuh"
+#include "tmap.cuh"
+#include "umma.cuh"
 
 namespace medusa {
 namespace {
+
+MEDUSA_WAIT_CONTROL()
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -35,7 +43,6 @@ struct AttnQ8Args {
 };
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) {
     uint16_t r;
@@ -243,6 +250,776 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
     }
 }
 
+// ---------------------------------------------------------------------------
+// tcgen05 kernel (bf16 queries).
+//
+// Products on the 8-bit codes themselves.  The codes go from the page into the
+// matrix instruction as they are; what has more than e4m3's four significant
+// bits is split into planes that the instruction takes:
+//   scores   bf16 has 8 bits: q = q_hi + 2^-5 q_lo, two e4m3 planes under one
+//            power-of-two factor for the block, S = K q_hi + 2^-5 K q_lo; the
+//            page's scale multiplies S
+//   output   weight times V scale = p_hi + 2^-12 p_lo, p_hi in e4m3 and the rest
+//            in e5m2 (7 to 8 bits together), each plane summed on its own so that
+//            small weights keep their bits down to 2^-30 of the largest
+// so no key or value is ever converted: converting them would cost more
+// instructions than the whole softmax of 64 rows, and twice the shared memory.
+//
+// Transposed: S^T = K Q^T and O^T = V^T P^T, the 128 keys of a tile (then the D
+// output columns) in the TMEM lanes and the query rows in the columns.  A thread
+// owns one key: its scale is one register, the work is in proportion to the
+// query rows (from 16 on) rather than to the 128 rows of a matrix tile, and the
+// row sums are added up per thread and joined once per segment.  What crosses
+// threads is the rows' maximum, and that only when a score rises 2^4 above the
+// reference it is held against (the first tile and few others), which one
+// barrier vote per tile finds out.
+//
+// Two streams per CTA (threads 0-127 and 128-255), each with its own S and O in
+// TMEM, so that one stream's softmax runs while the other's products do:
+//   SHARED = false  blocks of NB rows; the streams take alternate tiles, each an
+//                   online softmax of its own, joined at the end
+//   SHARED = true   blocks of 2 NB rows; each stream has NB of them, both use
+//                   every tile
+// Steps x = 0, 1, 2, ...: stream x & 1, tile x (or x / 2).  For each x the MMA
+// lane issues PV(x), then S(x + 2); the commit of S of a stream's step therefore
+// covers its previous PV, and P and O are free when the scores arrive.
+//
+// Warps 0-7 softmax, warp 8 MMA, warp 9 TMA (page tables, scales and tiles run
+// ahead through a ring of R slots; a slot is K and V of one tile of 128 keys).
+// The tree's rows are bf16: such a tile takes two slots, and its products are
+// kind::f16 with q and P in bf16, added to the same sums.
+// Every wait is bounded; a CTA that gives up marks its results NaN.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 128;  // keys per tile
+constexpr int kUThreads = 320, kUSoftmax = 256, kUMmaWarp = 8, kUTmaWarp = 9;
+constexpr float kTau = 4.f;              // log2 by which weights may exceed 1
+constexpr float kPScale = 16.f;          // p_hi = weight * vs / v_ref * kPScale <= 256
+constexpr float kVHead = 4.f;            // v_ref = kVHead * the largest V scale when set
+constexpr float kQLo = 0.03125f;         // 2^-5
+constexpr float kPLo = 1.f / 4096.f;     // 2^-12
+constexpr long long kDrainCycles = kDefaultWaitCycles;
+
+template <int D, int NB, bool SHARED>
+struct USmem {
+    static constexpr int kRing = SHARED ? 3 : 4;
+    static constexpr int kBlocks = SHARED ? 2 : 1;             // row blocks of NB
+    static constexpr int kRowsBlock = NB * kBlocks;
+    static constexpr int kQ8 = 2 * NB * D;                     // hi rows, lo rows
+    static constexpr int kQB = NB * D * 2;                     // bf16, for the tree tiles
+    static constexpr int kHalf = kTile * D;                    // K or V codes of a tile
+    static constexpr int kSlot = 2 * kHalf;
+    static constexpr int kP = 2 * kTile * 64;                  // p_hi, p_lo (rows of 64 bytes)
+    static constexpr int kOffRing = 0;
+    static constexpr int kOffP = kOffRing + kRing * kSlot;
+    static constexpr int kOffQ8 = kOffP + 2 * kP;
+    static constexpr int kOffQB = kOffQ8 + (kBlocks * kQ8 + 1023) / 1024 * 1024;
+    static constexpr int kOffM = kOffQB + (kBlocks * kQB + 1023) / 1024 * 1024;  // float m[2][NB]
+    static constexpr int kOffCorr = kOffM + 2 * NB * 4;        // float corr[2][NB], later coefficients
+    static constexpr int kOffRed = kOffCorr + 2 * NB * 4;      // float red[2][4][NB]
+    static constexpr int kOffInfo = kOffRed + 8 * NB * 4;      // float2 (k, v scale)[kRing][8]
+    static constexpr int kOffBad = kOffInfo + kRing * 8 * 8;   // uint32 [16]: tree rows with a non-finite V
+    static constexpr int kOffMisc = kOffBad + 64;              // see below, 128 bytes
+    static constexpr int kOffBar = kOffMisc + 128;
+    // full[R] empty[R] s_full[2] p_full[2] o_done[2] qfull drain
+    static constexpr int kNumBar = 2 * kRing + 8;
+    static constexpr int kOffFirst = (kOffBar + kNumBar * 8 + 15) / 16 * 16;
+    static int bytes(int B) { return kOffFirst + (B + 1) * 8 + 1024; }  // + alignment slack
+};
+
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// pairs of floats on the paired float32 pipe
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
+    asm("{\n.reg .b64 ra, rb, rc, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\nmov.b64 rc, {%5, %6};\n"
+        "fma.rn.f32x2 rd, ra, rb, rc;\nmov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b) {
+    asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\n"
+        "mul.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+    asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%0, %1};\nmov.b64 rb, {%2, %3};\n"
+        "add.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}"
+        : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two weights (times V scale) into their e4m3 and e5m2 planes.  The pair passes
+// through f16 (11 bits), where hi and the rest it leaves are exact.
+__device__ __forceinline__ void split_weights(float a, float b, uint16_t& hi, uint16_t& lo) {
+    asm("{\n.reg .b32 x, h, r, k;\n.reg .b16 c;\n"
+        "cvt.rn.f16x2.f32 x, %3, %2;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 c, x;\n"
+        "mov.b16 %0, c;\n"
+        "cvt.rn.f16x2.e4m3x2 h, c;\n"
+        "sub.rn.f16x2 r, x, h;\n"
+        "mov.b32 k, 0x6c006c00;\n"  // 2^12, 2^12
+        "mul.rn.f16x2 r, r, k;\n"
+        "cvt.rn.satfinite.e5m2x2.f16x2 %1, r;\n}"
+        : "=h"(hi), "=h"(lo) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) { return (uint32_t)lo | (uint32_t)hi << 16; }
+
+template <int D, int NB, bool SHARED>
+__global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
+    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+    const __grid_constant__ CUtensorMap tmkt, const __grid_constant__ CUtensorMap tmvt, const AttnQ8Args a) {
+    using namespace umma;
+    using L = USmem<D, NB, SHARED>;
+    constexpr int R = L::kRing;
+    constexpr int kCols = NB == 64 ? 512 : 128;      // TMEM columns: S[2], O[2] of 2 NB each
+    constexpr uint32_t kS = 0, kO = 4 * NB;          // S_s at 2 NB s; O_s at 4 NB + 2 NB s
+    extern __shared__ uint8_t smem_raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const q8::Work w = a.work;
+
+    const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+    uint8_t* base = smem_raw + pad;
+    const uint32_t base_a = smem_addr(base);
+    const uint32_t ring_a = base_a + L::kOffRing, p_a = base_a + L::kOffP, q8_a = base_a + L::kOffQ8,
+                   qb_a = base_a + L::kOffQB;
+    const uint32_t bar_a = base_a + L::kOffBar;
+    const uint32_t full0 = bar_a, empty0 = full0 + 8 * R, s_full0 = empty0 + 8 * R, p_full0 = s_full0 + 16,
+                   o_done0 = p_full0 + 16, qfull = o_done0 + 16, drain = qfull + 8;
+    float* s_m = reinterpret_cast<float*>(base + L::kOffM);
+    float* s_corr = reinterpret_cast<float*>(base + L::kOffCorr);
+    float* s_red = reinterpret_cast<float*>(base + L::kOffRed);
+    float2* s_info = reinterpret_cast<float2*>(base + L::kOffInfo);
+    uint32_t* s_bad = reinterpret_cast<uint32_t*>(base + L::kOffBad);
+    float* s_misc = reinterpret_cast<float*>(base + L::kOffMisc);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_misc);
+    volatile int* flag = reinterpret_cast<volatile int*>(s_misc + 1);      // a wait gave up
+    volatile int* s_fail = reinterpret_cast<volatile int*>(s_misc + 2);    // [2] per stream
+    float* s_qmax = s_misc + 4;                                            // [8] per warp
+    float* s_vmax = s_misc + 12;                                           // [2][4] largest V scale per warp
+    float* s_vref = s_misc + 20;                                           // [2] at the end of a segment
+    long long* first = reinterpret_cast<long long*>(base + L::kOffFirst);
+    const long long lim = g_wait_limit;
+
+    if (warp == kUTmaWarp && lane == 0) {
+        for (int i = 0; i < L::kNumBar; ++i) mbar_init(bar_a + 8 * i, 1);
+        mbar_init(p_full0, 4);
+        mbar_init(p_full0 + 8, 4);
+        mbar_init(qfull, kUSoftmax / 32);
+        mbar_init_fence();
+        *flag = 0;
+        s_fail[0] = s_fail[1] = 0;
+        prefetch_tmap(&tmk);
+        prefetch_tmap(&tmv);
+        prefetch_tmap(&tmkt);
+        prefetch_tmap(&tmvt);
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, kCols);
+    pdl_wait();
+    pdl_trigger();
+    q8::tile_offsets(w, a.kv_len, first);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const long long total = first[w.B];
+    const long long g_begin = w.cta_begin(total, blockIdx.x), g_end = w.cta_begin(total, blockIdx.x + 1);
+    const int ppt = kTile / a.P;  // pages per tile
+    const int rows_all = w.N * a.G;
+    long long g_failed = g_end;   // first segment whose results are not there
+    bool gave_up = false;
+
+    // tiles of a segment: n_pre of the prefix, then n_tree of the tree
+    auto prefix_of = [&](const q8::Segment& s, int& n_pre, int& n_tree) {
+        const int pt = w.prefix_tiles(s.L);
+        n_pre = max(0, min(s.t1, pt) - s.t0);
+        n_tree = s.t1 - s.t0 - n_pre;
+    };
+
+    if (warp == kUMmaWarp) {
+        // -------------------------------- MMA lane --------------------------------
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_f8(128, 2 * NB, 0, 0, 0, 0);
+            constexpr uint32_t id_hi = idesc_f8(128, NB, 0, 0, 1, 1), id_lo = idesc_f8(128, NB, 0, 1, 1, 1);
+            constexpr uint32_t id_st = idesc_bf16(128, NB, 0, 0), id_pt = idesc_bf16(128, NB, 1, 1);
+            bool fail = false;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (fail) return false;
+                if (!mbar_wait(bar, parity, lim)) { fail = true; *flag = 1; return false; }
+                return true;
+            };
+            auto desc8 = [](uint32_t addr) {  // codes: rows of D bytes, either major
+                return D == 128 ? desc_sw128(addr, 16, 1024) : desc_sw64(addr, 0, 512);
+            };
+            int slot0 = 0;           // first slot of the segment
+            int n_p[2] = {0, 0};     // steps of each stream so far
+            int seg = 0;
+            for (long long g = g_begin; g < g_end && !fail; ++seg) {
+                const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+                g += s.t1 - s.t0;
+                int n_pre, n_tree;
+                prefix_of(s, n_pre, n_tree);
+                const int steps = (n_pre + n_tree) * (SHARED ? 2 : 1);
+                auto tile_of = [&](int x) { return SHARED ? x >> 1 : x; };
+                auto slot_of = [&](int t) { return slot0 + t + max(0, t - n_pre); };
+                auto issue_s = [&](int x) {
+                    const int t = tile_of(x), sl = slot_of(t), st = x & 1, blk = SHARED ? st : 0;
+                    if (!wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1))) return;
+                    fence_after_sync();
+                    const uint32_t k = ring_a + (sl % R) * L::kSlot, d = tmem + kS + st * 2 * NB;
+                    if (t < n_pre) {
+                        const uint64_t dk = desc8(k), dq = desc8(q8_a + blk * L::kQ8);
+#pragma unroll
+                        for (int ks = 0; ks < D / 32; ++ks) mma_f8(d, dk + 2 * ks, dq + 2 * ks, id_s, ks > 0);
+                    } else {
+                        const uint64_t dk = desc_sw128(k, 16, 1024), dq = desc_sw128(qb_a + blk * L::kQB, 16, 1024);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_bf16(d, dk + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
+                                     dq + (((ks >> 2) * (NB * 128) + (ks & 3) * 32) >> 4), id_st, ks > 0);
+                    }
+                    commit(s_full0 + 8 * st);
+                };
+                auto issue_pv = [&](int x) {
+                    const int t = tile_of(x), sl = slot_of(t), st = x & 1, i = x >> 1;
+                    const uint32_t d = tmem + kO + st * 2 * NB, p = p_a + st * L::kP;
+                    if (t < n_pre) {
+                        const uint64_t dv = desc8(ring_a + (sl % R) * L::kSlot + L::kHalf);
+                        const uint64_t dh = desc_sw64(p, 0, 512), dl = desc_sw64(p + kTile * 64, 0, 512);
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 32; ++ks)
+                            mma_f8(d, dv + ((ks * 32 * D) >> 4), dh + ((ks * 2048) >> 4), id_hi, i > 0 || ks > 0);
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 32; ++ks)
+                            mma_f8(d + NB, dv + ((ks * 32 * D) >> 4), dl + ((ks * 2048) >> 4), id_lo, i > 0 || ks > 0);
+                    } else {
+                        const int sv = sl + 1;
+                        if (!wait(full0 + 8 * (sv % R), (uint32_t)((sv / R) & 1))) return;
+                        // D = 64: the second half of the lanes repeats the first
+                        const uint64_t dv = desc_sw128(ring_a + (sv % R) * L::kSlot, D == 128 ? kTile * 128 : 0, 1024);
+                        const uint64_t dp = desc_sw128(p, 0, 1024);
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 16; ++ks)
+                            mma_bf16(d, dv + ((ks * 2048) >> 4), dp + ((ks * 2048) >> 4), id_pt, i > 0 || ks > 0);
+                    }
+                    if (x + 2 >= steps) commit(o_done0 + 8 * st);  // the stream's last
+                    if (!SHARED || st == 1) {
+                        commit(empty0 + 8 * (sl % R));
+                        if (t >= n_pre) commit(empty0 + 8 * ((sl + 1) % R));
+                    }
+                };
+                if (!wait(qfull, (uint32_t)(seg & 1))) break;
+                for (int x = 0; x < 2 && x < steps && !fail; ++x) issue_s(x);
+                for (int x = 0; x < steps && !fail; ++x) {
+                    const int st = x & 1;
+                    if (!wait(p_full0 + 8 * st, (uint32_t)((n_p[st] + (x >> 1)) & 1))) break;
+                    fence_after_sync();
+                    issue_pv(x);
+                    if (x + 2 < steps && !fail) issue_s(x + 2);
+                }
+                n_p[0] += (steps + 1) >> 1;
+                n_p[1] += steps >> 1;
+                slot0 += n_pre + 2 * n_tree;
+            }
+            if (fail) {  // let everything in flight complete before TMEM is freed
+                commit(drain);
+                mbar_wait(drain, 0, kDrainCycles);
+            }
+        }
+    } else if (warp == kUTmaWarp) {
+        // -------------------------------- TMA warp --------------------------------
+        int slot = 0;
+        bool fail = false;
+        auto free_slot = [&](int sl) {
+            if (sl >= R && !mbar_wait(empty0 + 8 * (sl % R), (uint32_t)((sl / R - 1) & 1), lim)) fail = true;
+            fail = __any_sync(0xffffffffu, fail);
+            return !fail;
+        };
+        for (long long g = g_begin; g < g_end && !fail;) {
+            const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+            g += s.t1 - s.t0;
+            int n_pre, n_tree;
+            prefix_of(s, n_pre, n_tree);
+            const int hk = s.unit / a.qblocks;
+            const int32_t* table = a.page_table + (size_t)s.b * a.M;
+            const int pg0 = s.t0 * ppt, pages = (s.L + a.P - 1) / a.P;
+            // lane i holds page i of a group of 32: its number two groups ahead, its
+            // scales one group ahead
+            auto page_id = [&](int i) {
+                const int pg = pg0 + i;
+                if (n_pre == 0 || pg >= pages) return -1;
+                const int p = __ldg(table + pg);
+                return p >= 0 && p < a.n_pages ? p : -1;
+            };
+            auto scales = [&](int p) {
+                if (p < 0) return make_float2(0.f, 0.f);
+                const size_t u = (size_t)p * a.Hkv + hk;
+                return make_float2(__ldg(a.k_scale + u), __ldg(a.v_scale + u));
+            };
+            int id = page_id(lane), id1 = page_id(32 + lane), id2 = -1;
+            float2 sc = scales(id), sc1 = make_float2(0.f, 0.f);
+            for (int u = 0; u < n_pre; ++u, ++slot) {
+                const int li = (u * ppt) & 31;
+                if (li == 0) {
+                    if (u) { id = id1; sc = sc1; id1 = id2; }
+                    sc1 = scales(id1);
+                    id2 = page_id(u * ppt + 64 + lane);
+                }
+                if (!free_slot(slot)) break;
+                const int st = slot % R, j = lane - li;
+                const bool in = j >= 0 && j < ppt, there = in && id >= 0;
+                if (there) {
+                    const int y = (id * a.Hkv + hk) * a.P;
+                    const uint32_t dst = ring_a + st * L::kSlot + j * a.P * D;
+                    tma_load_2d(dst, &tmk, 0, y, full0 + 8 * st);
+                    tma_load_2d(dst + L::kHalf, &tmv, 0, y, full0 + 8 * st);
+                }
+                const unsigned m = __ballot_sync(0xffffffffu, there);
+                if (in)
+                    s_info[st * 8 + j] = there && q8::scale_ok(sc.x) && q8::scale_ok(sc.y) ? sc : make_float2(0.f, 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_expect_tx(full0 + 8 * st, (uint32_t)(__popc(m) * a.P * D * 2));
+            }
+            const int pt = w.prefix_tiles(s.L);
+            for (int u = n_pre; u < n_pre + n_tree && !fail; ++u) {
+                const int row = (s.t0 + u - pt) * kTile;
+                for (int kv = 0; kv < 2; ++kv, ++slot) {
+                    if (!free_slot(slot)) break;
+                    if (lane == 0) {
+                        const int st = slot % R;
+                        mbar_expect_tx(full0 + 8 * st, kTile * D * 2);
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_4d(ring_a + st * L::kSlot + x * kTile * 128, kv ? &tmvt : &tmkt, x * 64, hk, row, s.b,
+                                        full0 + 8 * st);
+                    }
+                }
+            }
+        }
+        if (fail) {
+            if (lane == 0) {
+                *flag = 1;
+                // every slot that was asked for lands before the CTA leaves
+                for (int sl = max(0, slot - R); sl < slot; ++sl)
+                    mbar_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), kDrainCycles);
+            }
+        }
+    } else {
+        // ------------------------------ softmax warps ------------------------------
+        const int st = warp >> 2, quarter = warp & 3;
+        const int key = quarter * 32 + lane;  // TMEM lane: key of a tile, then output column
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off + kS + st * 2 * NB, tO = tmem + lane_off + kO + st * 2 * NB;
+        float* m_row = s_m + st * NB;
+        float* corr_row = s_corr + st * NB;
+        uint8_t* p_row = base + L::kOffP + st * L::kP;
+        const float scale = a.scale_log2;
+        int n_s = 0;       // steps of this stream before the segment
+        int n_o = 0;       // segments in which it had any
+        int slot0 = 0;
+        for (long long g = g_begin; g < g_end;) {
+            const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+            const long long g_seg = g;
+            g += s.t1 - s.t0;
+            int n_pre, n_tree;
+            prefix_of(s, n_pre, n_tree);
+            const int n = n_pre + n_tree;
+            const int steps = SHARED ? n : (n + 1 - st) >> 1;  // of this stream
+            const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * L::kRowsBlock;
+            const int nrows = min(L::kRowsBlock, rows_all - row0);
+
+            // Q into shared memory: bf16 for the tree's tiles, two e4m3 planes for the
+            // pages'.  Rows behind the block's end are zero.
+            constexpr int CH = D / 8, QCH = L::kRowsBlock * CH / kUSoftmax;
+            static_assert(L::kRowsBlock * CH % kUSoftmax == 0 || L::kRowsBlock * CH < kUSoftmax, "whole passes over Q");
+            constexpr int QN = QCH ? QCH : 1;
+            uint4 qv[QN];
+            float qmax = 0.f;
+#pragma unroll
+            for (int i = 0; i < QN; ++i) {
+                const int c = tid + i * kUSoftmax, r = c / CH;
+                qv[i] = make_uint4(0, 0, 0, 0);
+                if (r < nrows) {
+                    const int gr = row0 + r;
+                    qv[i] = ld_stream16(static_cast<const uint16_t*>(a.q) +
+                                        (((size_t)s.b * w.N + gr / a.G) * a.Hq + hk * a.G + gr % a.G) * D + c % CH * 8);
+                }
+                const uint32_t x[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float f0 = fabsf(bf16_lo(x[e])), f1 = fabsf(bf16_hi(x[e]));
+                    if (f0 < INFINITY) qmax = fmaxf(qmax, f0);
+                    if (f1 < INFINITY) qmax = fmaxf(qmax, f1);
+                }
+            }
+            // tree rows whose V is not finite: 0 * inf of a row that does not see them
+            // would spoil that row, so their V counts as zero and rows that see them get NaN
+            if (n_tree) {
+                if (tid < 16) s_bad[tid] = 0;
+                bar_sync(3, kUSoftmax);
+                for (int c = tid; c < w.N * CH; c += kUSoftmax) {
+                    const int m = c / CH;
+                    const uint4 v = ld_stream16(static_cast<const uint16_t*>(a.v_tree) +
+                                                (((size_t)s.b * w.N + m) * a.Hkv + hk) * D + c % CH * 8);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        bad = bad || (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+                    if (bad) atomicOr(&s_bad[m >> 5], 1u << (m & 31));
+                }
+            }
+            qmax = redux_max(qmax);
+            if (lane == 0) s_qmax[warp] = qmax;
+            if (key < NB) m_row[key] = -INFINITY;
+            bar_sync(3, kUSoftmax);  // the last segment's sums are read, its Q is free
+#pragma unroll
+            for (int i = 0; i < kUSoftmax / 32; ++i) qmax = fmaxf(qmax, s_qmax[i]);
+            // factor 2^k with qmax * 2^k in [128, 256)
+            const int qe = q8::clamp_int(254 + 7 - (int)(__float_as_uint(qmax) >> 23), 1, 253);
+            const float qf = __uint_as_float((uint32_t)qe << 23);
+            const float kq = scale * __uint_as_float((uint32_t)(254 - qe) << 23);  // scale / qf
+#pragma unroll
+            for (int i = 0; i < QN; ++i) {
+                const int c = tid + i * kUSoftmax, r = c / CH, ch = c % CH;
+                if (r >= L::kRowsBlock) continue;
+                const int blk = SHARED ? r / NB : 0, rb = SHARED ? r % NB : r;
+                const uint32_t x[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+                uint16_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float f0 = bf16_lo(x[e]) * qf, f1 = bf16_hi(x[e]) * qf;
+                    if (!(fabsf(f0) < INFINITY)) f0 = NAN;
+                    if (!(fabsf(f1) < INFINITY)) f1 = NAN;
+                    hi[e] = q8::float2_to_e4m3x2(f0, f1);
+                    const float2 h = q8::e4m3x2_to_float2(hi[e]);
+                    lo[e] = q8::float2_to_e4m3x2((f0 - h.x) * 32.f, (f1 - h.y) * 32.f);
+                }
+                uint8_t* q8p = base + L::kOffQ8 + blk * L::kQ8;
+                auto at8 = [&](int row) {  // 8 bytes of chunk ch of a row of D codes
+                    const int c16 = ch >> 1;
+                    return D == 128 ? row * 128 + ((c16 ^ (row & 7)) << 4) + (ch & 1) * 8
+                                    : row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4) + (ch & 1) * 8;
+                };
+                *reinterpret_cast<uint2*>(q8p + at8(rb)) = make_uint2(join16(hi[0], hi[1]), join16(hi[2], hi[3]));
+                *reinterpret_cast<uint2*>(q8p + at8(NB + rb)) = make_uint2(join16(lo[0], lo[1]), join16(lo[2], lo[3]));
+                if (n_tree)
+                    *reinterpret_cast<uint4*>(base + L::kOffQB + blk * L::kQB + sw128_offset(rb, ch, NB)) = qv[i];
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull);
+
+            float l[NB];
+#pragma unroll
+            for (int c = 0; c < NB; ++c) l[c] = 0.f;
+            float v_ref = 0.f;
+            bool fail = false;
+            const int pt = w.prefix_tiles(s.L);
+            for (int i = 0; i < steps; ++i) {
+                const int t = SHARED ? i : 2 * i + st;
+                const int sl = slot0 + t + max(0, t - n_pre);
+                const bool tree = t >= n_pre;
+                bool ok = mbar_wait(s_full0 + 8 * st, (uint32_t)((n_s + i) & 1), lim);
+                float kc = kq, vs = 1.f;
+                uint32_t seen_lo = 0xffffffffu, seen_hi = 0xffffffffu;  // rows that see the key
+                bool valid = true, bad_v = false;
+                if (!tree) {
+                    // the slot is in since the scores are; this wait makes the scales visible
+                    ok = mbar_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), lim) && ok;
+                    const float2 sc = s_info[(sl % R) * 8 + key / a.P];
+                    valid = sc.y > 0.f && (s.t0 + t) * kTile + key < s.L;
+                    kc = valid ? kq * sc.x : 0.f;
+                    vs = valid ? sc.y : 0.f;
+                } else {
+                    kc = scale;
+                    const int m = (s.t0 + t - pt) * kTile + key;  // tree row
+                    valid = m < w.N;
+                    seen_lo = seen_hi = 0;
+                    // bit c: row c of this stream's block sees tree row m (all lanes of a
+                    // warp read the same word)
+                    const int r_first = row0 + (SHARED ? st * NB : 0);
+                    if ((m & ~31) < w.N)
+                        for (int c = 0; c < NB && r_first + c < rows_all; ++c) {
+                            const uint64_t word = __ldg(a.mask + (size_t)((r_first + c) / a.G) * a.W + (m >> 6));
+                            const uint32_t bit = valid ? (uint32_t)(word >> (m & 63)) & 1u : 0u;
+                            if (c < 32) seen_lo |= bit << c; else seen_hi |= bit << (c - 32);
+                        }
+                    bad_v = valid && (s_bad[m >> 5] >> (m & 31) & 1);
+                    if (__any_sync(0xffffffffu, bad_v))
+                        ok = mbar_wait(full0 + 8 * ((sl + 1) % R), (uint32_t)(((sl + 1) / R) & 1), lim) && ok;
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                fence_after_sync();
+                if (!ok && lane == 0) s_fail[st] = 1;
+                // A key that is not there has no V either: whatever the slot holds (stale
+                // codes may be NaN) is cleared.  When two streams share the tile, stream 0
+                // does it: its PV comes first.
+                if (!SHARED || st == 0) {
+                    if (!tree && !valid) {
+                        uint4* v = reinterpret_cast<uint4*>(base + L::kOffRing + (sl % R) * L::kSlot + L::kHalf + key * D);
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                    }
+                    if (bad_v) {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x) {
+                            uint4* v = reinterpret_cast<uint4*>(base + L::kOffRing + ((sl + 1) % R) * L::kSlot +
+                                                                x * kTile * 128 + key * 128);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
+
+                // scores in log2 units above the rows' references
+                float t2[NB];
+                auto load_scores = [&](bool relative) {
+#pragma unroll
+                    for (int c0 = 0; c0 < NB; c0 += 16) {
+                        float hi[16], lo[16];
+                        tmem_ld16(tS + c0, hi);
+                        tmem_ld16(tS + NB + c0, lo);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float x0 = hi[e], x1 = hi[e + 1];
+                            if (!tree) fma2(x0, x1, lo[e], lo[e + 1], kQLo, x0, x1);
+                            float m0 = 0.f, m1 = 0.f;
+                            if (relative) {
+                                const float2 mm = *reinterpret_cast<const float2*>(m_row + c0 + e);
+                                m0 = -mm.x; m1 = -mm.y;
+                            }
+                            fma2(t2[c0 + e], t2[c0 + e + 1], x0, x1, kc, m0, m1);
+                        }
+                    }
+                    if (tree || !valid) {
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) {
+                            const bool see = valid && ((c < 32 ? seen_lo >> c : seen_hi >> (c - 32)) & 1);
+                            t2[c] = see ? t2[c] : -INFINITY;
+                        }
+                    }
+                };
+                load_scores(true);
+                float top = t2[0];
+#pragma unroll
+                for (int c = 1; c + 1 < NB; c += 2) top = max3(top, t2[c], t2[c + 1]);
+                top = fmaxf(top, t2[NB - 1]);
+                if (named_barrier_or(1 + st, 128, !ok || top > kTau || vs > v_ref)) {
+                    // the references move: largest score per row over the tile's keys
+                    load_scores(false);
+#pragma unroll
+                    for (int c = 0; c < NB; ++c) {
+                        const float m = redux_max(t2[c]);
+                        if (lane == (c & 31)) s_red[(st * 4 + quarter) * NB + c] = m;
+                    }
+                    const float vm = redux_max(vs);
+                    if (lane == 0) s_vmax[st * 4 + quarter] = vm;
+                    bar_sync(1 + st, 128);
+                    if (s_fail[st]) { fail = true; }
+                    if (key < NB) {
+                        const float* r = s_red + st * 4 * NB + key;
+                        const float m0 = m_row[key];
+                        const float m1 = fmaxf(fmaxf(fmaxf(r[0], r[NB]), fmaxf(r[2 * NB], r[3 * NB])), m0);
+                        corr_row[key] = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);
+                        m_row[key] = m1;
+                    }
+                    float v1 = fmaxf(fmaxf(s_vmax[st * 4], s_vmax[st * 4 + 1]), fmaxf(s_vmax[st * 4 + 2], s_vmax[st * 4 + 3]));
+                    v1 = v1 > v_ref ? v1 * kVHead : v_ref;
+                    const float vf = v1 > 0.f ? v_ref / v1 : 0.f;
+                    v_ref = v1;
+                    bar_sync(1 + st, 128);
+                    if (fail) break;
+#pragma unroll
+                    for (int c = 0; c < NB; ++c) l[c] *= corr_row[c];
+                    if (i > 0) {  // O holds the earlier tiles: their PV preceded these scores
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 2 * NB; c0 += 16) {
+                            float o[16];
+                            tmem_ld16(tO + c0, o);
+                            tmem_wait_ld();
+                            const float* cr = corr_row + (c0 & (NB - 1));
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= cr[e] * vf;
+                            tmem_st16(tO + c0, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    load_scores(true);
+                }
+                // weights, their sums, and their planes
+                const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
+                if (!tree) {
+#pragma unroll
+                    for (int c0 = 0; c0 < NB; c0 += 16) {
+                        uint32_t h[4], lw[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint16_t hh[2], ll[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int c = c0 + 4 * e + 2 * k;
+                                const float p0 = exp2_approx(t2[c]), p1 = exp2_approx(t2[c + 1]);
+                                add2(l[c], l[c + 1], p0, p1);
+                                float w0, w1;
+                                mul2(w0, w1, p0, p1, f);
+                                split_weights(w0, w1, hh[k], ll[k]);
+                            }
+                            h[e] = join16(hh[0], hh[1]);
+                            lw[e] = join16(ll[0], ll[1]);
+                        }
+                        const int off = key * 64 + (((c0 >> 4) ^ ((key >> 1) & 3)) << 4);
+                        *reinterpret_cast<uint4*>(p_row + off) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(p_row + kTile * 64 + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c0 = 0; c0 < NB; c0 += 8) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = c0 + 2 * e;
+                            float p0 = exp2_approx(t2[c]), p1 = exp2_approx(t2[c + 1]);
+                            h[e] = pack_bf16x2(p0 * f, p1 * f);
+                            if (bad_v) {
+                                if (t2[c] > -INFINITY) p0 = NAN;
+                                if (t2[c + 1] > -INFINITY) p1 = NAN;
+                            }
+                            add2(l[c], l[c + 1], p0, p1);
+                        }
+                        *reinterpret_cast<uint4*>(p_row + key * 128 + (((c0 >> 3) ^ (key & 7)) << 4)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+                fence_async_smem();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full0 + 8 * st);
+            }
+            bool ok = !fail;
+            if (ok && steps > 0) ok = mbar_wait(o_done0 + 8 * st, (uint32_t)(n_o & 1), lim);
+            // row sums over the stream's keys: halve the columns a thread holds while
+            // exchanging the other half
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                const float v = warp_sum(l[c]);
+                if (lane == (c & 31)) s_red[(st * 4 + quarter) * NB + c] = v;
+            }
+            if (key == 0) s_vref[st] = v_ref;
+            if (named_barrier_or(3, kUSoftmax, !ok)) {
+                gave_up = true;
+                g_failed = g_seg;
+                break;
+            }
+            fence_after_sync();
+            n_s += steps;
+            n_o += steps > 0;
+            slot0 += n_pre + 2 * n_tree;
+
+            // Each row's coefficients.  Split streams: relative to the larger reference.
+            const bool whole = s.whole();
+            const size_t part = (size_t)s.slot(blockIdx.x) * L::kRowsBlock;
+            if (tid < L::kRowsBlock) {
+                auto sum_of = [&](int x, int c) {
+                    const float* r = s_red + x * 4 * NB + c;
+                    return (r[0] + r[NB]) + (r[2 * NB] + r[3 * NB]);
+                };
+                float m, sum, c0, c1 = 0.f;
+                if (SHARED) {
+                    const int x = tid / NB, c = tid % NB;
+                    m = s_m[x * NB + c];
+                    sum = sum_of(x, c);
+                    c0 = s_vref[x] / kPScale;
+                } else {
+                    const float ma = s_m[tid], mb = s_m[NB + tid];
+                    m = fmaxf(ma, mb);
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const float wa = exp2f(ma - ref), wb = exp2f(mb - ref);
+                    sum = sum_of(0, tid) * wa + sum_of(1, tid) * wb;
+                    c0 = wa * s_vref[0] / kPScale;
+                    c1 = wb * s_vref[1] / kPScale;
+                }
+                if (whole) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    c0 *= inv;
+                    c1 *= inv;
+                } else {
+                    a.part_ml[part + tid] = make_float2(m, sum);
+                }
+                s_corr[tid] = c0;
+                if (!SHARED) s_corr[NB + tid] = c1;
+            }
+            bar_sync(3, kUSoftmax);
+            // O^T: this thread's output column of half the rows (split) or of its
+            // stream's rows (shared)
+            const int n_a = SHARED ? n : (n + 1) >> 1, n_b = SHARED ? 0 : n >> 1;  // steps behind O_0 and O_1
+            const bool lo_a = n_pre > 0, lo_b = n_pre > 1;                          // prefix tiles among them
+            constexpr int COLS = SHARED ? NB : NB / 2;
+            const int col0 = SHARED ? 0 : st * COLS;
+            const uint32_t oa = tmem + lane_off + kO + (SHARED ? st * 2 * NB : 0), ob = tmem + lane_off + kO + 2 * NB;
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 8) {
+                float va[8], vl[8], wa[8], wl[8];
+                tmem_ld8(oa + col0 + c, va);
+                if (lo_a) tmem_ld8(oa + NB + col0 + c, vl);
+                if (n_b > 0) tmem_ld8(ob + col0 + c, wa);
+                if (n_b > 0 && lo_b) tmem_ld8(ob + NB + col0 + c, wl);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = SHARED ? st * NB + c + e : col0 + c + e;  // row of the block
+                    if (r >= nrows || key >= D) continue;
+                    float o = n_a > 0 ? va[e] + (lo_a ? vl[e] * kPLo : 0.f) : 0.f;
+                    o *= s_corr[r];
+                    if (n_b > 0) o = fmaf(wa[e] + (lo_b ? wl[e] * kPLo : 0.f), s_corr[NB + r], o);
+                    if (whole) {
+                        const int gr = row0 + r;
+                        store1(static_cast<uint16_t*>(a.out) +
+                                   (((size_t)s.b * w.N + gr / a.G) * a.Hq + hk * a.G + gr % a.G) * D + key, o);
+                    } else {
+                        a.part_o[(part + r) * D + key] = o;
+                    }
+                }
+            }
+            fence_before_sync();
+        }
+    }
+    const bool bad = __syncthreads_or(gave_up);
+    if (bad) {
+        // what this CTA was to give from the segment on that it could not finish
+        if (tid == 0) atomicExch(&g_wait_gave_up, 1);
+        for (long long g = g_failed; g < g_end && warp < 8;) {
+            const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+            g += s.t1 - s.t0;
+            const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * L::kRowsBlock;
+            const int nrows = min(L::kRowsBlock, rows_all - row0);
+            if (!s.whole()) {
+                if (tid < L::kRowsBlock)
+                    a.part_ml[(size_t)s.slot(blockIdx.x) * L::kRowsBlock + tid] = make_float2(0.f, NAN);
+                continue;
+            }
+            for (int i = tid; i < nrows * D; i += kUSoftmax) {
+                const int gr = row0 + i / D;
+                store1(static_cast<uint16_t*>(a.out) +
+                           (((size_t)s.b * w.N + gr / a.G) * a.Hq + hk * a.G + gr % a.G) * D + i % D, NAN);
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, kCols);
+}
+
 // Joins the partial results.  Block (c, y): the unit that share c - 1 leaves
 // unfinished, if that is the first share boundary inside it; rows y, y + gridDim.y, ...
 template <typename T, int D>
@@ -290,10 +1067,16 @@ __global__ void __launch_bounds__(D) attn_q8_merge_kernel(const AttnQ8Args a, in
 
 struct Plan {
     int rows, keys, ctas;
+    bool shared;
 };
-Plan plan_q8(medusa_dtype dtype) {
-    (void)dtype;
-    return Plan{kRows, kKeys, 2 * sm_count()};
+// Rows per block, by the rows a KV head has: 16 (plain decoding), 64, or 128 in
+// two streams.
+Plan plan_q8(medusa_dtype dtype, int N, int G) {
+    const int rows = N * G, sms = sm_count();
+    if (dtype == MEDUSA_F32) return Plan{kRows, kKeys, 2 * sms, false};
+    if (rows <= 16) return Plan{16, kTile, sms, false};
+    if (rows <= 64) return Plan{64, kTile, sms, false};
+    return Plan{128, kTile, sms, true};
 }
 
 int check_attn_q8(int B, int N, int Hq, int Hkv, int D, int P, int n_pages, int M) {
@@ -318,14 +1101,55 @@ cudaError_t launch_simple(AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     return e;
 }
 
+// codes [n_pages * Hkv * P][D] in boxes of one (page, head)
+int pages_map(CUtensorMap* m, const void* pages, int D, int P, long long rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return fail(MEDUSA_ERR_CUDA, "tree_attention_q8: cuTensorMapEncodeTiled is unavailable");
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)D};
+    cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)P};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pages), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MEDUSA_ERR_CUDA, "tree_attention_q8: tensor map encode failed (%d)", (int)r);
+    return MEDUSA_OK;
+}
+
+// tree rows [B][N][Hkv][D] bf16 in boxes of 128 rows of one head x 64 elements;
+// rows behind N read zero
+int rows_map(CUtensorMap* m, const void* rows, int D, int Hkv, int N, int B) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)N, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)N * Hkv * D * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)kTile, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(rows), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MEDUSA_ERR_CUDA, "tree_attention_q8: tensor map encode failed (%d)", (int)r);
+    return MEDUSA_OK;
+}
+
+template <int D, int NB, bool SHARED>
+cudaError_t launch_umma(const CUtensorMap (&m)[4], AttnQ8Args& a, const Plan& p, cudaStream_t st) {
+    auto kern = tree_attn_q8_umma_kernel<D, NB, SHARED>;
+    const int smem = USmem<D, NB, SHARED>::bytes(a.work.B);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch(kern, dim3(p.ctas), dim3(kUThreads), smem, st, m[0], m[1], m[2], m[3], a);
+    if (e == cudaSuccess)
+        e = launch(attn_q8_merge_kernel<uint16_t, D>, dim3(p.ctas - 1, 4), dim3(D), (a.work.B + 1) * 8, st, a, p.rows);
+    return e;
+}
+
 }  // namespace
 }  // namespace medusa
 
 using namespace medusa;
 
 extern "C" size_t medusa_tree_attention_q8_workspace(int B, int N, int Hq, int Hkv, int D, medusa_dtype dtype) {
-    if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || (D != 64 && D != 128)) return 0;
-    return ws_bytes_q8(plan_q8(dtype), D);
+    if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128)) return 0;
+    return ws_bytes_q8(plan_q8(dtype, N, Hq / Hkv), D);
 }
 
 extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype,
@@ -344,7 +1168,7 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
         return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: q, tree rows, pages and out must be 16-byte aligned");
     if (!(scale > 0.f) || scale > 3.0e38f)
         return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: scale must be positive and finite");
-    const Plan p = plan_q8(dtype);
+    const Plan p = plan_q8(dtype, N, Hq / Hkv);
     const size_t need = ws_bytes_q8(p, D);
     if (!ws || ws_bytes < need)
         return fail(MEDUSA_ERR_WORKSPACE, "tree_attention_q8: workspace of %zu bytes needed", need);
@@ -362,10 +1186,25 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     a.scale_log2 = scale * kLog2e;
     cudaStream_t st = as_stream(stream);
     cudaError_t e;
-    if (dtype == MEDUSA_F32)
+    if (dtype == MEDUSA_F32) {
         e = D == 64 ? launch_simple<float, 64>(a, p, st) : launch_simple<float, 128>(a, p, st);
-    else
-        e = D == 64 ? launch_simple<uint16_t, 64>(a, p, st) : launch_simple<uint16_t, 128>(a, p, st);
+    } else {
+        CUtensorMap m[4];
+        const long long rows = (long long)n_pages * Hkv * P;
+        int rc = pages_map(&m[0], k_pages, D, P, rows);
+        if (!rc) rc = pages_map(&m[1], v_pages, D, P, rows);
+        if (!rc) rc = rows_map(&m[2], k_tree, D, Hkv, N, B);
+        if (!rc) rc = rows_map(&m[3], v_tree, D, Hkv, N, B);
+        if (rc) return rc;
+        if (D == 64)
+            e = p.rows == 16   ? launch_umma<64, 16, false>(m, a, p, st)
+                : p.rows == 64 ? launch_umma<64, 64, false>(m, a, p, st)
+                               : launch_umma<64, 64, true>(m, a, p, st);
+        else
+            e = p.rows == 16   ? launch_umma<128, 16, false>(m, a, p, st)
+                : p.rows == 64 ? launch_umma<128, 64, false>(m, a, p, st)
+                               : launch_umma<128, 64, true>(m, a, p, st);
+    }
     if (e != cudaSuccess)
         return fail(MEDUSA_ERR_CUDA, "tree_attention_q8: launch failed: %s", cudaGetErrorString(e));
     return MEDUSA_OK;
