@@ -361,9 +361,10 @@ int medusa_kv_compact(void* k_cache, void* v_cache, int32_t* kv_len, const int32
 /*   mask           [N, ceil(N/64)] uint64 from medusa_tree_layout             */
 /*   out            [B,N,Hq,D]   dtype, rounded once from float32              */
 /* Scores, softmax and sums are float32; codes, q and tree rows enter the      */
-/* products exactly (bf16 q to 2^-19 of the largest |q| of a block of 64 or    */
-/* 128 query rows), the weights of the sum over V with at least 7 bits         */
-/* (dtype bf16) or in float32 (dtype float32).                                 */
+/* products exactly (bf16 q to 2^-17 of the largest |q| of a block of 64 or    */
+/* 128 query rows), the weights of the sum over V with 9 bits down to 2^-17 of  */
+/* the largest and, for tree rows, as bf16 (dtype bf16), or in float32          */
+/* (dtype float32).                                                            */
 /* kv_len is clamped to [0, M*P].  Keys of a page that is not in               */
 /* [0, n_pages) or whose scale is not readable count as absent.  A row that    */
 /* sees no key is zero.  A row that sees a tree row with a non-finite V is     */

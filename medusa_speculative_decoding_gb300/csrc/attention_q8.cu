@@ -13,6 +13,8 @@
 //                                CTAs share (q8.cuh, Work)
 #include <float.h>
 
+#include <type_traits>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -68,7 +70,7 @@ struct SimpleSmem {
     static constexpr int kOffP = kOffQ + kRows * D * 4;
     static constexpr int kOffStat = kOffP + kRows * kKeys * 4;  // corr, m, l
     static constexpr int kOffFirst = kOffStat + 3 * kRows * 4;  // tile offsets
-    static int bytes(int B) { return kOffFirst + (B + 1) * 8; }
+    static int bytes(int B) { return kOffFirst + q8::offsets_bytes(B); }
 };
 
 template <typename T, int D>
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
     float* s_corr = reinterpret_cast<float*>(smem + L::kOffStat);
     float* s_m = s_corr + kRows;
     float* s_l = s_m + kRows;
-    long long* first = reinterpret_cast<long long*>(smem + L::kOffFirst);
+    const q8::Offsets first(smem + L::kOffFirst, a.work.B);
     __shared__ uint32_t s_seen[kKeys];  // rows that see the key, one bit each
     __shared__ int s_bad[kKeys];        // tree key whose V row holds an infinity or NaN
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -90,14 +92,14 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
     pdl_wait();
     pdl_trigger();
     q8::tile_offsets(w, a.kv_len, first);
-    const long long total = first[w.B];
+    const long long total = first.total(w);
     long long g = w.cta_begin(total, blockIdx.x);
     const long long g_end = w.cta_begin(total, blockIdx.x + 1);
     const int rows_all = w.N * a.G;
     constexpr int ACC = kRows * D / kSimpleThreads;  // output rows per thread (one column)
     const int d = tid % D, r0 = tid / D * ACC;
     while (g < g_end) {
-        const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+        const q8::Segment s = q8::segment_at(w, first, g, g_end);
         g += s.t1 - s.t0;
         const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * kRows;
         const int nrows = min(kRows, rows_all - row0);
@@ -256,12 +258,13 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 // Products on the 8-bit codes themselves.  The codes go from the page into the
 // matrix instruction as they are; what has more than e4m3's four significant
 // bits is split into planes that the instruction takes:
-//   scores   bf16 has 8 bits: q = q_hi + 2^-5 q_lo, two e4m3 planes under one
-//            power-of-two factor for the block, S = K q_hi + 2^-5 K q_lo; the
-//            page's scale multiplies S
-//   output   weight times V scale = p_hi + 2^-12 p_lo, p_hi in e4m3 and the rest
-//            in e5m2 (7 to 8 bits together), each plane summed on its own so that
-//            small weights keep their bits down to 2^-30 of the largest
+//   scores   bf16 has 8 bits: q = q_hi + q_lo, two e4m3 planes under one power of
+//            two for the block (exact down to 2^-17 of its largest |q|), both added
+//            into S = K q; the page's scale multiplies S
+//   output   weight times V scale = p_1 + p_2 + p_3, three e5m2 planes side by side
+//            in one product: 9 bits, for weights down to 2^-17 of the largest, and
+//            fewer from there to 2^-26 (e5m2 has the range that a softmax needs: with
+//            an attention sink the weights that count can be 2^-12 of the largest)
 // so no key or value is ever converted: converting them would cost more
 // instructions than the whole softmax of 64 rows, and twice the shared memory.
 //
@@ -274,15 +277,16 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 // reference it is held against (the first tile and few others), which one
 // barrier vote per tile finds out.
 //
-// Two streams per CTA (threads 0-127 and 128-255), each with its own S and O in
+// Two streams per CTA (four warps each, one per lane quarter), each with its own S and O in
 // TMEM, so that one stream's softmax runs while the other's products do:
 //   SHARED = false  blocks of NB rows; the streams take alternate tiles, each an
 //                   online softmax of its own, joined at the end
 //   SHARED = true   blocks of 2 NB rows; each stream has NB of them, both use
 //                   every tile
-// Steps x = 0, 1, 2, ...: stream x & 1, tile x (or x / 2).  For each x the MMA
-// lane issues PV(x), then S(x + 2); the commit of S of a stream's step therefore
-// covers its previous PV, and P and O are free when the scores arrive.
+// Steps x = 0, 1, 2, ...: stream x & 1, tile x (or x / 2).  When the weights of x
+// are written the MMA warp issues S(x + 2), if its keys are in, before PV(x): the
+// stream can go on with its next scores while PV(x) runs, and waits for that only
+// before it writes the next weights or rescales O.
 //
 // Warps 0-7 softmax, warp 8 MMA, warp 9 TMA (page tables, scales and tiles run
 // ahead through a ring of R slots; a slot is K and V of one tile of 128 keys).
@@ -291,12 +295,13 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 // Every wait is bounded; a CTA that gives up marks its results NaN.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;  // keys per tile
-constexpr int kUThreads = 320, kUSoftmax = 256, kUMmaWarp = 8, kUTmaWarp = 9;
+constexpr int kHalves = 1;               // warps that share a lane quarter of a stream
+constexpr int kUSoftmax = 256 * kHalves, kUThreads = kUSoftmax + 64;
+constexpr int kUMmaWarp = kUSoftmax / 32, kUTmaWarp = kUMmaWarp + 1;
+constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
 constexpr float kTau = 4.f;              // log2 by which weights may exceed 1
-constexpr float kPScale = 16.f;          // p_hi = weight * vs / v_ref * kPScale <= 256
+constexpr float kPScale = 2048.f;        // planes hold weight * vs / v_ref * kPScale <= 2^15
 constexpr float kVHead = 4.f;            // v_ref = kVHead * the largest V scale when set
-constexpr float kQLo = 0.03125f;         // 2^-5
-constexpr float kPLo = 1.f / 4096.f;     // 2^-12
 constexpr long long kDrainCycles = kDefaultWaitCycles;
 
 template <int D, int NB, bool SHARED>
@@ -308,22 +313,25 @@ struct USmem {
     static constexpr int kQB = NB * D * 2;                     // bf16, for the tree tiles
     static constexpr int kHalf = kTile * D;                    // K or V codes of a tile
     static constexpr int kSlot = 2 * kHalf;
-    static constexpr int kP = 2 * kTile * 64;                  // p_hi, p_lo (rows of 64 bytes)
+    static constexpr int kPlane = kTile * 64;                  // one plane of weights: rows of 64 bytes
+    static constexpr int kP = 3 * kPlane;
     static constexpr int kOffRing = 0;
     static constexpr int kOffP = kOffRing + kRing * kSlot;
     static constexpr int kOffQ8 = kOffP + 2 * kP;
     static constexpr int kOffQB = kOffQ8 + (kBlocks * kQ8 + 1023) / 1024 * 1024;
-    static constexpr int kOffM = kOffQB + (kBlocks * kQB + 1023) / 1024 * 1024;  // float m[2][NB]
+    static constexpr int kOffM = kOffQB + (kBlocks * kQB + 1023) / 1024 * 1024;  // float -m[2][NB], m = row reference
     static constexpr int kOffCorr = kOffM + 2 * NB * 4;        // float corr[2][NB], later coefficients
     static constexpr int kOffRed = kOffCorr + 2 * NB * 4;      // float red[2][4][NB]
-    static constexpr int kOffInfo = kOffRed + 8 * NB * 4;      // float2 (k, v scale)[kRing][8]
+    static constexpr int kOffRow = kOffRed + 8 * NB * 4;       // int [2 * NB]: (node, head) of a row, in rows of D
+    static constexpr int kOffMask = kOffRow + 2 * NB * 4;      // uint32 [kRowsBlock][16]: mask rows
+    static constexpr int kOffInfo = kOffMask + kRowsBlock * 64;  // float2 (k, v scale)[kRing][8]
     static constexpr int kOffBad = kOffInfo + kRing * 8 * 8;   // uint32 [16]: tree rows with a non-finite V
-    static constexpr int kOffMisc = kOffBad + 64;              // see below, 128 bytes
-    static constexpr int kOffBar = kOffMisc + 128;
-    // full[R] empty[R] s_full[2] p_full[2] o_done[2] qfull drain
+    static constexpr int kOffMisc = kOffBad + 64;              // see below, 256 bytes
+    static constexpr int kOffBar = kOffMisc + 256;
+    // full[R] empty[R] s_full[2] p_full[2] pv_done[2] qfull drain
     static constexpr int kNumBar = 2 * kRing + 8;
     static constexpr int kOffFirst = (kOffBar + kNumBar * 8 + 15) / 16 * 16;
-    static int bytes(int B) { return kOffFirst + (B + 1) * 8 + 1024; }  // + alignment slack
+    static int bytes(int B) { return kOffFirst + q8::offsets_bytes(B) + 1024; }  // + alignment slack
 };
 
 __device__ __forceinline__ float redux_max(float v) {
@@ -331,7 +339,18 @@ __device__ __forceinline__ float redux_max(float v) {
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// (the barrier takes whole warps in step: lanes that left a wait or a branch at
+// different times meet first)
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// All lanes wait; the same answer in all of them.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long lim) {
+    const bool ok = umma::mbar_wait(bar, parity, lim);
+    __syncwarp();
+    return __all_sync(0xffffffffu, ok);
+}
 // pairs of floats on the paired float32 pipe
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
     asm("{\n.reg .b64 ra, rb, rc, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\nmov.b64 rc, {%5, %6};\n"
@@ -358,19 +377,25 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Two weights (times V scale) into their e4m3 and e5m2 planes.  The pair passes
-// through f16 (11 bits), where hi and the rest it leaves are exact.
-__device__ __forceinline__ void split_weights(float a, float b, uint16_t& hi, uint16_t& lo) {
-    asm("{\n.reg .b32 x, h, r, k;\n.reg .b16 c;\n"
-        "cvt.rn.f16x2.f32 x, %3, %2;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 c, x;\n"
-        "mov.b16 %0, c;\n"
-        "cvt.rn.f16x2.e4m3x2 h, c;\n"
-        "sub.rn.f16x2 r, x, h;\n"
-        "mov.b32 k, 0x6c006c00;\n"  // 2^12, 2^12
-        "mul.rn.f16x2 r, r, k;\n"
-        "cvt.rn.satfinite.e5m2x2.f16x2 %1, r;\n}"
-        : "=h"(hi), "=h"(lo) : "f"(a), "f"(b));
+// Two weights (times V scale) into their planes.  e5m2 is the upper byte of f16,
+// so a plane is the f16 value rounded to that byte (adding half a step; the sign is
+// apart, so this rounds magnitudes), and what it leaves is exact in f16.  Returns
+// the three planes' values in the upper bytes of each half.
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t (&plane)[3]) {
+    uint32_t x;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(b), "f"(a));
+    plane[0] = (x + 0x00800080u) & 0xff00ff00u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(plane[0]));
+    plane[1] = (x + 0x00800080u) & 0xff00ff00u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(plane[1]));
+    plane[2] = x + 0x00800080u;
+}
+__device__ __forceinline__ bool not_finite(const uint4& v) {  // any of eight bf16 values
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad = bad || (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+    return bad;
 }
 __device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) { return (uint32_t)lo | (uint32_t)hi << 16; }
 
@@ -381,10 +406,10 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     using namespace umma;
     using L = USmem<D, NB, SHARED>;
     constexpr int R = L::kRing;
-    constexpr int kCols = NB == 64 ? 512 : 128;      // TMEM columns: S[2], O[2] of 2 NB each
-    constexpr uint32_t kS = 0, kO = 4 * NB;          // S_s at 2 NB s; O_s at 4 NB + 2 NB s
+    constexpr int kCols = NB == 64 ? 512 : 128;      // TMEM columns
+    constexpr uint32_t kS = 0, kO = 2 * NB;          // S_s at NB s; O_s (three planes) at 2 NB + 3 NB s
     extern __shared__ uint8_t smem_raw[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const q8::Work w = a.work;
 
     const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
@@ -394,26 +419,28 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                    qb_a = base_a + L::kOffQB;
     const uint32_t bar_a = base_a + L::kOffBar;
     const uint32_t full0 = bar_a, empty0 = full0 + 8 * R, s_full0 = empty0 + 8 * R, p_full0 = s_full0 + 16,
-                   o_done0 = p_full0 + 16, qfull = o_done0 + 16, drain = qfull + 8;
+                   pv_done0 = p_full0 + 16, qfull = pv_done0 + 16, drain = qfull + 8;
     float* s_m = reinterpret_cast<float*>(base + L::kOffM);
     float* s_corr = reinterpret_cast<float*>(base + L::kOffCorr);
     float* s_red = reinterpret_cast<float*>(base + L::kOffRed);
     float2* s_info = reinterpret_cast<float2*>(base + L::kOffInfo);
     uint32_t* s_bad = reinterpret_cast<uint32_t*>(base + L::kOffBad);
+    int* s_row = reinterpret_cast<int*>(base + L::kOffRow);
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(base + L::kOffMask);
     float* s_misc = reinterpret_cast<float*>(base + L::kOffMisc);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_misc);
     volatile int* flag = reinterpret_cast<volatile int*>(s_misc + 1);      // a wait gave up
     volatile int* s_fail = reinterpret_cast<volatile int*>(s_misc + 2);    // [2] per stream
-    float* s_qmax = s_misc + 4;                                            // [8] per warp
-    float* s_vmax = s_misc + 12;                                           // [2][4] largest V scale per warp
-    float* s_vref = s_misc + 20;                                           // [2] at the end of a segment
-    long long* first = reinterpret_cast<long long*>(base + L::kOffFirst);
+    float* s_qmax = s_misc + 4;                                            // [kUSoftmax / 32] per warp
+    float* s_vmax = s_misc + 20;                                           // [2][4] largest V scale per quarter
+    float* s_vref = s_misc + 28;                                           // [2] at the end of a segment
+    const q8::Offsets first(base + L::kOffFirst, w.B);
     const long long lim = g_wait_limit;
 
     if (warp == kUTmaWarp && lane == 0) {
         for (int i = 0; i < L::kNumBar; ++i) mbar_init(bar_a + 8 * i, 1);
-        mbar_init(p_full0, 4);
-        mbar_init(p_full0 + 8, 4);
+        mbar_init(p_full0, kUStream / 32);
+        mbar_init(p_full0 + 8, kUStream / 32);
         mbar_init(qfull, kUSoftmax / 32);
         mbar_init_fence();
         *flag = 0;
@@ -431,7 +458,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const long long total = first[w.B];
+    const long long total = first.total(w);
     const long long g_begin = w.cta_begin(total, blockIdx.x), g_end = w.cta_begin(total, blockIdx.x + 1);
     const int ppt = kTile / a.P;  // pages per tile
     const int rows_all = w.N * a.G;
@@ -446,16 +473,17 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     };
 
     if (warp == kUMmaWarp) {
-        // -------------------------------- MMA lane --------------------------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f8(128, 2 * NB, 0, 0, 0, 0);
-            constexpr uint32_t id_hi = idesc_f8(128, NB, 0, 0, 1, 1), id_lo = idesc_f8(128, NB, 0, 1, 1, 1);
+        // -------------------------------- MMA warp --------------------------------
+        {
+            constexpr uint32_t id_s = idesc_f8(128, NB, 0, 0, 0, 0), id_pv = idesc_f8(128, 3 * NB, 0, 1, 1, 1);
             constexpr uint32_t id_st = idesc_bf16(128, NB, 0, 0), id_pt = idesc_bf16(128, NB, 1, 1);
             bool fail = false;
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (fail) return false;
-                if (!mbar_wait(bar, parity, lim)) { fail = true; *flag = 1; return false; }
-                return true;
+                if (!fail && !warp_wait(bar, parity, lim)) {
+                    fail = true;
+                    *flag = 1;
+                }
+                return !fail;
             };
             auto desc8 = [](uint32_t addr) {  // codes: rows of D bytes, either major
                 return D == 128 ? desc_sw128(addr, 16, 1024) : desc_sw64(addr, 0, 512);
@@ -464,10 +492,13 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             int n_p[2] = {0, 0};     // steps of each stream so far
             int seg = 0;
             for (long long g = g_begin; g < g_end && !fail; ++seg) {
-                const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+                const q8::Segment s = q8::segment_at(w, first, g, g_end);
                 g += s.t1 - s.t0;
                 int n_pre, n_tree;
                 prefix_of(s, n_pre, n_tree);
+                // (the shuffles tell the compiler that these are the same in all lanes)
+                n_pre = __shfl_sync(0xffffffffu, n_pre, 0);
+                n_tree = __shfl_sync(0xffffffffu, n_tree, 0);
                 const int steps = (n_pre + n_tree) * (SHARED ? 2 : 1);
                 auto tile_of = [&](int x) { return SHARED ? x >> 1 : x; };
                 auto slot_of = [&](int t) { return slot0 + t + max(0, t - n_pre); };
@@ -475,32 +506,34 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     const int t = tile_of(x), sl = slot_of(t), st = x & 1, blk = SHARED ? st : 0;
                     if (!wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1))) return;
                     fence_after_sync();
-                    const uint32_t k = ring_a + (sl % R) * L::kSlot, d = tmem + kS + st * 2 * NB;
+                    const uint32_t k = ring_a + (sl % R) * L::kSlot, d = tmem + kS + st * NB;
                     if (t < n_pre) {
                         const uint64_t dk = desc8(k), dq = desc8(q8_a + blk * L::kQ8);
 #pragma unroll
-                        for (int ks = 0; ks < D / 32; ++ks) mma_f8(d, dk + 2 * ks, dq + 2 * ks, id_s, ks > 0);
+                        for (int ks = 0; ks < D / 32; ++ks) {
+                            mma_f8_warp(d, dk + 2 * ks, dq + 2 * ks, id_s, ks > 0);
+                            mma_f8_warp(d, dk + 2 * ks, dq + ((NB * D) >> 4) + 2 * ks, id_s, 1);
+                        }
                     } else {
                         const uint64_t dk = desc_sw128(k, 16, 1024), dq = desc_sw128(qb_a + blk * L::kQB, 16, 1024);
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
-                            mma_bf16(d, dk + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
+                            mma_bf16_warp(d, dk + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
                                      dq + (((ks >> 2) * (NB * 128) + (ks & 3) * 32) >> 4), id_st, ks > 0);
                     }
-                    commit(s_full0 + 8 * st);
+                    commit_warp(s_full0 + 8 * st);
                 };
                 auto issue_pv = [&](int x) {
                     const int t = tile_of(x), sl = slot_of(t), st = x & 1, i = x >> 1;
-                    const uint32_t d = tmem + kO + st * 2 * NB, p = p_a + st * L::kP;
+                    const uint32_t d = tmem + kO + st * 3 * NB, p = p_a + st * L::kP;
                     if (t < n_pre) {
                         const uint64_t dv = desc8(ring_a + (sl % R) * L::kSlot + L::kHalf);
-                        const uint64_t dh = desc_sw64(p, 0, 512), dl = desc_sw64(p + kTile * 64, 0, 512);
+                        // NB = 64: a plane is one swizzle atom wide, the next one a plane behind;
+                        // NB = 16: the planes share the 64 bytes of a key
+                        const uint64_t dp = desc_sw64(p, L::kPlane, 512);
 #pragma unroll
                         for (int ks = 0; ks < kTile / 32; ++ks)
-                            mma_f8(d, dv + ((ks * 32 * D) >> 4), dh + ((ks * 2048) >> 4), id_hi, i > 0 || ks > 0);
-#pragma unroll
-                        for (int ks = 0; ks < kTile / 32; ++ks)
-                            mma_f8(d + NB, dv + ((ks * 32 * D) >> 4), dl + ((ks * 2048) >> 4), id_lo, i > 0 || ks > 0);
+                            mma_f8_warp(d, dv + ((ks * 32 * D) >> 4), dp + ((ks * 2048) >> 4), id_pv, i > 0 || ks > 0);
                     } else {
                         const int sv = sl + 1;
                         if (!wait(full0 + 8 * (sv % R), (uint32_t)((sv / R) & 1))) return;
@@ -509,12 +542,12 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         const uint64_t dp = desc_sw128(p, 0, 1024);
 #pragma unroll
                         for (int ks = 0; ks < kTile / 16; ++ks)
-                            mma_bf16(d, dv + ((ks * 2048) >> 4), dp + ((ks * 2048) >> 4), id_pt, i > 0 || ks > 0);
+                            mma_bf16_warp(d, dv + ((ks * 2048) >> 4), dp + ((ks * 2048) >> 4), id_pt, i > 0 || ks > 0);
                     }
-                    if (x + 2 >= steps) commit(o_done0 + 8 * st);  // the stream's last
+                    commit_warp(pv_done0 + 8 * st);
                     if (!SHARED || st == 1) {
-                        commit(empty0 + 8 * (sl % R));
-                        if (t >= n_pre) commit(empty0 + 8 * ((sl + 1) % R));
+                        commit_warp(empty0 + 8 * (sl % R));
+                        if (t >= n_pre) commit_warp(empty0 + 8 * ((sl + 1) % R));
                     }
                 };
                 if (!wait(qfull, (uint32_t)(seg & 1))) break;
@@ -523,15 +556,22 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     const int st = x & 1;
                     if (!wait(p_full0 + 8 * st, (uint32_t)((n_p[st] + (x >> 1)) & 1))) break;
                     fence_after_sync();
+                    // keys that are not in yet must not hold up PV(x), which frees their slot
+                    bool s_first = false;
+                    if (x + 2 < steps) {
+                        const int sl = slot_of(tile_of(x + 2));
+                        s_first = __all_sync(0xffffffffu, mbar_try(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1)));
+                    }
+                    if (s_first) issue_s(x + 2);
                     issue_pv(x);
-                    if (x + 2 < steps && !fail) issue_s(x + 2);
+                    if (!s_first && x + 2 < steps && !fail) issue_s(x + 2);
                 }
                 n_p[0] += (steps + 1) >> 1;
                 n_p[1] += steps >> 1;
                 slot0 += n_pre + 2 * n_tree;
             }
             if (fail) {  // let everything in flight complete before TMEM is freed
-                commit(drain);
+                commit_warp(drain);
                 mbar_wait(drain, 0, kDrainCycles);
             }
         }
@@ -540,12 +580,11 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         int slot = 0;
         bool fail = false;
         auto free_slot = [&](int sl) {
-            if (sl >= R && !mbar_wait(empty0 + 8 * (sl % R), (uint32_t)((sl / R - 1) & 1), lim)) fail = true;
-            fail = __any_sync(0xffffffffu, fail);
+            if (sl >= R && !warp_wait(empty0 + 8 * (sl % R), (uint32_t)((sl / R - 1) & 1), lim)) fail = true;
             return !fail;
         };
         for (long long g = g_begin; g < g_end && !fail;) {
-            const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+            const q8::Segment s = q8::segment_at(w, first, g, g_end);
             g += s.t1 - s.t0;
             int n_pre, n_tree;
             prefix_of(s, n_pre, n_tree);
@@ -613,21 +652,24 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     mbar_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), kDrainCycles);
             }
         }
-    } else {
+    } else if (warp < kUMmaWarp) {
         // ------------------------------ softmax warps ------------------------------
-        const int st = warp >> 2, quarter = warp & 3;
+        constexpr int CW = NB / kHalves;  // rows (columns of S^T) per thread
+        const int st = warp / (4 * kHalves), half = (warp >> 2) % kHalves, quarter = warp & 3;
         const int key = quarter * 32 + lane;  // TMEM lane: key of a tile, then output column
+        const int stid = tid & (kUStream - 1);
+        const int page_shift = 31 - __clz(a.P);
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lane_off + kS + st * 2 * NB, tO = tmem + lane_off + kO + st * 2 * NB;
-        float* m_row = s_m + st * NB;
+        const uint32_t tS = tmem + lane_off + kS + st * NB + half * CW;
+        const uint32_t tO = tmem + lane_off + kO + st * 3 * NB + half * CW;
+        float* m_row = s_m + st * NB;  // negated
         float* corr_row = s_corr + st * NB;
         uint8_t* p_row = base + L::kOffP + st * L::kP;
         const float scale = a.scale_log2;
         int n_s = 0;       // steps of this stream before the segment
-        int n_o = 0;       // segments in which it had any
         int slot0 = 0;
         for (long long g = g_begin; g < g_end;) {
-            const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+            const q8::Segment s = q8::segment_at(w, first, g, g_end);
             const long long g_seg = g;
             g += s.t1 - s.t0;
             int n_pre, n_tree;
@@ -639,9 +681,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 
             // Q into shared memory: bf16 for the tree's tiles, two e4m3 planes for the
             // pages'.  Rows behind the block's end are zero.
-            constexpr int CH = D / 8, QCH = L::kRowsBlock * CH / kUSoftmax;
-            static_assert(L::kRowsBlock * CH % kUSoftmax == 0 || L::kRowsBlock * CH < kUSoftmax, "whole passes over Q");
-            constexpr int QN = QCH ? QCH : 1;
+            constexpr int CH = D / 8, QN = (L::kRowsBlock * CH + kUSoftmax - 1) / kUSoftmax;
             uint4 qv[QN];
             float qmax = 0.f;
 #pragma unroll
@@ -653,6 +693,17 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     qv[i] = ld_stream16(static_cast<const uint16_t*>(a.q) +
                                         (((size_t)s.b * w.N + gr / a.G) * a.Hq + hk * a.G + gr % a.G) * D + c % CH * 8);
                 }
+            }
+            if (n_tree) {
+                const uint32_t* mask = reinterpret_cast<const uint32_t*>(a.mask);
+                for (int i = tid; i < L::kRowsBlock * 16; i += kUSoftmax) {
+                    const int r = i >> 4, word = i & 15;
+                    if (word < 2 * a.W) s_mask[i] = r < nrows ? __ldg(mask + (size_t)((row0 + r) / a.G) * (2 * a.W) + word) : 0u;
+                }
+                if (SHARED && tid < 16) s_bad[tid] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < QN; ++i) {
                 const uint32_t x[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -661,27 +712,14 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     if (f1 < INFINITY) qmax = fmaxf(qmax, f1);
                 }
             }
-            // tree rows whose V is not finite: 0 * inf of a row that does not see them
-            // would spoil that row, so their V counts as zero and rows that see them get NaN
-            if (n_tree) {
-                if (tid < 16) s_bad[tid] = 0;
-                bar_sync(3, kUSoftmax);
-                for (int c = tid; c < w.N * CH; c += kUSoftmax) {
-                    const int m = c / CH;
-                    const uint4 v = ld_stream16(static_cast<const uint16_t*>(a.v_tree) +
-                                                (((size_t)s.b * w.N + m) * a.Hkv + hk) * D + c % CH * 8);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    bool bad = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        bad = bad || (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
-                    if (bad) atomicOr(&s_bad[m >> 5], 1u << (m & 31));
-                }
-            }
             qmax = redux_max(qmax);
             if (lane == 0) s_qmax[warp] = qmax;
-            if (key < NB) m_row[key] = -INFINITY;
-            bar_sync(3, kUSoftmax);  // the last segment's sums are read, its Q is free
+            if (stid < NB) m_row[stid] = INFINITY;
+            bar_sync(3, kUSoftmax);  // the last segment's results are out, its Q is free
+            if (tid < L::kRowsBlock) {
+                const int gr = row0 + tid;
+                s_row[tid] = gr / a.G * a.Hq + hk * a.G + gr % a.G;
+            }
 #pragma unroll
             for (int i = 0; i < kUSoftmax / 32; ++i) qmax = fmaxf(qmax, s_qmax[i]);
             // factor 2^k with qmax * 2^k in [128, 256)
@@ -702,7 +740,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     if (!(fabsf(f1) < INFINITY)) f1 = NAN;
                     hi[e] = q8::float2_to_e4m3x2(f0, f1);
                     const float2 h = q8::e4m3x2_to_float2(hi[e]);
-                    lo[e] = q8::float2_to_e4m3x2((f0 - h.x) * 32.f, (f1 - h.y) * 32.f);
+                    lo[e] = q8::float2_to_e4m3x2(f0 - h.x, f1 - h.y);
                 }
                 uint8_t* q8p = base + L::kOffQ8 + blk * L::kQ8;
                 auto at8 = [&](int row) {  // 8 bytes of chunk ch of a row of D codes
@@ -718,186 +756,264 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
+            // Tree rows whose V is not finite: 0 * inf of a row that does not see them
+            // would spoil that row, so their V counts as zero and rows that see them get
+            // NaN.  Split streams look at their tile; shared ones, where one stream may
+            // clear what the other has still to look at, look ahead here.
+            if (SHARED && n_tree) {
+#pragma unroll 4
+                for (int c = tid; c < w.N * CH; c += kUSoftmax) {
+                    const int m = c / CH;
+                    const uint4 v = ld_stream16(static_cast<const uint16_t*>(a.v_tree) +
+                                                (((size_t)s.b * w.N + m) * a.Hkv + hk) * D + c % CH * 8);
+                    if (not_finite(v)) atomicOr(&s_bad[m >> 5], 1u << (m & 31));
+                }
+                bar_sync(3, kUSoftmax);
+            }
 
-            float l[NB];
+            float l[CW];
 #pragma unroll
-            for (int c = 0; c < NB; ++c) l[c] = 0.f;
+            for (int c = 0; c < CW; ++c) l[c] = 0.f;
             float v_ref = 0.f;
-            bool fail = false;
+            bool fail = false, late = false;
             const int pt = w.prefix_tiles(s.L);
-            for (int i = 0; i < steps; ++i) {
+            // One step; false: a wait gave up.  The tree's tiles have a body of their own,
+            // which keeps their bookkeeping out of the prefix's registers.
+            auto step = [&](auto is_tree, const int i) -> bool {
+                constexpr bool tree = decltype(is_tree)::value;
                 const int t = SHARED ? i : 2 * i + st;
-                const int sl = slot0 + t + max(0, t - n_pre);
-                const bool tree = t >= n_pre;
-                bool ok = mbar_wait(s_full0 + 8 * st, (uint32_t)((n_s + i) & 1), lim);
+                const int sl = slot0 + t + (tree ? t - n_pre : 0);
+                bool ok = warp_wait(s_full0 + 8 * st, (uint32_t)((n_s + i) & 1), lim);
                 float kc = kq, vs = 1.f;
-                uint32_t seen_lo = 0xffffffffu, seen_hi = 0xffffffffu;  // rows that see the key
-                bool valid = true, bad_v = false;
-                if (!tree) {
+                bool valid, bad_v = false;
+                if constexpr (!tree) {
                     // the slot is in since the scores are; this wait makes the scales visible
-                    ok = mbar_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), lim) && ok;
-                    const float2 sc = s_info[(sl % R) * 8 + key / a.P];
+                    ok = warp_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), lim) && ok;
+                    const float2 sc = s_info[(sl % R) * 8 + (key >> page_shift)];
                     valid = sc.y > 0.f && (s.t0 + t) * kTile + key < s.L;
-                    kc = valid ? kq * sc.x : 0.f;
+                    kc = kq * sc.x;
                     vs = valid ? sc.y : 0.f;
                 } else {
                     kc = scale;
+                    ok = warp_wait(full0 + 8 * ((sl + 1) % R), (uint32_t)(((sl + 1) / R) & 1), lim) && ok;
                     const int m = (s.t0 + t - pt) * kTile + key;  // tree row
                     valid = m < w.N;
-                    seen_lo = seen_hi = 0;
-                    // bit c: row c of this stream's block sees tree row m (all lanes of a
-                    // warp read the same word)
-                    const int r_first = row0 + (SHARED ? st * NB : 0);
-                    if ((m & ~31) < w.N)
-                        for (int c = 0; c < NB && r_first + c < rows_all; ++c) {
-                            const uint64_t word = __ldg(a.mask + (size_t)((r_first + c) / a.G) * a.W + (m >> 6));
-                            const uint32_t bit = valid ? (uint32_t)(word >> (m & 63)) & 1u : 0u;
-                            if (c < 32) seen_lo |= bit << c; else seen_hi |= bit << (c - 32);
-                        }
-                    bad_v = valid && (s_bad[m >> 5] >> (m & 31) & 1);
-                    if (__any_sync(0xffffffffu, bad_v))
-                        ok = mbar_wait(full0 + 8 * ((sl + 1) % R), (uint32_t)(((sl + 1) / R) & 1), lim) && ok;
+                    if constexpr (SHARED) {
+                        bad_v = valid && (s_bad[m >> 5] >> (m & 31) & 1);
+                    } else {
+                        const uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; ++c)
+                            bad_v = not_finite(*reinterpret_cast<const uint4*>(v + (c >> 3) * kTile * 128 +
+                                                                               (((c + lane) & 7) << 4))) || bad_v;
+                    }
                 }
-                ok = __all_sync(0xffffffffu, ok);
                 fence_after_sync();
-                if (!ok && lane == 0) s_fail[st] = 1;
+                if ((!ok || late) && lane == 0) s_fail[st] = 1;
+                // rows of columns c0 .. c0 + 7 that see the key: all, but for the tree's keys
+                auto seen8 = [&](int c0) -> uint32_t {
+                    uint32_t seen = 0xffu;
+                    if constexpr (tree) {
+                        seen = 0;
+                        const int m0 = (s.t0 + t - pt) * kTile + quarter * 32;
+                        const uint32_t* words = s_mask + ((SHARED ? st * NB : 0) + half * CW + c0) * 16 + (m0 >> 5);
+                        if (m0 < w.N) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) seen |= ((words[c * 16] >> lane) & 1u) << c;
+                        }
+                    }
+                    return valid ? seen : 0u;
+                };
+                // Eight columns of scores from c0 on, in log2 units, less the rows'
+                // references or as they are.
+                auto scores8 = [&](int c0, bool relative, float* x) {
+                    float y[8];
+                    tmem_ld8(tS + c0, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (relative) m = *reinterpret_cast<const float4*>(m_row + half * CW + c0 + e);
+                        fma2(x[e], x[e + 1], y[e], y[e + 1], kc, m.x, m.y);
+                        fma2(x[e + 2], x[e + 3], y[e + 2], y[e + 3], kc, m.z, m.w);
+                    }
+                };
+                const bool partial = tree || __any_sync(0xffffffffu, !valid);
+                // The scores are formed twice from TMEM, for the check and for the weights, WX
+                // columns at a time: held in between they would not fit next to the sums, and
+                // what the compiler then spills does not fit L1 next to this much shared memory.
+                constexpr int WX = tree ? 8 : (CW < 16 ? CW : 16);
+                float x[WX];
+                auto load_x = [&](int c0) {
+                    if constexpr (WX == 32)
+                        tmem_ld32(tS + c0, x);
+                    else if constexpr (WX == 16)
+                        tmem_ld16(tS + c0, x);
+                    else
+                        tmem_ld8(tS + c0, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < WX; e += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(m_row + half * CW + c0 + e);
+                        fma2(x[e], x[e + 1], x[e], x[e + 1], kc, m.x, m.y);
+                        fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], kc, m.z, m.w);
+                    }
+                    if (partial) {
+#pragma unroll
+                        for (int e = 0; e < WX; ++e) x[e] = valid ? x[e] : -INFINITY;
+                    }
+                };
+                bool move = !ok || late || i == 0 || vs > v_ref;
+                // (i, not move, decides here: TMEM loads take whole warps)
+                {
+                    if (i > 0) {
+                        float top = -INFINITY;
+                        if constexpr (!tree) {
+#pragma unroll
+                            for (int c0 = 0; c0 < CW; c0 += WX) {
+                                load_x(c0);
+#pragma unroll
+                                for (int e = 0; e < WX; e += 2) top = max3(top, x[e], x[e + 1]);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int c0 = 0; c0 < CW; c0 += 8) {
+                                scores8(c0, true, x);
+                                const uint32_t seen = seen8(c0);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) top = fmaxf(top, (seen >> e) & 1 ? x[e] : -INFINITY);
+                            }
+                        }
+                        move = move || top > kTau;
+                    }
+                    __syncwarp();
+                }
+                if (named_barrier_or(1 + st, kUStream, move)) {
+                    // The references move: largest score per row over the tile's keys.
+#pragma unroll 1
+                    for (int c0 = 0; c0 < CW; c0 += 8) {
+                        float y[8];
+                        scores8(c0, false, y);
+                        const uint32_t seen = seen8(c0);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float m = redux_max((seen >> e) & 1 ? y[e] : -INFINITY);
+                            if (lane == e) s_red[(st * 4 + quarter) * NB + half * CW + c0 + e] = m;
+                        }
+                    }
+                    const float vm = redux_max(vs);
+                    if (lane == 0) s_vmax[st * 4 + quarter] = vm;
+                    // the stream's last PV: O is free behind it
+                    if (i > 0 && !warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + i - 1) & 1), lim)) s_fail[st] = 1;
+                    bar_sync(1 + st, kUStream);
+                    const bool fail = s_fail[st] != 0;
+                    if (stid < NB) {
+                        const float* r = s_red + st * 4 * NB + stid;
+                        const float m0 = -m_row[stid];
+                        const float m1 = fmaxf(max3(r[0], r[NB], r[2 * NB]), fmaxf(r[3 * NB], m0));
+                        corr_row[stid] = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);
+                        m_row[stid] = -m1;
+                    }
+                    float v1 = fmaxf(fmaxf(s_vmax[st * 4], s_vmax[st * 4 + 1]), fmaxf(s_vmax[st * 4 + 2], s_vmax[st * 4 + 3]));
+                    v1 = v1 > v_ref ? v1 * kVHead : v_ref;
+                    const float vf = v1 > 0.f ? v_ref / v1 : 0.f;
+                    v_ref = v1;
+                    bar_sync(1 + st, kUStream);
+                    if (fail) return false;
+                    if (i > 0) {  // what was added up so far
+#pragma unroll
+                        for (int c = 0; c < CW; c += 4) {
+                            const float4 r = *reinterpret_cast<const float4*>(corr_row + half * CW + c);
+                            l[c] *= r.x; l[c + 1] *= r.y; l[c + 2] *= r.z; l[c + 3] *= r.w;
+                        }
+                        fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < CW; c += 8) {
+                            float o[3][8];
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) tmem_ld8(tO + p * NB + c, o[p]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                uint32_t ow[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) ow[e] = __float_as_uint(o[p][e] * (corr_row[half * CW + c + e] * vf));
+                                tmem_st8(tO + p * NB + c, ow);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // the stream's last PV: P is free behind it
+                if (i > 0) late = !warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + i - 1) & 1), lim);
                 // A key that is not there has no V either: whatever the slot holds (stale
                 // codes may be NaN) is cleared.  When two streams share the tile, stream 0
                 // does it: its PV comes first.
-                if (!SHARED || st == 0) {
+                if (half == 0 && (!SHARED || st == 0)) {
                     if (!tree && !valid) {
                         uint4* v = reinterpret_cast<uint4*>(base + L::kOffRing + (sl % R) * L::kSlot + L::kHalf + key * D);
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
                     }
                     if (bad_v) {
-#pragma unroll
-                        for (int x = 0; x < D / 64; ++x) {
-                            uint4* v = reinterpret_cast<uint4*>(base + L::kOffRing + ((sl + 1) % R) * L::kSlot +
-                                                                x * kTile * 128 + key * 128);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                }
-
-                // scores in log2 units above the rows' references
-                float t2[NB];
-                auto load_scores = [&](bool relative) {
-#pragma unroll
-                    for (int c0 = 0; c0 < NB; c0 += 16) {
-                        float hi[16], lo[16];
-                        tmem_ld16(tS + c0, hi);
-                        tmem_ld16(tS + NB + c0, lo);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float x0 = hi[e], x1 = hi[e + 1];
-                            if (!tree) fma2(x0, x1, lo[e], lo[e + 1], kQLo, x0, x1);
-                            float m0 = 0.f, m1 = 0.f;
-                            if (relative) {
-                                const float2 mm = *reinterpret_cast<const float2*>(m_row + c0 + e);
-                                m0 = -mm.x; m1 = -mm.y;
-                            }
-                            fma2(t2[c0 + e], t2[c0 + e + 1], x0, x1, kc, m0, m1);
-                        }
-                    }
-                    if (tree || !valid) {
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) {
-                            const bool see = valid && ((c < 32 ? seen_lo >> c : seen_hi >> (c - 32)) & 1);
-                            t2[c] = see ? t2[c] : -INFINITY;
-                        }
-                    }
-                };
-                load_scores(true);
-                float top = t2[0];
-#pragma unroll
-                for (int c = 1; c + 1 < NB; c += 2) top = max3(top, t2[c], t2[c + 1]);
-                top = fmaxf(top, t2[NB - 1]);
-                if (named_barrier_or(1 + st, 128, !ok || top > kTau || vs > v_ref)) {
-                    // the references move: largest score per row over the tile's keys
-                    load_scores(false);
-#pragma unroll
-                    for (int c = 0; c < NB; ++c) {
-                        const float m = redux_max(t2[c]);
-                        if (lane == (c & 31)) s_red[(st * 4 + quarter) * NB + c] = m;
-                    }
-                    const float vm = redux_max(vs);
-                    if (lane == 0) s_vmax[st * 4 + quarter] = vm;
-                    bar_sync(1 + st, 128);
-                    if (s_fail[st]) { fail = true; }
-                    if (key < NB) {
-                        const float* r = s_red + st * 4 * NB + key;
-                        const float m0 = m_row[key];
-                        const float m1 = fmaxf(fmaxf(fmaxf(r[0], r[NB]), fmaxf(r[2 * NB], r[3 * NB])), m0);
-                        corr_row[key] = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);
-                        m_row[key] = m1;
-                    }
-                    float v1 = fmaxf(fmaxf(s_vmax[st * 4], s_vmax[st * 4 + 1]), fmaxf(s_vmax[st * 4 + 2], s_vmax[st * 4 + 3]));
-                    v1 = v1 > v_ref ? v1 * kVHead : v_ref;
-                    const float vf = v1 > 0.f ? v_ref / v1 : 0.f;
-                    v_ref = v1;
-                    bar_sync(1 + st, 128);
-                    if (fail) break;
-#pragma unroll
-                    for (int c = 0; c < NB; ++c) l[c] *= corr_row[c];
-                    if (i > 0) {  // O holds the earlier tiles: their PV preceded these scores
+                        uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
 #pragma unroll 1
-                        for (int c0 = 0; c0 < 2 * NB; c0 += 16) {
-                            float o[16];
-                            tmem_ld16(tO + c0, o);
-                            tmem_wait_ld();
-                            const float* cr = corr_row + (c0 & (NB - 1));
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= cr[e] * vf;
-                            tmem_st16(tO + c0, o);
-                        }
-                        tmem_wait_st();
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4*>(v + (c >> 3) * kTile * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     }
-                    load_scores(true);
                 }
+                __syncwarp();
                 // weights, their sums, and their planes
                 const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
-                if (!tree) {
+                if constexpr (!tree) {
+                    constexpr int W = CW < 16 ? CW : 16;
 #pragma unroll
-                    for (int c0 = 0; c0 < NB; c0 += 16) {
-                        uint32_t h[4], lw[4];
+                    for (int c0 = 0; c0 < CW; c0 += W) {
+                        if (c0 % WX == 0) load_x(c0);
+                        uint32_t pw[3][W / 4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint16_t hh[2], ll[2];
+                        for (int e = 0; e < W / 4; ++e) {
+                            uint32_t two[2][3];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const int c = c0 + 4 * e + 2 * k;
-                                const float p0 = exp2_approx(t2[c]), p1 = exp2_approx(t2[c + 1]);
+                                const float p0 = exp2_approx(x[c % WX]), p1 = exp2_approx(x[c % WX + 1]);
                                 add2(l[c], l[c + 1], p0, p1);
                                 float w0, w1;
                                 mul2(w0, w1, p0, p1, f);
-                                split_weights(w0, w1, hh[k], ll[k]);
+                                split_weights(w0, w1, two[k]);
                             }
-                            h[e] = join16(hh[0], hh[1]);
-                            lw[e] = join16(ll[0], ll[1]);
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) pw[p][e] = __byte_perm(two[0][p], two[1][p], 0x7531);
                         }
-                        const int off = key * 64 + (((c0 >> 4) ^ ((key >> 1) & 3)) << 4);
-                        *reinterpret_cast<uint4*>(p_row + off) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4*>(p_row + kTile * 64 + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                        const int col = half * CW + c0;
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) {
+                            // NB = 64: one plane of 64 bytes a key after the other; NB = 16:
+                            // the planes are the key's 16-byte chunks 0, 1, 2
+                            const int chunk = NB == 64 ? col >> 4 : p;
+                            uint8_t* to = p_row + (NB == 64 ? p * L::kPlane : 0) + key * 64 +
+                                          ((chunk ^ ((key >> 1) & 3)) << 4) + (col & 15);
+                            if constexpr (W == 16)
+                                *reinterpret_cast<uint4*>(to) = make_uint4(pw[p][0], pw[p][1], pw[p][2], pw[p][3]);
+                            else
+                                *reinterpret_cast<uint2*>(to) = make_uint2(pw[p][0], pw[p][1]);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int c0 = 0; c0 < NB; c0 += 8) {
+                    for (int c0 = 0; c0 < CW; c0 += 8) {
                         uint32_t h[4];
+                        scores8(c0, true, x);
+                        const uint32_t seen = seen8(c0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int c = c0 + 2 * e;
-                            float p0 = exp2_approx(t2[c]), p1 = exp2_approx(t2[c + 1]);
+                            const bool see0 = (seen >> (2 * e)) & 1, see1 = (seen >> (2 * e + 1)) & 1;
+                            const float p0 = see0 ? exp2_approx(x[2 * e]) : 0.f, p1 = see1 ? exp2_approx(x[2 * e + 1]) : 0.f;
                             h[e] = pack_bf16x2(p0 * f, p1 * f);
-                            if (bad_v) {
-                                if (t2[c] > -INFINITY) p0 = NAN;
-                                if (t2[c + 1] > -INFINITY) p1 = NAN;
-                            }
-                            add2(l[c], l[c + 1], p0, p1);
+                            add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], bad_v && see0 ? NAN : p0, bad_v && see1 ? NAN : p1);
                         }
-                        *reinterpret_cast<uint4*>(p_row + key * 128 + (((c0 >> 3) ^ (key & 7)) << 4)) =
+                        *reinterpret_cast<uint4*>(p_row + key * 128 + ((((half * CW + c0) >> 3) ^ (key & 7)) << 4)) =
                             make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
@@ -905,17 +1021,38 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full0 + 8 * st);
-            }
-            bool ok = !fail;
-            if (ok && steps > 0) ok = mbar_wait(o_done0 + 8 * st, (uint32_t)(n_o & 1), lim);
-            // row sums over the stream's keys: halve the columns a thread holds while
-            // exchanging the other half
+                return true;
+            };
+            const int i_tree = min(steps, SHARED ? n_pre : (n_pre + 1 - st) >> 1);  // first of the tree's
+            for (int i = 0; i < i_tree && !fail; ++i) fail = !step(std::false_type{}, i);
+            for (int i = i_tree; i < steps && !fail; ++i) fail = !step(std::true_type{}, i);
+            // row sums over the keys of this warp: halve the columns a lane holds while
+            // adding the other half's
+            if constexpr (CW >= 32) {
 #pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                const float v = warp_sum(l[c]);
-                if (lane == (c & 31)) s_red[(st * 4 + quarter) * NB + c] = v;
+                for (int c0 = 0; c0 < CW; c0 += 32) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        const bool up = lane & o;
+#pragma unroll
+                        for (int c = c0; c < c0 + o; ++c) {
+                            const float give = up ? l[c] : l[c + o], keep = up ? l[c + o] : l[c];
+                            l[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                        }
+                    }
+                    s_red[(st * 4 + quarter) * NB + half * CW + c0 + lane] = l[c0];
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < CW; ++c) {
+                    const float v = warp_sum(l[c]);
+                    if (lane == c) s_red[(st * 4 + quarter) * NB + half * CW + c] = v;
+                }
             }
-            if (key == 0) s_vref[st] = v_ref;
+            if (stid == 0) s_vref[st] = v_ref;
+            bool ok = !fail && !late;
+            if (ok && steps > 0) ok = warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + steps - 1) & 1), lim);
+            __syncwarp();
             if (named_barrier_or(3, kUSoftmax, !ok)) {
                 gave_up = true;
                 g_failed = g_seg;
@@ -923,7 +1060,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             }
             fence_after_sync();
             n_s += steps;
-            n_o += steps > 0;
             slot0 += n_pre + 2 * n_tree;
 
             // Each row's coefficients.  Split streams: relative to the larger reference.
@@ -937,11 +1073,11 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 float m, sum, c0, c1 = 0.f;
                 if (SHARED) {
                     const int x = tid / NB, c = tid % NB;
-                    m = s_m[x * NB + c];
+                    m = -s_m[x * NB + c];
                     sum = sum_of(x, c);
                     c0 = s_vref[x] / kPScale;
                 } else {
-                    const float ma = s_m[tid], mb = s_m[NB + tid];
+                    const float ma = -s_m[tid], mb = -s_m[NB + tid];
                     m = fmaxf(ma, mb);
                     const float ref = m == -INFINITY ? 0.f : m;
                     const float wa = exp2f(ma - ref), wb = exp2f(mb - ref);
@@ -960,34 +1096,39 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 if (!SHARED) s_corr[NB + tid] = c1;
             }
             bar_sync(3, kUSoftmax);
-            // O^T: this thread's output column of half the rows (split) or of its
-            // stream's rows (shared)
-            const int n_a = SHARED ? n : (n + 1) >> 1, n_b = SHARED ? 0 : n >> 1;  // steps behind O_0 and O_1
-            const bool lo_a = n_pre > 0, lo_b = n_pre > 1;                          // prefix tiles among them
-            constexpr int COLS = SHARED ? NB : NB / 2;
-            const int col0 = SHARED ? 0 : st * COLS;
-            const uint32_t oa = tmem + lane_off + kO + (SHARED ? st * 2 * NB : 0), ob = tmem + lane_off + kO + 2 * NB;
+            // O^T: this thread's output column of some rows: of the stream's own (shared),
+            // or of a share of the block's
+            const int n_b = SHARED ? 0 : n >> 1;               // steps behind O_1
+            const bool all_a = n_pre > 0, all_b = n_pre > 1;   // prefix tiles among a stream's: all planes are there
+            constexpr int ALL = SHARED ? NB : NB / 2, COLS = ALL / kHalves < 8 ? 8 : ALL / kHalves;
+            const int col0 = SHARED ? half * COLS : (st * kHalves + half) * COLS;
+            const uint32_t oa = tmem + lane_off + kO + (SHARED ? st * 3 * NB : 0) + col0, ob = tmem + lane_off + kO + 3 * NB + col0;
+            const int first_row = (SHARED ? st * NB : 0) + col0;
+            if (col0 < NB && first_row < nrows) {
 #pragma unroll 1
-            for (int c = 0; c < COLS; c += 8) {
-                float va[8], vl[8], wa[8], wl[8];
-                tmem_ld8(oa + col0 + c, va);
-                if (lo_a) tmem_ld8(oa + NB + col0 + c, vl);
-                if (n_b > 0) tmem_ld8(ob + col0 + c, wa);
-                if (n_b > 0 && lo_b) tmem_ld8(ob + NB + col0 + c, wl);
-                tmem_wait_ld();
+                for (int c = 0; c < COLS; c += 8) {
+                    float va[3][8], vb[3][8];
+                    tmem_ld8(oa + c, va[0]);
+                    if (all_a) {
+                        tmem_ld8(oa + NB + c, va[1]);
+                        tmem_ld8(oa + 2 * NB + c, va[2]);
+                    }
+                    if (n_b > 0) tmem_ld8(ob + c, vb[0]);
+                    if (all_b && !SHARED) {
+                        tmem_ld8(ob + NB + c, vb[1]);
+                        tmem_ld8(ob + 2 * NB + c, vb[2]);
+                    }
+                    tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int r = SHARED ? st * NB + c + e : col0 + c + e;  // row of the block
-                    if (r >= nrows || key >= D) continue;
-                    float o = n_a > 0 ? va[e] + (lo_a ? vl[e] * kPLo : 0.f) : 0.f;
-                    o *= s_corr[r];
-                    if (n_b > 0) o = fmaf(wa[e] + (lo_b ? wl[e] * kPLo : 0.f), s_corr[NB + r], o);
-                    if (whole) {
-                        const int gr = row0 + r;
-                        store1(static_cast<uint16_t*>(a.out) +
-                                   (((size_t)s.b * w.N + gr / a.G) * a.Hq + hk * a.G + gr % a.G) * D + key, o);
-                    } else {
-                        a.part_o[(part + r) * D + key] = o;
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = first_row + c + e;  // row of the block
+                        if (r >= nrows || key >= D) continue;
+                        float o = (va[0][e] + (all_a ? va[1][e] + va[2][e] : 0.f)) * s_corr[r];
+                        if (n_b > 0) o = fmaf(vb[0][e] + (all_b ? vb[1][e] + vb[2][e] : 0.f), s_corr[NB + r], o);
+                        if (whole)
+                            store1(static_cast<uint16_t*>(a.out) + ((size_t)s.b * w.N * a.Hq + s_row[r]) * D + key, o);
+                        else
+                            a.part_o[(part + r) * D + key] = o;
                     }
                 }
             }
@@ -998,8 +1139,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     if (bad) {
         // what this CTA was to give from the segment on that it could not finish
         if (tid == 0) atomicExch(&g_wait_gave_up, 1);
-        for (long long g = g_failed; g < g_end && warp < 8;) {
-            const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g_end);
+        for (long long g = g_failed; g < g_end && tid < kUSoftmax;) {
+            const q8::Segment s = q8::segment_at(w, first, g, g_end);
             g += s.t1 - s.t0;
             const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * L::kRowsBlock;
             const int nrows = min(L::kRowsBlock, rows_all - row0);
@@ -1024,16 +1165,17 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 // unfinished, if that is the first share boundary inside it; rows y, y + gridDim.y, ...
 template <typename T, int D>
 __global__ void __launch_bounds__(D) attn_q8_merge_kernel(const AttnQ8Args a, int rows_block) {
-    extern __shared__ long long first[];
+    extern __shared__ uint32_t merge_smem[];
     const q8::Work w = a.work;
+    const q8::Offsets first(merge_smem, w.B);
     pdl_wait();
     pdl_trigger();
     q8::tile_offsets(w, a.kv_len, first);
-    const long long total = first[w.B];
+    const long long total = first.total(w);
     const int c = blockIdx.x + 1;
     const long long g = w.cta_begin(total, c);
     if (g >= total || w.cta_begin(total, c + 1) == g) return;  // an empty share
-    const q8::Segment s = q8::segment_at(w, first, a.kv_len, g, g);
+    const q8::Segment s = q8::segment_at(w, first, g, g);
     if (s.t0 == 0) return;                         // the boundary falls between units
     const long long u0 = g - s.t0, u1 = u0 + s.tiles;
     const int c0 = w.cta_of(total, u0);            // share that begins the unit
@@ -1097,7 +1239,7 @@ cudaError_t launch_simple(AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch(kern, dim3(p.ctas), dim3(kSimpleThreads), smem, st, a);
     if (e == cudaSuccess)
-        e = launch(attn_q8_merge_kernel<T, D>, dim3(p.ctas - 1, 4), dim3(D), (a.work.B + 1) * 8, st, a, p.rows);
+        e = launch(attn_q8_merge_kernel<T, D>, dim3(p.ctas - 1, 4), dim3(D), q8::offsets_bytes(a.work.B), st, a, p.rows);
     return e;
 }
 
@@ -1138,7 +1280,7 @@ cudaError_t launch_umma(const CUtensorMap (&m)[4], AttnQ8Args& a, const Plan& p,
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch(kern, dim3(p.ctas), dim3(kUThreads), smem, st, m[0], m[1], m[2], m[3], a);
     if (e == cudaSuccess)
-        e = launch(attn_q8_merge_kernel<uint16_t, D>, dim3(p.ctas - 1, 4), dim3(D), (a.work.B + 1) * 8, st, a, p.rows);
+        e = launch(attn_q8_merge_kernel<uint16_t, D>, dim3(p.ctas - 1, 4), dim3(D), q8::offsets_bytes(a.work.B), st, a, p.rows);
     return e;
 }
 
@@ -1183,6 +1325,9 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.P = P; a.M = M; a.n_pages = n_pages; a.W = (N + 63) / 64;
     a.qblocks = (N * a.G + p.rows - 1) / p.rows;
     a.work = q8::Work{B, N, Hkv * a.qblocks, p.keys, M * P, p.ctas};
+    if ((long long)B * a.work.U * (((long long)M * P + p.keys - 1) / p.keys + (N + p.keys - 1) / p.keys) > 0x7fffffffll)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "tree_attention_q8: %d sequences of up to %lld tokens are too many tiles", B,
+                    (long long)M * P);
     a.scale_log2 = scale * kLog2e;
     cudaStream_t st = as_stream(stream);
     cudaError_t e;

@@ -76,25 +76,39 @@ struct Work {
     }
 };
 
-// Fills first[b] (b <= B) with the number of tiles of sequences before b; called
-// by every thread of the block.
-__device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __restrict__ kv_len, long long* first) {
-    for (int b = threadIdx.x; b < w.B; b += blockDim.x)
-        first[b + 1] = (long long)w.U * w.tiles(w.len(kv_len, b));
-    if (threadIdx.x == 0) first[0] = 0;
+// Two tables in shared memory: first[b] (b <= B), the number of tiles of sequences
+// before b, and rest[b], the length of b less the whole tiles before its last one.
+// (Tiles are counted in 32 bits: the entry point bounds their number.)
+__host__ __device__ __forceinline__ int offsets_bytes(int B) { return (B + 1) * 4 + (B + 3) / 4 * 4; }
+struct Offsets {
+    uint32_t* first;
+    uint8_t* rest;
+    __device__ __forceinline__ Offsets(void* smem, int B)
+        : first(static_cast<uint32_t*>(smem)), rest(reinterpret_cast<uint8_t*>(first + B + 1)) {}
+    __device__ __forceinline__ long long total(const Work& w) const { return first[w.B]; }
+};
+
+// Fills the tables; called by every thread of the block.
+__device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __restrict__ kv_len, const Offsets& t) {
+    for (int b = threadIdx.x; b < w.B; b += blockDim.x) {
+        const int L = w.len(kv_len, b);
+        t.rest[b] = (uint8_t)(L ? (L - 1) % w.T : 0);
+        t.first[b + 1] = (uint32_t)w.U * w.tiles(L);
+    }
+    if (threadIdx.x == 0) t.first[0] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {  // inclusive scan by one warp, 32 sequences at a time
-        long long carry = 0;
+        uint32_t carry = 0;
         for (int b0 = 0; b0 < w.B; b0 += 32) {
             const int b = b0 + (int)threadIdx.x;
-            long long v = b < w.B ? first[b + 1] : 0;
+            uint32_t v = b < w.B ? t.first[b + 1] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
                 if ((int)threadIdx.x >= o) v += u;
             }
             v += carry;
-            if (b < w.B) first[b + 1] = v;
+            if (b < w.B) t.first[b + 1] = v;
             carry = __shfl_sync(0xffffffffu, v, 31);
         }
     }
@@ -102,7 +116,7 @@ __device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __res
 }
 
 // The sequence whose tiles hold g (first[b] <= g < first[b + 1]).
-__device__ __forceinline__ int find_sequence(const long long* first, int B, long long g) {
+__device__ __forceinline__ int find_sequence(const uint32_t* first, int B, long long g) {
     int lo = 0, hi = B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -119,15 +133,15 @@ struct Segment {
     // that begins a unit without ending it (its last): its two partial slots
     __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 > 0 ? 0 : 1); }
 };
-__device__ __forceinline__ Segment segment_at(const Work& w, const long long* first, const int32_t* kv_len,
-                                              long long g, long long g_end) {
+__device__ __forceinline__ Segment segment_at(const Work& w, const Offsets& t, long long g, long long g_end) {
     Segment s;
-    s.b = find_sequence(first, w.B, g);
-    s.L = w.len(kv_len, s.b);
-    s.tiles = w.tiles(s.L);
-    const long long x = g - first[s.b];
-    s.unit = (int)(x / s.tiles);
-    s.t0 = (int)(x - (long long)s.unit * s.tiles);
+    s.b = find_sequence(t.first, w.B, g);
+    s.tiles = (int)((t.first[s.b + 1] - t.first[s.b]) / (uint32_t)w.U);
+    const int pt = s.tiles - w.tree_tiles();
+    s.L = pt ? (pt - 1) * w.T + t.rest[s.b] + 1 : 0;
+    const uint32_t x = (uint32_t)g - t.first[s.b];
+    s.unit = (int)(x / (uint32_t)s.tiles);
+    s.t0 = (int)(x - (uint32_t)s.unit * s.tiles);
     const long long left = g_end - g;
     s.t1 = left < s.tiles - s.t0 ? s.t0 + (int)left : s.tiles;
     return s;

@@ -38,6 +38,15 @@ def page_scale(values):
     return 2.0 ** e
 
 
+def page_scales(x):
+    """page_scale of every [n, Hkv] block of x [n, Hkv, P, D]."""
+    top = np.where(np.isfinite(x), np.abs(x), 0.0).max((2, 3))
+    e = np.full(top.shape, -64.0)
+    for _ in range(128):
+        e = np.where((e < 64) & (top > 448.0 * 2.0 ** e), e + 1, e)
+    return 2.0 ** e
+
+
 def readable(s):
     return bool(2.0 ** -64 <= s <= 2.0 ** 64)
 
@@ -46,13 +55,13 @@ def readable(s):
 def prefix(pages, scale, other_scale, table, L, h):
     """Values [n, D] of one head's readable prefix keys (the slots whose page and
     scales count)."""
-    n_pages, _, P, _ = pages.shape
-    rows = []
-    for j in range(L):
-        p = int(table[j // P])
+    n_pages, _, P, D = pages.shape
+    rows = [np.zeros((0, D))]
+    for j in range(-(-L // P)):
+        p = int(table[j])
         if 0 <= p < n_pages and readable(scale[p, h]) and readable(other_scale[p, h]):
-            rows.append(decode(pages[p, h, j % P]) * float(scale[p, h]))
-    return np.array(rows).reshape(len(rows), pages.shape[3])
+            rows.append(decode(pages[p, h, : min(P, L - j * P)]) * float(scale[p, h]))
+    return np.concatenate(rows)
 
 
 def sees(mask, N):
@@ -76,18 +85,15 @@ def attention(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, table, kv_l
             kp = prefix(k_pages, k_scale, v_scale, table[b], L, h)
             vp = prefix(v_pages, v_scale, k_scale, table[b], L, h)
             k, v = np.concatenate([kp, k_tree[b, :, h]]), np.concatenate([vp, v_tree[b, :, h]])
-            for g in range(G):
-                for i in range(N):
-                    vis = np.concatenate([np.ones(len(kp), bool), seen[i]])
-                    if not vis.any():
-                        continue
-                    kk, vv, qq = k[vis], v[vis], q[b, i, h * G + g]
-                    z = kk @ qq * scale
-                    p = np.exp(z - z.max())
-                    p /= p.sum()
-                    out[b, i, h * G + g] = p @ vv
-                    spread[b, i, h * G + g] = p @ np.abs(vv)
-                    bounds[b, i, h * G + g] = (np.abs(kk) @ np.abs(qq) * scale).max(), (np.abs(kk).sum(1) * scale).max()
+            vis = np.concatenate([np.ones((N, len(kp)), bool), seen], 1)
+            some = vis.any(1)
+            for g in range(h * G, h * G + G):
+                z = np.where(vis, q[b, :, g] @ k.T * scale, -np.inf)[some]
+                p = np.exp(z - z.max(1, keepdims=True))
+                p /= p.sum(1, keepdims=True)
+                out[b, some, g], spread[b, some, g] = p @ v, p @ np.abs(v)
+                bounds[b, some, g, 0] = np.where(vis, np.abs(q[b, :, g]) @ np.abs(k).T * scale, 0)[some].max(1)
+                bounds[b, some, g, 1] = np.where(vis, np.abs(k).sum(1) * scale, 0)[some].max(1)
     return out, spread, bounds
 
 

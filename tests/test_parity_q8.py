@@ -19,9 +19,12 @@ def pool(rng, n, Hkv, P, D, fill=1.0):
     """Codes and power-of-two scales of random rows whose size varies by page."""
     out = {}
     for s in "kv":
-        x = rng.normal(0, 1, (n, Hkv, P, D)) * np.exp(rng.normal(0, 0.5, (n, Hkv, 1, 1))) * fill
-        scale = np.array([[R.page_scale(x[p, h]) for h in range(Hkv)] for p in range(n)], np.float32)
-        out[s] = R.encode(x / scale[:, :, None, None]), scale
+        x = rng.standard_normal((n, Hkv, P, D), np.float32) * np.exp(rng.normal(0, 0.5, (n, Hkv, 1, 1))).astype(np.float32) * fill
+        top = np.abs(x).max((2, 3), keepdims=True)
+        scale = R.page_scales(top).astype(np.float32)
+        # (the same codes as R.encode gives: nothing exceeds 448 under these scales)
+        codes = torch.from_numpy(x / scale[:, :, None, None]).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+        out[s] = codes, scale
     return out["k"][0], out["v"][0], out["k"][1], out["v"][1]
 
 
@@ -99,24 +102,31 @@ def tolerance(c, ref):
     is divided by likewise: 2.1 e.  Sums over the keys in float32: each addition
     rounds once, relative to the sum of magnitudes.  exp2: 2 units, its argument's
     rounding is part of e (arguments stay below 2^7 in units of the score).
-    bf16: q enters to 2^-19 of the largest |q| of the row block (all of q here);
-    weights of 7 bits: 2^-8 (half a step), and 2^-20 of the largest weight as the
-    end of their range; the output rounds to bf16: 2^-8 of itself."""
+    bf16: q enters to 2^-17 of the largest |q| of the row block (all of q here);
+    weights of tree rows are bf16, 2^-8, those of pages have 9 bits, 2^-10 (both are
+    held to 2^-8 here), and half of e5m2's least step, 2^-17, in
+    planes that hold at least 2^9 for a weight of 1 on the largest V scale: 2^-26,
+    times a code of at most 448, for each key; the output rounds to bf16: 2^-8."""
     out, spread, bounds = ref
     keys = min(int(c["kv_len"].max()), c["table"].shape[1] * c["k_pages"].shape[2]) + c["q"].shape[1]
     D = c["q"].shape[3]
     e = (D + 8) * U * bounds[..., 0] + 8 * U * 128
     per = (2 * keys + 64) * U
     if c["dtype"] == "bf16":
-        e = e + 2.0 ** -19 * np.abs(c["q"]).max() * bounds[..., 1]
+        e = e + 2.0 ** -17 * np.abs(c["q"]).max() * bounds[..., 1]
         per = per + 2.0 ** -8
     tol = spread * (2.1 * e[..., None] + per)
     if c["dtype"] == "bf16":
-        vmax = np.nanmax(np.abs(out)) + 8  # no single value of V is larger
-        tol = tol + 2.0 ** -8 * np.abs(out) + keys * 2.0 ** -28 * vmax
+        vs = np.where(np.isfinite(c["v_scale"]), c["v_scale"], 0).max()
+        tol = tol + 2.0 ** -8 * np.abs(out) + keys * 2.0 ** -26 * 448 * max(vs, 1 / 448)
     else:
         tol = tol + U * np.abs(out)
     return tol
+
+
+def worst_score(c, ref):
+    """What the rounding of q may add to a weight, as a share (tolerance's e)."""
+    return 2.1 * 2.0 ** -17 * np.abs(c["q"]).max() * np.nanmax(ref[2][..., 1])
 
 
 def check(c, got, ref):
@@ -125,9 +135,9 @@ def check(c, got, ref):
     assert (err - tol).max() <= 0, ((err - tol).max(), err.max())
     norm = np.linalg.norm(np.nan_to_num(ref[0]))
     if c["dtype"] == "bf16" and norm:
-        # two independent roundings (weights, output) of at most 2^-8 each: a
+        # independent roundings of the output and the weights, at most 2^-8 each: a
         # uniform error within +-h has root mean square h / sqrt(3)
-        assert np.linalg.norm(err) / norm <= np.sqrt(2 / 3) * 2.0 ** -8 + 2.0 ** -12
+        assert np.linalg.norm(err) / norm <= np.sqrt(2 / 3) * 2.0 ** -8 + 2.0 ** -12 + worst_score(c, ref)
 
 
 # ---------------------------------------------------------------------------
@@ -177,10 +187,24 @@ def test_attention_growing_scores_and_uneven_scales(medusa, dtype):
             c["v_scale"][p] *= 2.0 ** ((j * 5) % 13 - 6)
     ref = reference(c)
     got = attend(medusa, c)
-    # the weights' range ends 2^-20 below the largest weight times the largest V
-    vmax = max(448 * c["v_scale"].max(), np.abs(c["v_tree"]).max())
-    extra = 0 if dtype == "f32" else 1000 * 2.0 ** -28 * vmax
-    assert (np.abs(got - ref[0]) <= tolerance(c, ref) + extra).all()
+    assert (np.abs(got - ref[0]) <= tolerance(c, ref)).all()
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D,P", [(1, 120, 40, 128, 64), (9, 120, 120, 64, 16), (40, 80, 80, 128, 32), (70, 60, 60, 128, 128),
+                                          (64, 40, 40, 64, 64)])
+def test_attention_long_shares(medusa, N, Hq, Hkv, D, P):
+    """Each CTA works through many tiles and several units: references move in the
+    middle of a share (scores and V scales that grow from page to page, in some
+    pages of some heads only), pages are missing, units end and begin."""
+    c = attention_case(40 + N, 2, N, Hq, Hkv, D, P, [2000, 3171], "bf16", q_std=1.5)
+    rng = np.random.default_rng(N)
+    for b in range(2):
+        for j, p in enumerate(c["table"][b]):
+            if p >= 0:
+                c["k_scale"][p] *= 2.0 ** rng.integers(0, 3, Hkv) * (1 + (j > 20))
+                c["v_scale"][p] *= 2.0 ** rng.integers(-3, 4, Hkv)
+    c["table"][0, 5] = c["table"][1, 9] = -1
+    check(c, attend(medusa, c), reference(c))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -575,5 +599,5 @@ def test_paged_attention_agrees_with_the_dense_cache(medusa):
                                   c["scale"]).double().cpu().numpy()
     got = attend(medusa, c)
     ref = reference(c)
-    # each side is within its own rounding of the definition; the dense kernel rounds weights to bf16 (2^-8)
-    assert (np.abs(got - dense) <= 2 * tolerance(c, ref)).all()
+    # each side is within its own rounding of the definition; the dense kernel rounds its weights to bf16, half a step 2^-8
+    assert (np.abs(got - dense) <= 2 * tolerance(c, ref) + 2.0 ** -8 * ref[1]).all()

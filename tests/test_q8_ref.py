@@ -20,6 +20,8 @@ def test_encode_is_nearest_even_and_inverts_decode():
     grid = R.VALUES[np.isfinite(R.VALUES)]
     best = np.abs(grid[None] - np.clip(x, -448, 448)[:, None]).min(1)
     assert np.array_equal(np.abs(got - np.clip(x, -448, 448)), best)
+    y = x[np.abs(x) <= 448].astype(np.float32)
+    assert np.array_equal(R.encode(y), torch.from_numpy(y).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
     assert R.encode([2.0 ** -10])[0] == 0 and R.encode([3 * 2.0 ** -10])[0] == 2  # ties to the even code
 
 
