@@ -52,6 +52,16 @@ __device__ __forceinline__ void store1(uint16_t* p, float v) {
     *p = r;
 }
 
+__device__ __forceinline__ void store4(float* p, float4 v, float f) {
+    *reinterpret_cast<float4*>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v.y * f), "f"(v.x * f));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v.w * f), "f"(v.z * f));
+    *reinterpret_cast<uint2*>(p) = w;
+}
+
 // 2^x with x <= 0 or -inf; exp2f is within 2 units in the last place
 __device__ __forceinline__ float weight(float x) { return exp2f(x); }
 
@@ -295,8 +305,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 // Every wait is bounded; a CTA that gives up marks its results NaN.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;  // keys per tile
-constexpr int kHalves = 1;               // warps that share a lane quarter of a stream
-constexpr int kUSoftmax = 256 * kHalves, kUThreads = kUSoftmax + 64;
+constexpr int kUSoftmax = 256, kUThreads = kUSoftmax + 64;
 constexpr int kUMmaWarp = kUSoftmax / 32, kUTmaWarp = kUMmaWarp + 1;
 constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
 constexpr float kTau = 4.f;              // log2 by which weights may exceed 1
@@ -325,11 +334,11 @@ struct USmem {
     static constexpr int kOffRow = kOffRed + 8 * NB * 4;       // int [2 * NB]: (node, head) of a row, in rows of D
     static constexpr int kOffMask = kOffRow + 2 * NB * 4;      // uint32 [kRowsBlock][16]: mask rows
     static constexpr int kOffInfo = kOffMask + kRowsBlock * 64;  // float2 (k, v scale)[kRing][8]
-    static constexpr int kOffBad = kOffInfo + kRing * 8 * 8;   // uint32 [16]: tree rows with a non-finite V
-    static constexpr int kOffMisc = kOffBad + 64;              // see below, 256 bytes
+    static constexpr int kOffBad = kOffInfo + kRing * 8 * 8;   // uint32 [2][4]: keys of a tree tile with a non-finite V
+    static constexpr int kOffMisc = kOffBad + 32;              // see below, 256 bytes
     static constexpr int kOffBar = kOffMisc + 256;
-    // full[R] empty[R] s_full[2] p_full[2] pv_done[2] qfull drain
-    static constexpr int kNumBar = 2 * kRing + 8;
+    // full[R] empty[R] s_full[2] p_full[2] pv_done[2] qfull checked[2] drain
+    static constexpr int kNumBar = 2 * kRing + 10;
     static constexpr int kOffFirst = (kOffBar + kNumBar * 8 + 15) / 16 * 16;
     static int bytes(int B) { return kOffFirst + q8::offsets_bytes(B) + 1024; }  // + alignment slack
 };
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                    qb_a = base_a + L::kOffQB;
     const uint32_t bar_a = base_a + L::kOffBar;
     const uint32_t full0 = bar_a, empty0 = full0 + 8 * R, s_full0 = empty0 + 8 * R, p_full0 = s_full0 + 16,
-                   pv_done0 = p_full0 + 16, qfull = pv_done0 + 16, drain = qfull + 8;
+                   pv_done0 = p_full0 + 16, qfull = pv_done0 + 16, checked0 = qfull + 8, drain = checked0 + 16;
     float* s_m = reinterpret_cast<float*>(base + L::kOffM);
     float* s_corr = reinterpret_cast<float*>(base + L::kOffCorr);
     float* s_red = reinterpret_cast<float*>(base + L::kOffRed);
@@ -442,6 +451,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         mbar_init(p_full0, kUStream / 32);
         mbar_init(p_full0 + 8, kUStream / 32);
         mbar_init(qfull, kUSoftmax / 32);
+        mbar_init(checked0, 4);
+        mbar_init(checked0 + 8, 4);
         mbar_init_fence();
         *flag = 0;
         s_fail[0] = s_fail[1] = 0;
@@ -654,20 +665,39 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         }
     } else if (warp < kUMmaWarp) {
         // ------------------------------ softmax warps ------------------------------
-        constexpr int CW = NB / kHalves;  // rows (columns of S^T) per thread
-        const int st = warp / (4 * kHalves), half = (warp >> 2) % kHalves, quarter = warp & 3;
+        constexpr int CW = NB;
+        const int st = warp >> 2, quarter = warp & 3;
         const int key = quarter * 32 + lane;  // TMEM lane: key of a tile, then output column
         const int stid = tid & (kUStream - 1);
         const int page_shift = 31 - __clz(a.P);
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lane_off + kS + st * NB + half * CW;
-        const uint32_t tO = tmem + lane_off + kO + st * 3 * NB + half * CW;
+        const uint32_t tS = tmem + lane_off + kS + st * NB;
+        const uint32_t tO = tmem + lane_off + kO + st * 3 * NB;
         float* m_row = s_m + st * NB;  // negated
         float* corr_row = s_corr + st * NB;
         uint8_t* p_row = base + L::kOffP + st * L::kP;
         const float scale = a.scale_log2;
         int n_s = 0;       // steps of this stream before the segment
         int slot0 = 0;
+        int n_checked = 0;  // tree tiles before the segment (shared streams)
+        // Q rows of a segment's block, 16 bytes a load; rows behind its end are zero
+        constexpr int CH = D / 8, QN = (L::kRowsBlock * CH + kUSoftmax - 1) / kUSoftmax;
+        uint4 qv[QN];
+        auto load_q = [&](const q8::Segment& s) {
+            const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * L::kRowsBlock;
+            const int nrows = min(L::kRowsBlock, rows_all - row0);
+#pragma unroll
+            for (int i = 0; i < QN; ++i) {
+                const int c = tid + i * kUSoftmax, r = c / CH;
+                qv[i] = make_uint4(0, 0, 0, 0);
+                if (r < nrows) {
+                    const int gr = row0 + r;
+                    qv[i] = ld_stream16(static_cast<const uint16_t*>(a.q) +
+                                        (((size_t)s.b * w.N + gr / a.G) * a.Hq + hk * a.G + gr % a.G) * D + c % CH * 8);
+                }
+            }
+        };
+        if (g_begin < g_end) load_q(q8::segment_at(w, first, g_begin, g_end));
         for (long long g = g_begin; g < g_end;) {
             const q8::Segment s = q8::segment_at(w, first, g, g_end);
             const long long g_seg = g;
@@ -679,28 +709,15 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * L::kRowsBlock;
             const int nrows = min(L::kRowsBlock, rows_all - row0);
 
-            // Q into shared memory: bf16 for the tree's tiles, two e4m3 planes for the
-            // pages'.  Rows behind the block's end are zero.
-            constexpr int CH = D / 8, QN = (L::kRowsBlock * CH + kUSoftmax - 1) / kUSoftmax;
-            uint4 qv[QN];
+            // Q (its rows were asked for at the end of the last segment) into shared memory:
+            // bf16 for the tree's tiles, two e4m3 planes for the pages'.
             float qmax = 0.f;
-#pragma unroll
-            for (int i = 0; i < QN; ++i) {
-                const int c = tid + i * kUSoftmax, r = c / CH;
-                qv[i] = make_uint4(0, 0, 0, 0);
-                if (r < nrows) {
-                    const int gr = row0 + r;
-                    qv[i] = ld_stream16(static_cast<const uint16_t*>(a.q) +
-                                        (((size_t)s.b * w.N + gr / a.G) * a.Hq + hk * a.G + gr % a.G) * D + c % CH * 8);
-                }
-            }
             if (n_tree) {
                 const uint32_t* mask = reinterpret_cast<const uint32_t*>(a.mask);
                 for (int i = tid; i < L::kRowsBlock * 16; i += kUSoftmax) {
                     const int r = i >> 4, word = i & 15;
                     if (word < 2 * a.W) s_mask[i] = r < nrows ? __ldg(mask + (size_t)((row0 + r) / a.G) * (2 * a.W) + word) : 0u;
                 }
-                if (SHARED && tid < 16) s_bad[tid] = 0;
             }
 #pragma unroll
             for (int i = 0; i < QN; ++i) {
@@ -756,27 +773,25 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
-            // Tree rows whose V is not finite: 0 * inf of a row that does not see them
-            // would spoil that row, so their V counts as zero and rows that see them get
-            // NaN.  Split streams look at their tile; shared ones, where one stream may
-            // clear what the other has still to look at, look ahead here.
-            if (SHARED && n_tree) {
-#pragma unroll 4
-                for (int c = tid; c < w.N * CH; c += kUSoftmax) {
-                    const int m = c / CH;
-                    const uint4 v = ld_stream16(static_cast<const uint16_t*>(a.v_tree) +
-                                                (((size_t)s.b * w.N + m) * a.Hkv + hk) * D + c % CH * 8);
-                    if (not_finite(v)) atomicOr(&s_bad[m >> 5], 1u << (m & 31));
-                }
-                bar_sync(3, kUSoftmax);
-            }
-
             float l[CW];
 #pragma unroll
             for (int c = 0; c < CW; ++c) l[c] = 0.f;
             float v_ref = 0.f;
             bool fail = false, late = false;
             const int pt = w.prefix_tiles(s.L);
+            const int i_tree = min(steps, SHARED ? n_pre : (n_pre + 1 - st) >> 1);  // first step of the tree's
+            // Rows of this thread that see tree row m0 + lane.
+            auto seen64 = [&](int m0) -> uint64_t {
+                uint32_t lo = 0, hi = 0;
+                if (m0 < w.N) {
+                    const uint32_t* words = s_mask + (SHARED ? st * NB : 0) * 16 + (m0 >> 5);
+#pragma unroll 16
+                    for (int c = 0; c < (CW < 32 ? CW : 32); ++c) lo |= ((words[c * 16] >> lane) & 1u) << c;
+#pragma unroll 16
+                    for (int c = 32; c < CW; ++c) hi |= ((words[c * 16] >> lane) & 1u) << (c - 32);
+                }
+                return (uint64_t)hi << 32 | lo;
+            };
             // One step; false: a wait gave up.  The tree's tiles have a body of their own,
             // which keeps their bookkeeping out of the prefix's registers.
             auto step = [&](auto is_tree, const int i) -> bool {
@@ -786,6 +801,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 bool ok = warp_wait(s_full0 + 8 * st, (uint32_t)((n_s + i) & 1), lim);
                 float kc = kq, vs = 1.f;
                 bool valid, bad_v = false;
+                uint64_t seen = ~0ull;  // rows that see the key
                 if constexpr (!tree) {
                     // the slot is in since the scores are; this wait makes the scales visible
                     ok = warp_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), lim) && ok;
@@ -793,37 +809,39 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     valid = sc.y > 0.f && (s.t0 + t) * kTile + key < s.L;
                     kc = kq * sc.x;
                     vs = valid ? sc.y : 0.f;
+                    seen = valid ? seen : 0;
                 } else {
                     kc = scale;
                     ok = warp_wait(full0 + 8 * ((sl + 1) % R), (uint32_t)(((sl + 1) / R) & 1), lim) && ok;
                     const int m = (s.t0 + t - pt) * kTile + key;  // tree row
                     valid = m < w.N;
-                    if constexpr (SHARED) {
-                        bad_v = valid && (s_bad[m >> 5] >> (m & 31) & 1);
-                    } else {
+                    // A tree row whose V is not finite: 0 * inf of a query row that does not see
+                    // it would spoil that one, so its V counts as zero and rows that see it get
+                    // NaN.  Of two streams that share the tile stream 0 looks and clears.
+                    if (!SHARED || st == 0) {
                         const uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
-#pragma unroll 1
+#pragma unroll 4
                         for (int c = 0; c < D / 8; ++c)
                             bad_v = not_finite(*reinterpret_cast<const uint4*>(v + (c >> 3) * kTile * 128 +
                                                                                (((c + lane) & 7) << 4))) || bad_v;
+                        if constexpr (SHARED) {
+                            const unsigned bad = __ballot_sync(0xffffffffu, bad_v);
+                            if (lane == 0) {
+                                s_bad[((n_checked + t - n_pre) & 1) * 4 + quarter] = bad;
+                                mbar_arrive(checked0 + 8 * ((n_checked + t - n_pre) & 1));
+                            }
+                        }
+                    } else {
+                        // (stream 0 is at most a tile ahead: two answers are kept)
+                        const int k = n_checked + t - n_pre;
+                        ok = warp_wait(checked0 + 8 * (k & 1), (uint32_t)((k >> 1) & 1), lim) && ok;
+                        bad_v = s_bad[(k & 1) * 4 + quarter] >> lane & 1;
                     }
+                    seen = seen64(m - lane);
+                    if (!valid) seen = 0;
                 }
                 fence_after_sync();
                 if ((!ok || late) && lane == 0) s_fail[st] = 1;
-                // rows of columns c0 .. c0 + 7 that see the key: all, but for the tree's keys
-                auto seen8 = [&](int c0) -> uint32_t {
-                    uint32_t seen = 0xffu;
-                    if constexpr (tree) {
-                        seen = 0;
-                        const int m0 = (s.t0 + t - pt) * kTile + quarter * 32;
-                        const uint32_t* words = s_mask + ((SHARED ? st * NB : 0) + half * CW + c0) * 16 + (m0 >> 5);
-                        if (m0 < w.N) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) seen |= ((words[c * 16] >> lane) & 1u) << c;
-                        }
-                    }
-                    return valid ? seen : 0u;
-                };
                 // Eight columns of scores from c0 on, in log2 units, less the rows'
                 // references or as they are.
                 auto scores8 = [&](int c0, bool relative, float* x) {
@@ -833,7 +851,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 #pragma unroll
                     for (int e = 0; e < 8; e += 4) {
                         float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (relative) m = *reinterpret_cast<const float4*>(m_row + half * CW + c0 + e);
+                        if (relative) m = *reinterpret_cast<const float4*>(m_row + c0 + e);
                         fma2(x[e], x[e + 1], y[e], y[e + 1], kc, m.x, m.y);
                         fma2(x[e + 2], x[e + 3], y[e + 2], y[e + 3], kc, m.z, m.w);
                     }
@@ -854,7 +872,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < WX; e += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(m_row + half * CW + c0 + e);
+                        const float4 m = *reinterpret_cast<const float4*>(m_row + c0 + e);
                         fma2(x[e], x[e + 1], x[e], x[e + 1], kc, m.x, m.y);
                         fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], kc, m.z, m.w);
                     }
@@ -879,9 +897,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 #pragma unroll 1
                             for (int c0 = 0; c0 < CW; c0 += 8) {
                                 scores8(c0, true, x);
-                                const uint32_t seen = seen8(c0);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) top = fmaxf(top, (seen >> e) & 1 ? x[e] : -INFINITY);
+                                for (int e = 0; e < 8; ++e) top = fmaxf(top, (seen >> (c0 + e)) & 1 ? x[e] : -INFINITY);
                             }
                         }
                         move = move || top > kTau;
@@ -894,11 +911,10 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     for (int c0 = 0; c0 < CW; c0 += 8) {
                         float y[8];
                         scores8(c0, false, y);
-                        const uint32_t seen = seen8(c0);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const float m = redux_max((seen >> e) & 1 ? y[e] : -INFINITY);
-                            if (lane == e) s_red[(st * 4 + quarter) * NB + half * CW + c0 + e] = m;
+                            const float m = redux_max((seen >> (c0 + e)) & 1 ? y[e] : -INFINITY);
+                            if (lane == e) s_red[(st * 4 + quarter) * NB + c0 + e] = m;
                         }
                     }
                     const float vm = redux_max(vs);
@@ -923,7 +939,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     if (i > 0) {  // what was added up so far
 #pragma unroll
                         for (int c = 0; c < CW; c += 4) {
-                            const float4 r = *reinterpret_cast<const float4*>(corr_row + half * CW + c);
+                            const float4 r = *reinterpret_cast<const float4*>(corr_row + c);
                             l[c] *= r.x; l[c + 1] *= r.y; l[c + 2] *= r.z; l[c + 3] *= r.w;
                         }
                         fence_after_sync();
@@ -937,7 +953,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                             for (int p = 0; p < 3; ++p) {
                                 uint32_t ow[8];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) ow[e] = __float_as_uint(o[p][e] * (corr_row[half * CW + c + e] * vf));
+                                for (int e = 0; e < 8; ++e) ow[e] = __float_as_uint(o[p][e] * (corr_row[c + e] * vf));
                                 tmem_st8(tO + p * NB + c, ow);
                             }
                         }
@@ -949,7 +965,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 // A key that is not there has no V either: whatever the slot holds (stale
                 // codes may be NaN) is cleared.  When two streams share the tile, stream 0
                 // does it: its PV comes first.
-                if (half == 0 && (!SHARED || st == 0)) {
+                if (!SHARED || st == 0) {
                     if (!tree && !valid) {
                         uint4* v = reinterpret_cast<uint4*>(base + L::kOffRing + (sl % R) * L::kSlot + L::kHalf + key * D);
 #pragma unroll
@@ -986,7 +1002,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 #pragma unroll
                             for (int p = 0; p < 3; ++p) pw[p][e] = __byte_perm(two[0][p], two[1][p], 0x7531);
                         }
-                        const int col = half * CW + c0;
+                        const int col = c0;
 #pragma unroll
                         for (int p = 0; p < 3; ++p) {
                             // NB = 64: one plane of 64 bytes a key after the other; NB = 16:
@@ -1005,15 +1021,14 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     for (int c0 = 0; c0 < CW; c0 += 8) {
                         uint32_t h[4];
                         scores8(c0, true, x);
-                        const uint32_t seen = seen8(c0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const bool see0 = (seen >> (2 * e)) & 1, see1 = (seen >> (2 * e + 1)) & 1;
+                            const bool see0 = (seen >> (c0 + 2 * e)) & 1, see1 = (seen >> (c0 + 2 * e + 1)) & 1;
                             const float p0 = see0 ? exp2_approx(x[2 * e]) : 0.f, p1 = see1 ? exp2_approx(x[2 * e + 1]) : 0.f;
                             h[e] = pack_bf16x2(p0 * f, p1 * f);
                             add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], bad_v && see0 ? NAN : p0, bad_v && see1 ? NAN : p1);
                         }
-                        *reinterpret_cast<uint4*>(p_row + key * 128 + ((((half * CW + c0) >> 3) ^ (key & 7)) << 4)) =
+                        *reinterpret_cast<uint4*>(p_row + key * 128 + ((((c0) >> 3) ^ (key & 7)) << 4)) =
                             make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
@@ -1023,7 +1038,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 if (lane == 0) mbar_arrive(p_full0 + 8 * st);
                 return true;
             };
-            const int i_tree = min(steps, SHARED ? n_pre : (n_pre + 1 - st) >> 1);  // first of the tree's
             for (int i = 0; i < i_tree && !fail; ++i) fail = !step(std::false_type{}, i);
             for (int i = i_tree; i < steps && !fail; ++i) fail = !step(std::true_type{}, i);
             // row sums over the keys of this warp: halve the columns a lane holds while
@@ -1040,16 +1054,17 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                             l[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                         }
                     }
-                    s_red[(st * 4 + quarter) * NB + half * CW + c0 + lane] = l[c0];
+                    s_red[(st * 4 + quarter) * NB + c0 + lane] = l[c0];
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < CW; ++c) {
                     const float v = warp_sum(l[c]);
-                    if (lane == c) s_red[(st * 4 + quarter) * NB + half * CW + c] = v;
+                    if (lane == c) s_red[(st * 4 + quarter) * NB + c] = v;
                 }
             }
             if (stid == 0) s_vref[st] = v_ref;
+            if (g < g_end) load_q(q8::segment_at(w, first, g, g_end));
             bool ok = !fail && !late;
             if (ok && steps > 0) ok = warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + steps - 1) & 1), lim);
             __syncwarp();
@@ -1061,6 +1076,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             fence_after_sync();
             n_s += steps;
             slot0 += n_pre + 2 * n_tree;
+            n_checked += n_tree;
 
             // Each row's coefficients.  Split streams: relative to the larger reference.
             const bool whole = s.whole();
@@ -1100,11 +1116,11 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             // or of a share of the block's
             const int n_b = SHARED ? 0 : n >> 1;               // steps behind O_1
             const bool all_a = n_pre > 0, all_b = n_pre > 1;   // prefix tiles among a stream's: all planes are there
-            constexpr int ALL = SHARED ? NB : NB / 2, COLS = ALL / kHalves < 8 ? 8 : ALL / kHalves;
-            const int col0 = SHARED ? half * COLS : (st * kHalves + half) * COLS;
+            constexpr int COLS = SHARED ? NB : NB / 2;
+            const int col0 = SHARED ? 0 : st * COLS;
             const uint32_t oa = tmem + lane_off + kO + (SHARED ? st * 3 * NB : 0) + col0, ob = tmem + lane_off + kO + 3 * NB + col0;
             const int first_row = (SHARED ? st * NB : 0) + col0;
-            if (col0 < NB && first_row < nrows) {
+            if (first_row < nrows) {
 #pragma unroll 1
                 for (int c = 0; c < COLS; c += 8) {
                     float va[3][8], vb[3][8];
@@ -1161,10 +1177,14 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     if (warp == 0) tmem_dealloc(tmem, kCols);
 }
 
-// Joins the partial results.  Block (c, y): the unit that share c - 1 leaves
-// unfinished, if that is the first share boundary inside it; rows y, y + gridDim.y, ...
+// Joins the partial results.  Block (c, y): the unit that share c leaves
+// unfinished, if that is the first share boundary inside it; rows from y *
+// kMergeThreads / (D / 4) on, four columns a thread.  All of a thread's loads are
+// in flight at once (a loop of dependent loads took 16 rows x 10 round trips to
+// memory, 80 us).
+constexpr int kMergeThreads = 256, kMergeBatch = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(D) attn_q8_merge_kernel(const AttnQ8Args a, int rows_block) {
+__global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const AttnQ8Args a, int rows_block) {
     extern __shared__ uint32_t merge_smem[];
     const q8::Work w = a.work;
     const q8::Offsets first(merge_smem, w.B);
@@ -1182,29 +1202,44 @@ __global__ void __launch_bounds__(D) attn_q8_merge_kernel(const AttnQ8Args a, in
     if (c0 != w.cta_of(total, g - 1)) return;      // an earlier boundary is the first
     const int c1 = w.cta_of(total, u1 - 1);
     const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * rows_block;
-    const int nrows = min(rows_block, w.N * a.G - row0);
-    const int d = threadIdx.x;
-    for (int i = blockIdx.y; i < nrows; i += gridDim.y) {
-        float top = -INFINITY;
-        for (int j = c0; j <= c1; ++j) {
-            if (w.cta_begin(total, j) == w.cta_begin(total, j + 1)) continue;  // an empty share
-            const float2 ml = a.part_ml[(size_t)(2 * j + (j == c0 ? 1 : 0)) * rows_block + i];
-            top = fmaxf(top, ml.x);
+    const int i = blockIdx.y * (kMergeThreads / (D / 4)) + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    if (i >= min(rows_block, w.N * a.G - row0)) return;
+    // (shares are only empty when there are fewer tiles than CTAs; one left a slot
+    // unwritten then)
+    auto there = [&](int j) { return j <= c1 && w.cta_begin(total, j) != w.cta_begin(total, j + 1); };
+    auto slot = [&](int j) { return (size_t)(2 * j + (j == c0 ? 1 : 0)) * rows_block + i; };
+    float top = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = c0; j0 <= c1; j0 += kMergeBatch) {
+        float2 ml[kMergeBatch];
+        float4 v[kMergeBatch];
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (there(j0 + k)) {
+                ml[k] = a.part_ml[slot(j0 + k)];
+                v[k] = *reinterpret_cast<const float4*>(a.part_o + slot(j0 + k) * D + d);
+            }
         }
-        const float ref = top == -INFINITY ? 0.f : top;
-        float o = 0.f, l = 0.f;
-        for (int j = c0; j <= c1; ++j) {
-            if (w.cta_begin(total, j) == w.cta_begin(total, j + 1)) continue;
-            const size_t at = (size_t)(2 * j + (j == c0 ? 1 : 0)) * rows_block + i;
-            const float2 ml = a.part_ml[at];
-            const float f = weight(ml.x - ref);
-            l += ml.y * f;
-            o += a.part_o[at * D + d] * f;
+        float m = top;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) m = fmaxf(m, ml[k].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float f0 = weight(top - ref);
+        top = m;
+        l *= f0;
+        o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+            const float f = weight(ml[k].x - ref);
+            l += ml[k].y * f;
+            o.x += v[k].x * f; o.y += v[k].y * f; o.z += v[k].z * f; o.w += v[k].w * f;
         }
-        const int r = row0 + i;
-        store1(static_cast<T*>(a.out) + (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + d,
-               l == 0.f ? 0.f : o / l);
     }
+    const int r = row0 + i;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store4(static_cast<T*>(a.out) + (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + d, o, inv);
 }
 
 struct Plan {
@@ -1233,13 +1268,21 @@ int check_attn_q8(int B, int N, int Hq, int Hkv, int D, int P, int n_pages, int 
 size_t ws_bytes_q8(const Plan& p, int D) { return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float); }
 
 template <typename T, int D>
+cudaError_t launch_merge(const AttnQ8Args& a, const Plan& p, cudaStream_t st) {
+    constexpr int rows = kMergeThreads / (D / 4);  // of a block
+    const int all = a.work.N * a.G, most = all < p.rows ? all : p.rows;
+    return launch(attn_q8_merge_kernel<T, D>, dim3(p.ctas - 1, (most + rows - 1) / rows), dim3(kMergeThreads),
+                  q8::offsets_bytes(a.work.B), st, a, p.rows);
+}
+
+template <typename T, int D>
 cudaError_t launch_simple(AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     auto kern = tree_attn_q8_simple_kernel<T, D>;
     const int smem = SimpleSmem<D>::bytes(a.work.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch(kern, dim3(p.ctas), dim3(kSimpleThreads), smem, st, a);
     if (e == cudaSuccess)
-        e = launch(attn_q8_merge_kernel<T, D>, dim3(p.ctas - 1, 4), dim3(D), q8::offsets_bytes(a.work.B), st, a, p.rows);
+        e = launch_merge<T, D>(a, p, st);
     return e;
 }
 
@@ -1280,7 +1323,7 @@ cudaError_t launch_umma(const CUtensorMap (&m)[4], AttnQ8Args& a, const Plan& p,
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch(kern, dim3(p.ctas), dim3(kUThreads), smem, st, m[0], m[1], m[2], m[3], a);
     if (e == cudaSuccess)
-        e = launch(attn_q8_merge_kernel<uint16_t, D>, dim3(p.ctas - 1, 4), dim3(D), q8::offsets_bytes(a.work.B), st, a, p.rows);
+        e = launch_merge<uint16_t, D>(a, p, st);
     return e;
 }
 
