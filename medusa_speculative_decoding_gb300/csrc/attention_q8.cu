@@ -102,15 +102,13 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
     pdl_wait();
     pdl_trigger();
     q8::tile_offsets(w, a.kv_len, first);
-    const long long total = first.total(w);
-    long long g = w.cta_begin(total, blockIdx.x);
-    const long long g_end = w.cta_begin(total, blockIdx.x + 1);
+    const uint32_t total = first.total(w);
+    uint32_t g = w.cta_begin(total, blockIdx.x);
+    const uint32_t g_end = w.cta_begin(total, blockIdx.x + 1);
     const int rows_all = w.N * a.G;
     constexpr int ACC = kRows * D / kSimpleThreads;  // output rows per thread (one column)
     const int d = tid % D, r0 = tid / D * ACC;
-    while (g < g_end) {
-        const q8::Segment s = q8::segment_at(w, first, g, g_end);
-        g += s.t1 - s.t0;
+    for (q8::Segment s; q8::next_segment(w, first, g, g_end, s); g = s.end) {
         const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * kRows;
         const int nrows = min(kRows, rows_all - row0);
         for (int i = tid; i < kRows * D; i += kSimpleThreads) {
@@ -293,10 +291,9 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 //                   online softmax of its own, joined at the end
 //   SHARED = true   blocks of 2 NB rows; each stream has NB of them, both use
 //                   every tile
-// Steps x = 0, 1, 2, ...: stream x & 1, tile x (or x / 2).  When the weights of x
-// are written the MMA warp issues S(x + 2), if its keys are in, before PV(x): the
-// stream can go on with its next scores while PV(x) runs, and waits for that only
-// before it writes the next weights or rescales O.
+// Steps x = 0, 1, 2, ...: stream x & 1, tile x (or x / 2).  S has two buffers a
+// stream, so the MMA warp forms scores up to two steps ahead, and a stream waits
+// for its last PV only before it writes the next weights or rescales O.
 //
 // Warps 0-7 softmax, warp 8 MMA, warp 9 TMA (page tables, scales and tiles run
 // ahead through a ring of R slots; a slot is K and V of one tile of 128 keys).
@@ -305,9 +302,10 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 // Every wait is bounded; a CTA that gives up marks its results NaN.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;  // keys per tile
-constexpr int kUSoftmax = 256, kUThreads = kUSoftmax + 64;
-constexpr int kUMmaWarp = kUSoftmax / 32, kUTmaWarp = kUMmaWarp + 1;
+constexpr int kUSoftmax = 256, kUThreads = kUSoftmax + 96;
+constexpr int kUMmaWarp = kUSoftmax / 32, kUTmaWarp = kUMmaWarp + 2;  // an MMA warp per stream
 constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
+constexpr int kSetup = 3;               // tiles that a unit counts more (q8.cuh, Work)
 constexpr float kTau = 4.f;              // log2 by which weights may exceed 1
 constexpr float kPScale = 2048.f;        // planes hold weight * vs / v_ref * kPScale <= 2^15
 constexpr float kVHead = 4.f;            // v_ref = kVHead * the largest V scale when set
@@ -315,6 +313,9 @@ constexpr long long kDrainCycles = kDefaultWaitCycles;
 
 template <int D, int NB, bool SHARED>
 struct USmem {
+    // Slots of the ring.  Split streams take alternate tiles, so an even number keeps a
+    // slot with its stream: what a stream's tile replaces is an earlier tile of its own,
+    // and a look at the slot's barrier cannot mistake one phase for another.
     static constexpr int kRing = SHARED ? 3 : 4;
     static constexpr int kBlocks = SHARED ? 2 : 1;             // row blocks of NB
     static constexpr int kRowsBlock = NB * kBlocks;
@@ -323,7 +324,7 @@ struct USmem {
     static constexpr int kHalf = kTile * D;                    // K or V codes of a tile
     static constexpr int kSlot = 2 * kHalf;
     static constexpr int kPlane = kTile * 64;                  // one plane of weights: rows of 64 bytes
-    static constexpr int kP = 3 * kPlane;
+    static constexpr int kP = NB == 64 ? 3 * kPlane : 2 * kPlane;  // (two: bf16 weights of a tree tile)
     static constexpr int kOffRing = 0;
     static constexpr int kOffP = kOffRing + kRing * kSlot;
     static constexpr int kOffQ8 = kOffP + 2 * kP;
@@ -331,18 +332,28 @@ struct USmem {
     static constexpr int kOffM = kOffQB + (kBlocks * kQB + 1023) / 1024 * 1024;  // float -m[2][NB], m = row reference
     static constexpr int kOffCorr = kOffM + 2 * NB * 4;        // float corr[2][NB], later coefficients
     static constexpr int kOffRed = kOffCorr + 2 * NB * 4;      // float red[2][4][NB]
-    static constexpr int kOffRow = kOffRed + 8 * NB * 4;       // int [2 * NB]: (node, head) of a row, in rows of D
-    static constexpr int kOffMask = kOffRow + 2 * NB * 4;      // uint32 [kRowsBlock][16]: mask rows
+    static constexpr int kOffRow = kOffRed + 8 * NB * 4;       // int [2][kRowsBlock]: (node, head) of a row, in rows of D
+    static constexpr int kOffMask = kOffRow + 2 * kRowsBlock * 4;      // uint32 [kRowsBlock][16]: mask rows
     static constexpr int kOffInfo = kOffMask + kRowsBlock * 64;  // float2 (k, v scale)[kRing][8]
     static constexpr int kOffBad = kOffInfo + kRing * 8 * 8;   // uint32 [2][4]: keys of a tree tile with a non-finite V
     static constexpr int kOffMisc = kOffBad + 32;              // see below, 256 bytes
     static constexpr int kOffBar = kOffMisc + 256;
-    // full[R] empty[R] s_full[2] p_full[2] pv_done[2] qfull checked[2] drain
-    static constexpr int kNumBar = 2 * kRing + 10;
+    // full[R] empty[R] s_full[2][2] p_full[2] pv_done[2] qfull seen checked[2] drain[2]
+    static constexpr int kNumBar = 2 * kRing + 14;
     static constexpr int kOffFirst = (kOffBar + kNumBar * 8 + 15) / 16 * 16;
     static int bytes(int B) { return kOffFirst + q8::offsets_bytes(B) + 1024; }  // + alignment slack
 };
 
+__device__ __forceinline__ float redux_max_nan(float v) {  // NaN if any is
+    float r;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float redux_max(float v) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -415,8 +426,11 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     using namespace umma;
     using L = USmem<D, NB, SHARED>;
     constexpr int R = L::kRing;
-    constexpr int kCols = NB == 64 ? 512 : 128;      // TMEM columns
-    constexpr uint32_t kS = 0, kO = 2 * NB;          // S_s at NB s; O_s (three planes) at 2 NB + 3 NB s
+    // TMEM: S of stream s at NB (2 s + buffer); O behind it, OP sums of NB columns a
+    // stream.  NB = 64: the third plane is added to the second's sum, so that two
+    // buffers of S have room.
+    constexpr int OP = NB == 64 ? 2 : 3, kCols = NB == 64 ? 512 : 256;
+    constexpr uint32_t kO = 4 * NB;
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const q8::Work w = a.work;
@@ -427,8 +441,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     const uint32_t ring_a = base_a + L::kOffRing, p_a = base_a + L::kOffP, q8_a = base_a + L::kOffQ8,
                    qb_a = base_a + L::kOffQB;
     const uint32_t bar_a = base_a + L::kOffBar;
-    const uint32_t full0 = bar_a, empty0 = full0 + 8 * R, s_full0 = empty0 + 8 * R, p_full0 = s_full0 + 16,
-                   pv_done0 = p_full0 + 16, qfull = pv_done0 + 16, checked0 = qfull + 8, drain = checked0 + 16;
+    const uint32_t full0 = bar_a, empty0 = full0 + 8 * R, s_full0 = empty0 + 8 * R, p_full0 = s_full0 + 32,
+                   pv_done0 = p_full0 + 16, qfull = pv_done0 + 16, seen = qfull + 8, checked0 = seen + 8, drain = checked0 + 16;
     float* s_m = reinterpret_cast<float*>(base + L::kOffM);
     float* s_corr = reinterpret_cast<float*>(base + L::kOffCorr);
     float* s_red = reinterpret_cast<float*>(base + L::kOffRed);
@@ -450,7 +464,10 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         for (int i = 0; i < L::kNumBar; ++i) mbar_init(bar_a + 8 * i, 1);
         mbar_init(p_full0, kUStream / 32);
         mbar_init(p_full0 + 8, kUStream / 32);
+        if (SHARED)  // a slot is free when both streams' products are through
+            for (int i = 0; i < R; ++i) mbar_init(empty0 + 8 * i, 2);
         mbar_init(qfull, kUSoftmax / 32);
+        mbar_init(seen, 2);
         mbar_init(checked0, 4);
         mbar_init(checked0 + 8, 4);
         mbar_init_fence();
@@ -469,11 +486,11 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const long long total = first.total(w);
-    const long long g_begin = w.cta_begin(total, blockIdx.x), g_end = w.cta_begin(total, blockIdx.x + 1);
+    const uint32_t total = first.total(w);
+    const uint32_t g_begin = w.cta_begin(total, blockIdx.x), g_end = w.cta_begin(total, blockIdx.x + 1);
     const int ppt = kTile / a.P;  // pages per tile
     const int rows_all = w.N * a.G;
-    long long g_failed = g_end;   // first segment whose results are not there
+    uint32_t g_failed = g_end;   // first segment whose results are not there
     bool gave_up = false;
 
     // tiles of a segment: n_pre of the prefix, then n_tree of the tree
@@ -483,108 +500,115 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         n_tree = s.t1 - s.t0 - n_pre;
     };
 
-    if (warp == kUMmaWarp) {
-        // -------------------------------- MMA warp --------------------------------
-        {
-            constexpr uint32_t id_s = idesc_f8(128, NB, 0, 0, 0, 0), id_pv = idesc_f8(128, 3 * NB, 0, 1, 1, 1);
-            constexpr uint32_t id_st = idesc_bf16(128, NB, 0, 0), id_pt = idesc_bf16(128, NB, 1, 1);
-            bool fail = false;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (!fail && !warp_wait(bar, parity, lim)) {
-                    fail = true;
-                    *flag = 1;
+    if (warp >= kUMmaWarp && warp < kUTmaWarp) {
+        // ------------------------ MMA warp of a stream ------------------------
+        const int st = warp - kUMmaWarp;
+        constexpr uint32_t id_s = idesc_f8(128, NB, 0, 0, 0, 0);
+        constexpr uint32_t id_pv = idesc_f8(128, (NB == 64 ? 2 : 3) * NB, 0, 1, 1, 1), id_p3 = idesc_f8(128, NB, 0, 1, 1, 1);
+        constexpr uint32_t id_st = idesc_bf16(128, NB, 0, 0), id_pt = idesc_bf16(128, NB, 1, 1);
+        const uint32_t s_full = s_full0 + 16 * st, p_full = p_full0 + 8 * st, pv_done = pv_done0 + 8 * st;
+        const uint32_t tS = tmem + 2 * st * NB, tO = tmem + kO + st * OP * NB, p = p_a + st * L::kP;
+        const uint32_t q8s = q8_a + (SHARED ? st : 0) * L::kQ8, qbs = qb_a + (SHARED ? st : 0) * L::kQB;
+        auto desc8 = [](uint32_t addr) {  // codes: rows of D bytes, either major
+            return D == 128 ? desc_sw128(addr, 16, 1024) : desc_sw64(addr, 0, 512);
+        };
+        bool fail = false;
+        int slot0 = 0;      // first slot of the segment
+        uint32_t p_par = 0;  // parity of the next step's weights
+        int seg = 0;
+        uint32_t g = g_begin;
+        for (q8::Segment s; !fail && q8::next_segment(w, first, g, g_end, s); g = s.end, ++seg) {
+            int n_pre, n_tree;
+            prefix_of(s, n_pre, n_tree);
+            // (the shuffles tell the compiler that these are the same in all lanes)
+            n_pre = __shfl_sync(0xffffffffu, n_pre, 0);
+            n_tree = __shfl_sync(0xffffffffu, n_tree, 0);
+            const int n = n_pre + n_tree, steps = SHARED ? n : (n + 1 - st) >> 1;
+            auto tile_of = [&](int i) { return SHARED ? i : 2 * i + st; };
+            auto slot_of = [&](int t) { return slot0 + t + max(0, t - n_pre); };
+            if (!warp_wait(qfull, (uint32_t)(seg & 1), lim)) fail = true;
+            if (lane == 0) mbar_arrive(seen);  // (a stream without steps must not fall segments behind)
+            // S runs up to two steps ahead of PV; whichever of the next S and the next PV
+            // has its inputs goes, S first when the stream has no scores left
+            int ns = 0, np = 0, spins = 0;
+            int sl = slot_of(tile_of(0));
+            uint32_t s_stage = sl % R, s_bar = full0 + 8 * s_stage, s_par = (sl / R) & 1;  // K of step ns
+            long long t_last = 0;
+            while (np < steps && !fail) {
+                const bool can_s = ns < steps && ns < np + 2 && mbar_test(s_bar, s_par);
+                bool can_pv = np < ns && mbar_test(p_full, p_par);
+                const int t = tile_of(np);
+                if (can_pv && t >= n_pre) {
+                    const int sv = slot_of(t) + 1;
+                    can_pv = mbar_test(full0 + 8 * (sv % R), (uint32_t)((sv / R) & 1));
                 }
-                return !fail;
-            };
-            auto desc8 = [](uint32_t addr) {  // codes: rows of D bytes, either major
-                return D == 128 ? desc_sw128(addr, 16, 1024) : desc_sw64(addr, 0, 512);
-            };
-            int slot0 = 0;           // first slot of the segment
-            int n_p[2] = {0, 0};     // steps of each stream so far
-            int seg = 0;
-            for (long long g = g_begin; g < g_end && !fail; ++seg) {
-                const q8::Segment s = q8::segment_at(w, first, g, g_end);
-                g += s.t1 - s.t0;
-                int n_pre, n_tree;
-                prefix_of(s, n_pre, n_tree);
-                // (the shuffles tell the compiler that these are the same in all lanes)
-                n_pre = __shfl_sync(0xffffffffu, n_pre, 0);
-                n_tree = __shfl_sync(0xffffffffu, n_tree, 0);
-                const int steps = (n_pre + n_tree) * (SHARED ? 2 : 1);
-                auto tile_of = [&](int x) { return SHARED ? x >> 1 : x; };
-                auto slot_of = [&](int t) { return slot0 + t + max(0, t - n_pre); };
-                auto issue_s = [&](int x) {
-                    const int t = tile_of(x), sl = slot_of(t), st = x & 1, blk = SHARED ? st : 0;
-                    if (!wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1))) return;
+                if (__all_sync(0xffffffffu, can_s) && (ns <= np + 1 || !__all_sync(0xffffffffu, can_pv))) {
                     fence_after_sync();
-                    const uint32_t k = ring_a + (sl % R) * L::kSlot, d = tmem + kS + st * NB;
-                    if (t < n_pre) {
-                        const uint64_t dk = desc8(k), dq = desc8(q8_a + blk * L::kQ8);
+                    const uint32_t k = ring_a + s_stage * L::kSlot, d = tS + (ns & 1) * NB;
+                    if (tile_of(ns) < n_pre) {
+                        const uint64_t dk = desc8(k), dq = desc8(q8s);
 #pragma unroll
                         for (int ks = 0; ks < D / 32; ++ks) {
                             mma_f8_warp(d, dk + 2 * ks, dq + 2 * ks, id_s, ks > 0);
                             mma_f8_warp(d, dk + 2 * ks, dq + ((NB * D) >> 4) + 2 * ks, id_s, 1);
                         }
                     } else {
-                        const uint64_t dk = desc_sw128(k, 16, 1024), dq = desc_sw128(qb_a + blk * L::kQB, 16, 1024);
+                        const uint64_t dk = desc_sw128(k, 16, 1024), dq = desc_sw128(qbs, 16, 1024);
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
                             mma_bf16_warp(d, dk + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
-                                     dq + (((ks >> 2) * (NB * 128) + (ks & 3) * 32) >> 4), id_st, ks > 0);
+                                          dq + (((ks >> 2) * (NB * 128) + (ks & 3) * 32) >> 4), id_st, ks > 0);
                     }
-                    commit_warp(s_full0 + 8 * st);
-                };
-                auto issue_pv = [&](int x) {
-                    const int t = tile_of(x), sl = slot_of(t), st = x & 1, i = x >> 1;
-                    const uint32_t d = tmem + kO + st * 3 * NB, p = p_a + st * L::kP;
+                    commit_warp(s_full + 8 * (ns & 1));
+                    ++ns;
+                    sl = slot_of(tile_of(ns));
+                    s_stage = sl % R;
+                    s_bar = full0 + 8 * s_stage;
+                    s_par = (sl / R) & 1;
+                    spins = 0;
+                } else if (__all_sync(0xffffffffu, can_pv)) {
+                    fence_after_sync();
+                    const int slv = slot_of(t);
+                    const uint32_t stage = slv % R;
                     if (t < n_pre) {
-                        const uint64_t dv = desc8(ring_a + (sl % R) * L::kSlot + L::kHalf);
+                        const uint64_t dv = desc8(ring_a + stage * L::kSlot + L::kHalf);
                         // NB = 64: a plane is one swizzle atom wide, the next one a plane behind;
                         // NB = 16: the planes share the 64 bytes of a key
                         const uint64_t dp = desc_sw64(p, L::kPlane, 512);
 #pragma unroll
                         for (int ks = 0; ks < kTile / 32; ++ks)
-                            mma_f8_warp(d, dv + ((ks * 32 * D) >> 4), dp + ((ks * 2048) >> 4), id_pv, i > 0 || ks > 0);
+                            mma_f8_warp(tO, dv + ((ks * 32 * D) >> 4), dp + ((ks * 2048) >> 4), id_pv, np > 0 || ks > 0);
+                        if constexpr (NB == 64) {
+                            const uint64_t d3 = desc_sw64(p + 2 * L::kPlane, 0, 512);
+#pragma unroll
+                            for (int ks = 0; ks < kTile / 32; ++ks)
+                                mma_f8_warp(tO + NB, dv + ((ks * 32 * D) >> 4), d3 + ((ks * 2048) >> 4), id_p3, 1);
+                        }
                     } else {
-                        const int sv = sl + 1;
-                        if (!wait(full0 + 8 * (sv % R), (uint32_t)((sv / R) & 1))) return;
                         // D = 64: the second half of the lanes repeats the first
-                        const uint64_t dv = desc_sw128(ring_a + (sv % R) * L::kSlot, D == 128 ? kTile * 128 : 0, 1024);
+                        const uint64_t dv = desc_sw128(ring_a + ((slv + 1) % R) * L::kSlot, D == 128 ? kTile * 128 : 0, 1024);
                         const uint64_t dp = desc_sw128(p, 0, 1024);
 #pragma unroll
                         for (int ks = 0; ks < kTile / 16; ++ks)
-                            mma_bf16_warp(d, dv + ((ks * 2048) >> 4), dp + ((ks * 2048) >> 4), id_pt, i > 0 || ks > 0);
+                            mma_bf16_warp(tO, dv + ((ks * 2048) >> 4), dp + ((ks * 2048) >> 4), id_pt, np > 0 || ks > 0);
                     }
-                    commit_warp(pv_done0 + 8 * st);
-                    if (!SHARED || st == 1) {
-                        commit_warp(empty0 + 8 * (sl % R));
-                        if (t >= n_pre) commit_warp(empty0 + 8 * ((sl + 1) % R));
-                    }
-                };
-                if (!wait(qfull, (uint32_t)(seg & 1))) break;
-                for (int x = 0; x < 2 && x < steps && !fail; ++x) issue_s(x);
-                for (int x = 0; x < steps && !fail; ++x) {
-                    const int st = x & 1;
-                    if (!wait(p_full0 + 8 * st, (uint32_t)((n_p[st] + (x >> 1)) & 1))) break;
-                    fence_after_sync();
-                    // keys that are not in yet must not hold up PV(x), which frees their slot
-                    bool s_first = false;
-                    if (x + 2 < steps) {
-                        const int sl = slot_of(tile_of(x + 2));
-                        s_first = __all_sync(0xffffffffu, mbar_try(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1)));
-                    }
-                    if (s_first) issue_s(x + 2);
-                    issue_pv(x);
-                    if (!s_first && x + 2 < steps && !fail) issue_s(x + 2);
+                    commit_warp(pv_done);
+                    commit_warp(empty0 + 8 * stage);
+                    if (t >= n_pre) commit_warp(empty0 + 8 * ((slv + 1) % R));
+                    ++np;
+                    p_par ^= 1;
+                    spins = 0;
+                } else if ((++spins & 63) == 0) {
+                    if (spins == 64) t_last = clock64();
+                    fail = __any_sync(0xffffffffu, clock64() - t_last > lim);
                 }
-                n_p[0] += (steps + 1) >> 1;
-                n_p[1] += steps >> 1;
-                slot0 += n_pre + 2 * n_tree;
             }
-            if (fail) {  // let everything in flight complete before TMEM is freed
-                commit_warp(drain);
-                mbar_wait(drain, 0, kDrainCycles);
-            }
+            if (fail) *flag = 1;
+            slot0 += n_pre + 2 * n_tree;
+        }
+        if (fail) {  // let everything in flight complete before TMEM is freed
+            commit_warp(drain + 8 * st);
+            mbar_wait(drain + 8 * st, 0, kDrainCycles);
         }
     } else if (warp == kUTmaWarp) {
         // -------------------------------- TMA warp --------------------------------
@@ -594,9 +618,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             if (sl >= R && !warp_wait(empty0 + 8 * (sl % R), (uint32_t)((sl / R - 1) & 1), lim)) fail = true;
             return !fail;
         };
-        for (long long g = g_begin; g < g_end && !fail;) {
-            const q8::Segment s = q8::segment_at(w, first, g, g_end);
-            g += s.t1 - s.t0;
+        uint32_t g = g_begin;
+        for (q8::Segment s; !fail && q8::next_segment(w, first, g, g_end, s); g = s.end) {
             int n_pre, n_tree;
             prefix_of(s, n_pre, n_tree);
             const int hk = s.unit / a.qblocks;
@@ -642,8 +665,10 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             const int pt = w.prefix_tiles(s.L);
             for (int u = n_pre; u < n_pre + n_tree && !fail; ++u) {
                 const int row = (s.t0 + u - pt) * kTile;
+                // both slots are free before either is filled: when K is in, V's slot holds
+                // no earlier tile on its way
+                if (!free_slot(slot) || !free_slot(slot + 1)) break;
                 for (int kv = 0; kv < 2; ++kv, ++slot) {
-                    if (!free_slot(slot)) break;
                     if (lane == 0) {
                         const int st = slot % R;
                         mbar_expect_tx(full0 + 8 * st, kTile * D * 2);
@@ -671,13 +696,13 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         const int stid = tid & (kUStream - 1);
         const int page_shift = 31 - __clz(a.P);
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lane_off + kS + st * NB;
-        const uint32_t tO = tmem + lane_off + kO + st * 3 * NB;
+        const uint32_t tO = tmem + lane_off + kO + st * OP * NB;
         float* m_row = s_m + st * NB;  // negated
         float* corr_row = s_corr + st * NB;
         uint8_t* p_row = base + L::kOffP + st * L::kP;
         const float scale = a.scale_log2;
-        int n_s = 0;       // steps of this stream before the segment
+        int n_s = 0;             // steps of this stream before the segment
+        int n_buf[2] = {0, 0};   // of them in each buffer of S
         int slot0 = 0;
         int n_checked = 0;  // tree tiles before the segment (shared streams)
         // Q rows of a segment's block, 16 bytes a load; rows behind its end are zero
@@ -697,28 +722,14 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 }
             }
         };
-        if (g_begin < g_end) load_q(q8::segment_at(w, first, g_begin, g_end));
-        for (long long g = g_begin; g < g_end;) {
-            const q8::Segment s = q8::segment_at(w, first, g, g_end);
-            const long long g_seg = g;
-            g += s.t1 - s.t0;
-            int n_pre, n_tree;
-            prefix_of(s, n_pre, n_tree);
-            const int n = n_pre + n_tree;
-            const int steps = SHARED ? n : (n + 1 - st) >> 1;  // of this stream
+        float kq = 0.f;  // scale / the factor of Q's planes
+        // What a segment needs before its first step, in two parts around a barrier of
+        // all softmax threads: largest |q| and rows' addresses; then Q into shared memory
+        // (bf16 for the tree's tiles, two e4m3 planes for the pages'), which the MMA warp
+        // waits for.
+        auto begin_segment = [&](const q8::Segment& s, int seg) {
             const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * L::kRowsBlock;
-            const int nrows = min(L::kRowsBlock, rows_all - row0);
-
-            // Q (its rows were asked for at the end of the last segment) into shared memory:
-            // bf16 for the tree's tiles, two e4m3 planes for the pages'.
             float qmax = 0.f;
-            if (n_tree) {
-                const uint32_t* mask = reinterpret_cast<const uint32_t*>(a.mask);
-                for (int i = tid; i < L::kRowsBlock * 16; i += kUSoftmax) {
-                    const int r = i >> 4, word = i & 15;
-                    if (word < 2 * a.W) s_mask[i] = r < nrows ? __ldg(mask + (size_t)((row0 + r) / a.G) * (2 * a.W) + word) : 0u;
-                }
-            }
 #pragma unroll
             for (int i = 0; i < QN; ++i) {
                 const uint32_t x[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
@@ -730,19 +741,23 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 }
             }
             qmax = redux_max(qmax);
-            if (lane == 0) s_qmax[warp] = qmax;
-            if (stid < NB) m_row[stid] = INFINITY;
-            bar_sync(3, kUSoftmax);  // the last segment's results are out, its Q is free
+            if (lane == 0) s_qmax[(seg & 1) * 8 + warp] = qmax;
             if (tid < L::kRowsBlock) {
                 const int gr = row0 + tid;
-                s_row[tid] = gr / a.G * a.Hq + hk * a.G + gr % a.G;
+                s_row[(seg & 1) * L::kRowsBlock + tid] = gr / a.G * a.Hq + hk * a.G + gr % a.G;
             }
+        };
+        auto take_q = [&](const q8::Segment& s, int seg) {
+            const int row0 = s.unit % a.qblocks * L::kRowsBlock;
+            const int nrows = min(L::kRowsBlock, rows_all - row0);
+            const bool tree = s.t1 > w.prefix_tiles(s.L);
+            float qmax = 0.f;
 #pragma unroll
-            for (int i = 0; i < kUSoftmax / 32; ++i) qmax = fmaxf(qmax, s_qmax[i]);
+            for (int i = 0; i < kUSoftmax / 32; ++i) qmax = fmaxf(qmax, s_qmax[(seg & 1) * 8 + i]);
             // factor 2^k with qmax * 2^k in [128, 256)
             const int qe = q8::clamp_int(254 + 7 - (int)(__float_as_uint(qmax) >> 23), 1, 253);
             const float qf = __uint_as_float((uint32_t)qe << 23);
-            const float kq = scale * __uint_as_float((uint32_t)(254 - qe) << 23);  // scale / qf
+            kq = scale * __uint_as_float((uint32_t)(254 - qe) << 23);
 #pragma unroll
             for (int i = 0; i < QN; ++i) {
                 const int c = tid + i * kUSoftmax, r = c / CH, ch = c % CH;
@@ -767,17 +782,44 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 };
                 *reinterpret_cast<uint2*>(q8p + at8(rb)) = make_uint2(join16(hi[0], hi[1]), join16(hi[2], hi[3]));
                 *reinterpret_cast<uint2*>(q8p + at8(NB + rb)) = make_uint2(join16(lo[0], lo[1]), join16(lo[2], lo[3]));
-                if (n_tree)
+                if (tree)
                     *reinterpret_cast<uint4*>(base + L::kOffQB + blk * L::kQB + sw128_offset(rb, ch, NB)) = qv[i];
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
+            if (tree) {
+                const uint32_t* mask = reinterpret_cast<const uint32_t*>(a.mask);
+                for (int i = tid; i < L::kRowsBlock * 16; i += kUSoftmax) {
+                    const int r = i >> 4, word = i & 15;
+                    if (word < 2 * a.W) s_mask[i] = r < nrows ? __ldg(mask + (size_t)((row0 + r) / a.G) * (2 * a.W) + word) : 0u;
+                }
+            }
+        };
+        uint32_t g = g_begin;
+        q8::Segment s;
+        bool more = q8::next_segment(w, first, g, g_end, s);
+        if (more) {
+            load_q(s);
+            begin_segment(s, 0);
+            bar_sync(3, kUSoftmax);
+            take_q(s, 0);
+            bar_sync(3, kUSoftmax);
+        }
+        for (int seg = 0; more; ++seg) {
+            int n_pre, n_tree;
+            prefix_of(s, n_pre, n_tree);
+            const int n = n_pre + n_tree;
+            const int steps = SHARED ? n : (n + 1 - st) >> 1;  // of this stream
+            const int row0 = s.unit % a.qblocks * L::kRowsBlock;
+            const int nrows = min(L::kRowsBlock, rows_all - row0);
+            if (stid < NB) m_row[stid] = INFINITY;
+
             float l[CW];
 #pragma unroll
             for (int c = 0; c < CW; ++c) l[c] = 0.f;
             float v_ref = 0.f;
-            bool fail = false, late = false;
+            bool fail = false;
             const int pt = w.prefix_tiles(s.L);
             const int i_tree = min(steps, SHARED ? n_pre : (n_pre + 1 - st) >> 1);  // first step of the tree's
             // Rows of this thread that see tree row m0 + lane.
@@ -798,10 +840,11 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 constexpr bool tree = decltype(is_tree)::value;
                 const int t = SHARED ? i : 2 * i + st;
                 const int sl = slot0 + t + (tree ? t - n_pre : 0);
-                bool ok = warp_wait(s_full0 + 8 * st, (uint32_t)((n_s + i) & 1), lim);
+                const uint32_t tS = tmem + lane_off + (2 * st + (i & 1)) * NB;
+                bool ok = warp_wait(s_full0 + 8 * (2 * st + (i & 1)), (uint32_t)((n_buf[i & 1] + (i >> 1)) & 1), lim);
                 float kc = kq, vs = 1.f;
                 bool valid, bad_v = false;
-                uint64_t seen = ~0ull;  // rows that see the key
+                uint64_t sees = ~0ull;  // rows that see the key
                 if constexpr (!tree) {
                     // the slot is in since the scores are; this wait makes the scales visible
                     ok = warp_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), lim) && ok;
@@ -809,7 +852,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     valid = sc.y > 0.f && (s.t0 + t) * kTile + key < s.L;
                     kc = kq * sc.x;
                     vs = valid ? sc.y : 0.f;
-                    seen = valid ? seen : 0;
+                    sees = valid ? sees : 0;
                 } else {
                     kc = scale;
                     ok = warp_wait(full0 + 8 * ((sl + 1) % R), (uint32_t)(((sl + 1) / R) & 1), lim) && ok;
@@ -817,7 +860,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     valid = m < w.N;
                     // A tree row whose V is not finite: 0 * inf of a query row that does not see
                     // it would spoil that one, so its V counts as zero and rows that see it get
-                    // NaN.  Of two streams that share the tile stream 0 looks and clears.
+                    // NaN.  Of two streams that share the tile stream 0 looks.
                     if (!SHARED || st == 0) {
                         const uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
 #pragma unroll 4
@@ -837,11 +880,10 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         ok = warp_wait(checked0 + 8 * (k & 1), (uint32_t)((k >> 1) & 1), lim) && ok;
                         bad_v = s_bad[(k & 1) * 4 + quarter] >> lane & 1;
                     }
-                    seen = seen64(m - lane);
-                    if (!valid) seen = 0;
+                    sees = seen64(m - lane);
+                    if (!valid) sees = 0;
                 }
                 fence_after_sync();
-                if ((!ok || late) && lane == 0) s_fail[st] = 1;
                 // Eight columns of scores from c0 on, in log2 units, less the rows'
                 // references or as they are.
                 auto scores8 = [&](int c0, bool relative, float* x) {
@@ -860,52 +902,118 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 // The scores are formed twice from TMEM, for the check and for the weights, WX
                 // columns at a time: held in between they would not fit next to the sums, and
                 // what the compiler then spills does not fit L1 next to this much shared memory.
-                constexpr int WX = tree ? 8 : (CW < 16 ? CW : 16);
-                float x[WX];
-                auto load_x = [&](int c0) {
-                    if constexpr (WX == 32)
-                        tmem_ld32(tS + c0, x);
-                    else if constexpr (WX == 16)
-                        tmem_ld16(tS + c0, x);
-                    else
-                        tmem_ld8(tS + c0, x);
-                    tmem_wait_ld();
+                auto relative = [&](int c0, auto& x, int n) {
 #pragma unroll
-                    for (int e = 0; e < WX; e += 4) {
+                    for (int e = 0; e < n; e += 4) {
                         const float4 m = *reinterpret_cast<const float4*>(m_row + c0 + e);
                         fma2(x[e], x[e + 1], x[e], x[e + 1], kc, m.x, m.y);
                         fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], kc, m.z, m.w);
                     }
                     if (partial) {
 #pragma unroll
-                        for (int e = 0; e < WX; ++e) x[e] = valid ? x[e] : -INFINITY;
+                        for (int e = 0; e < n; ++e) x[e] = valid ? x[e] : -INFINITY;
                     }
                 };
-                bool move = !ok || late || i == 0 || vs > v_ref;
-                // (i, not move, decides here: TMEM loads take whole warps)
-                {
-                    if (i > 0) {
-                        float top = -INFINITY;
-                        if constexpr (!tree) {
+                // the stream's last PV: P and O are free behind it
+                if (i > 0) ok = warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + i - 1) & 1), lim) && ok;
+                if (!ok && lane == 0) s_fail[st] = 1;
+                // Weights, their sums and their planes; returns the largest score.  They are
+                // written on the old references; where a score turns out to lie too far above
+                // them they are taken back and written again.
+                auto weights = [&]() -> float {
+                    const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
+                    float top = -INFINITY;
+                    if constexpr (!tree) {
+                        // eight columns at a time, the next ones on their way from TMEM
+                        float x[2][8];
+                        tmem_ld8(tS, x[0]);
 #pragma unroll
-                            for (int c0 = 0; c0 < CW; c0 += WX) {
-                                load_x(c0);
+                        for (int c0 = 0; c0 < CW; c0 += 8) {
+                            float(&y)[8] = x[(c0 >> 3) & 1];
+                            tmem_wait_ld();
+                            if (c0 + 8 < CW) tmem_ld8(tS + c0 + 8, x[((c0 >> 3) & 1) ^ 1]);
+                            relative(c0, y, 8);
+                            uint32_t pw[3][2];
 #pragma unroll
-                                for (int e = 0; e < WX; e += 2) top = max3(top, x[e], x[e + 1]);
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t two[2][3];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int c = 4 * e + 2 * k;
+                                    top = max3(top, y[c], y[c + 1]);
+                                    const float p0 = exp2_approx(y[c]), p1 = exp2_approx(y[c + 1]);
+                                    add2(l[c0 + c], l[c0 + c + 1], p0, p1);
+                                    float w0, w1;
+                                    mul2(w0, w1, p0, p1, f);
+                                    split_weights(w0, w1, two[k]);
+                                }
+#pragma unroll
+                                for (int p = 0; p < 3; ++p) pw[p][e] = __byte_perm(two[0][p], two[1][p], 0x7531);
                             }
-                        } else {
-#pragma unroll 1
-                            for (int c0 = 0; c0 < CW; c0 += 8) {
-                                scores8(c0, true, x);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) top = fmaxf(top, (seen >> (c0 + e)) & 1 ? x[e] : -INFINITY);
+                            for (int p = 0; p < 3; ++p) {
+                                // NB = 64: one plane of 64 bytes a key after the other; NB = 16:
+                                // the planes are the key's 16-byte chunks 0, 1, 2
+                                const int chunk = NB == 64 ? c0 >> 4 : p;
+                                *reinterpret_cast<uint2*>(p_row + (NB == 64 ? p * L::kPlane : 0) + key * 64 +
+                                                          ((chunk ^ ((key >> 1) & 3)) << 4) + (c0 & 8)) =
+                                    make_uint2(pw[p][0], pw[p][1]);
                             }
                         }
-                        move = move || top > kTau;
+                    } else {
+#pragma unroll
+                        for (int c0 = 0; c0 < CW; c0 += 8) {
+                            uint32_t h[4];
+                            float x[8];
+                            scores8(c0, true, x);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool see0 = (sees >> (c0 + 2 * e)) & 1, see1 = (sees >> (c0 + 2 * e + 1)) & 1;
+                                const float x0 = see0 ? x[2 * e] : -INFINITY, x1 = see1 ? x[2 * e + 1] : -INFINITY;
+                                top = max3(top, x0, x1);
+                                const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                                h[e] = pack_bf16x2(p0 * f, p1 * f);
+                                add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], bad_v && see0 ? NAN : p0, bad_v && see1 ? NAN : p1);
+                            }
+                            *reinterpret_cast<uint4*>(p_row + key * 128 + (((c0 >> 3) ^ (key & 7)) << 4)) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
+                    return top;
+                };
+                bool move = true;
+                if (i > 0) {
+                    const float top = weights();
                     __syncwarp();
+                    move = named_barrier_or(1 + st, kUStream, !ok || vs > v_ref || top > kTau);
+                    // l + p - p is off by half a unit of l + p at most, and p falls to at most 1
+                    // on the new references: the error is one rounding of the row's sum.
+                    if (move) {
+                        if constexpr (!tree) {
+#pragma unroll
+                            for (int c0 = 0; c0 < CW; c0 += 8) {
+                                float y[8];
+                                tmem_ld8(tS + c0, y);
+                                tmem_wait_ld();
+                                relative(c0, y, 8);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) l[c0 + e] -= exp2_approx(y[e]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c0 = 0; c0 < CW; c0 += 8) {
+                                float x[8];
+                                scores8(c0, true, x);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) l[c0 + e] -= (sees >> (c0 + e)) & 1 ? exp2_approx(x[e]) : 0.f;
+                            }
+                        }
+                    }
+                } else {
+                    __syncwarp();
+                    move = named_barrier_or(1 + st, kUStream, true);
                 }
-                if (named_barrier_or(1 + st, kUStream, move)) {
+                if (move) {
                     // The references move: largest score per row over the tile's keys.
 #pragma unroll 1
                     for (int c0 = 0; c0 < CW; c0 += 8) {
@@ -913,21 +1021,22 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         scores8(c0, false, y);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const float m = redux_max((seen >> (c0 + e)) & 1 ? y[e] : -INFINITY);
+                            const float m = redux_max_nan((sees >> (c0 + e)) & 1 ? y[e] : -INFINITY);
                             if (lane == e) s_red[(st * 4 + quarter) * NB + c0 + e] = m;
                         }
                     }
                     const float vm = redux_max(vs);
                     if (lane == 0) s_vmax[st * 4 + quarter] = vm;
-                    // the stream's last PV: O is free behind it
-                    if (i > 0 && !warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + i - 1) & 1), lim)) s_fail[st] = 1;
                     bar_sync(1 + st, kUStream);
                     const bool fail = s_fail[st] != 0;
                     if (stid < NB) {
                         const float* r = s_red + st * 4 * NB + stid;
                         const float m0 = -m_row[stid];
-                        const float m1 = fmaxf(max3(r[0], r[NB], r[2 * NB]), fmaxf(r[3 * NB], m0));
-                        corr_row[stid] = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);
+                        // (a NaN score makes the reference, and with it the row, NaN)
+                        const float m1 = max_nan(max_nan(max_nan(r[0], r[NB]), max_nan(r[2 * NB], r[3 * NB])), m0);
+                        // (what is 2^100 too small to count is dropped: no weight that a
+                        // factor above 0 belongs to was infinite)
+                        corr_row[stid] = m0 == -INFINITY || m0 - m1 < -100.f ? 0.f : exp2f(m0 - m1);
                         m_row[stid] = -m1;
                     }
                     float v1 = fmaxf(fmaxf(s_vmax[st * 4], s_vmax[st * 4 + 1]), fmaxf(s_vmax[st * 4 + 2], s_vmax[st * 4 + 3]));
@@ -940,17 +1049,21 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 #pragma unroll
                         for (int c = 0; c < CW; c += 4) {
                             const float4 r = *reinterpret_cast<const float4*>(corr_row + c);
-                            l[c] *= r.x; l[c + 1] *= r.y; l[c + 2] *= r.z; l[c + 3] *= r.w;
+                            // (0, not l * 0: where p was infinite l is none)
+                            l[c] = r.x == 0.f ? 0.f : l[c] * r.x;
+                            l[c + 1] = r.y == 0.f ? 0.f : l[c + 1] * r.y;
+                            l[c + 2] = r.z == 0.f ? 0.f : l[c + 2] * r.z;
+                            l[c + 3] = r.w == 0.f ? 0.f : l[c + 3] * r.w;
                         }
                         fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < CW; c += 8) {
-                            float o[3][8];
+                            float o[OP][8];
 #pragma unroll
-                            for (int p = 0; p < 3; ++p) tmem_ld8(tO + p * NB + c, o[p]);
+                            for (int p = 0; p < OP; ++p) tmem_ld8(tO + p * NB + c, o[p]);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int p = 0; p < 3; ++p) {
+                            for (int p = 0; p < OP; ++p) {
                                 uint32_t ow[8];
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) ow[e] = __float_as_uint(o[p][e] * (corr_row[c + e] * vf));
@@ -959,13 +1072,11 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         }
                         tmem_wait_st();
                     }
+                    weights();
                 }
-                // the stream's last PV: P is free behind it
-                if (i > 0) late = !warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + i - 1) & 1), lim);
                 // A key that is not there has no V either: whatever the slot holds (stale
-                // codes may be NaN) is cleared.  When two streams share the tile, stream 0
-                // does it: its PV comes first.
-                if (!SHARED || st == 0) {
+                // codes may be NaN) is cleared, by each stream that multiplies it.
+                {
                     if (!tree && !valid) {
                         uint4* v = reinterpret_cast<uint4*>(base + L::kOffRing + (sl % R) * L::kSlot + L::kHalf + key * D);
 #pragma unroll
@@ -979,59 +1090,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     }
                 }
                 __syncwarp();
-                // weights, their sums, and their planes
-                const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
-                if constexpr (!tree) {
-                    constexpr int W = CW < 16 ? CW : 16;
-#pragma unroll
-                    for (int c0 = 0; c0 < CW; c0 += W) {
-                        if (c0 % WX == 0) load_x(c0);
-                        uint32_t pw[3][W / 4];
-#pragma unroll
-                        for (int e = 0; e < W / 4; ++e) {
-                            uint32_t two[2][3];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int c = c0 + 4 * e + 2 * k;
-                                const float p0 = exp2_approx(x[c % WX]), p1 = exp2_approx(x[c % WX + 1]);
-                                add2(l[c], l[c + 1], p0, p1);
-                                float w0, w1;
-                                mul2(w0, w1, p0, p1, f);
-                                split_weights(w0, w1, two[k]);
-                            }
-#pragma unroll
-                            for (int p = 0; p < 3; ++p) pw[p][e] = __byte_perm(two[0][p], two[1][p], 0x7531);
-                        }
-                        const int col = c0;
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) {
-                            // NB = 64: one plane of 64 bytes a key after the other; NB = 16:
-                            // the planes are the key's 16-byte chunks 0, 1, 2
-                            const int chunk = NB == 64 ? col >> 4 : p;
-                            uint8_t* to = p_row + (NB == 64 ? p * L::kPlane : 0) + key * 64 +
-                                          ((chunk ^ ((key >> 1) & 3)) << 4) + (col & 15);
-                            if constexpr (W == 16)
-                                *reinterpret_cast<uint4*>(to) = make_uint4(pw[p][0], pw[p][1], pw[p][2], pw[p][3]);
-                            else
-                                *reinterpret_cast<uint2*>(to) = make_uint2(pw[p][0], pw[p][1]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int c0 = 0; c0 < CW; c0 += 8) {
-                        uint32_t h[4];
-                        scores8(c0, true, x);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const bool see0 = (seen >> (c0 + 2 * e)) & 1, see1 = (seen >> (c0 + 2 * e + 1)) & 1;
-                            const float p0 = see0 ? exp2_approx(x[2 * e]) : 0.f, p1 = see1 ? exp2_approx(x[2 * e + 1]) : 0.f;
-                            h[e] = pack_bf16x2(p0 * f, p1 * f);
-                            add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], bad_v && see0 ? NAN : p0, bad_v && see1 ? NAN : p1);
-                        }
-                        *reinterpret_cast<uint4*>(p_row + key * 128 + ((((c0) >> 3) ^ (key & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                }
                 fence_async_smem();
                 fence_before_sync();
                 __syncwarp();
@@ -1064,19 +1122,30 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 }
             }
             if (stid == 0) s_vref[st] = v_ref;
-            if (g < g_end) load_q(q8::segment_at(w, first, g, g_end));
-            bool ok = !fail && !late;
+            // the next segment's Q, asked for now; its products start while this one's
+            // results go out
+            q8::Segment next = s;
+            g = s.end;
+            more = q8::next_segment(w, first, g, g_end, next);
+            if (more) {
+                load_q(next);
+                begin_segment(next, seg + 1);
+            }
+            bool ok = !fail && warp_wait(seen, (uint32_t)(seg & 1), lim);
             if (ok && steps > 0) ok = warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + steps - 1) & 1), lim);
             __syncwarp();
             if (named_barrier_or(3, kUSoftmax, !ok)) {
                 gave_up = true;
-                g_failed = g_seg;
+                g_failed = s.begin + w.V + s.t0;
                 break;
             }
             fence_after_sync();
             n_s += steps;
+            n_buf[0] += (steps + 1) >> 1;
+            n_buf[1] += steps >> 1;
             slot0 += n_pre + 2 * n_tree;
             n_checked += n_tree;
+            if (more) take_q(next, seg + 1);
 
             // Each row's coefficients.  Split streams: relative to the larger reference.
             const bool whole = s.whole();
@@ -1112,52 +1181,78 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 if (!SHARED) s_corr[NB + tid] = c1;
             }
             bar_sync(3, kUSoftmax);
-            // O^T: this thread's output column of some rows: of the stream's own (shared),
-            // or of a share of the block's
+            // O^T: this thread's output column of the stream's own rows (shared) or of half
+            // of the block's
+            constexpr int COLS = SHARED ? NB : NB / 2;
+            const int first_row = st * COLS, o_col = SHARED ? 0 : first_row;
+            const uint32_t oa = tmem + lane_off + kO + (SHARED ? st * OP * NB : 0) + o_col, ob = tmem + lane_off + kO + OP * NB + o_col;
             const int n_b = SHARED ? 0 : n >> 1;               // steps behind O_1
             const bool all_a = n_pre > 0, all_b = n_pre > 1;   // prefix tiles among a stream's: all planes are there
-            constexpr int COLS = SHARED ? NB : NB / 2;
-            const int col0 = SHARED ? 0 : st * COLS;
-            const uint32_t oa = tmem + lane_off + kO + (SHARED ? st * 3 * NB : 0) + col0, ob = tmem + lane_off + kO + 3 * NB + col0;
-            const int first_row = (SHARED ? st * NB : 0) + col0;
-            if (first_row < nrows) {
+            const int* rows = s_row + (seg & 1) * L::kRowsBlock + first_row;
+            uint16_t* out = static_cast<uint16_t*>(a.out) + (size_t)s.b * w.N * a.Hq * D + key;
+            float* part_o = a.part_o + (part + first_row) * D + key;
+            if (first_row < nrows && (D == 128 || quarter < 2)) {
 #pragma unroll 1
                 for (int c = 0; c < COLS; c += 8) {
-                    float va[3][8], vb[3][8];
+                    float va[OP][8], vb[OP][8];
                     tmem_ld8(oa + c, va[0]);
                     if (all_a) {
-                        tmem_ld8(oa + NB + c, va[1]);
-                        tmem_ld8(oa + 2 * NB + c, va[2]);
+#pragma unroll
+                        for (int p = 1; p < OP; ++p) tmem_ld8(oa + p * NB + c, va[p]);
                     }
                     if (n_b > 0) tmem_ld8(ob + c, vb[0]);
-                    if (all_b && !SHARED) {
-                        tmem_ld8(ob + NB + c, vb[1]);
-                        tmem_ld8(ob + 2 * NB + c, vb[2]);
+                    if (!SHARED && all_b) {
+#pragma unroll
+                        for (int p = 1; p < OP; ++p) tmem_ld8(ob + p * NB + c, vb[p]);
                     }
+                    const float4 ca[2] = {*reinterpret_cast<const float4*>(s_corr + first_row + c),
+                                          *reinterpret_cast<const float4*>(s_corr + first_row + c + 4)};
+                    const int4 rr[2] = {*reinterpret_cast<const int4*>(rows + c), *reinterpret_cast<const int4*>(rows + c + 4)};
                     tmem_wait_ld();
+                    float o[8];
+                    const float* cf = &ca[0].x;
+                    const int* rf = &rr[0].x;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int r = first_row + c + e;  // row of the block
-                        if (r >= nrows || key >= D) continue;
-                        float o = (va[0][e] + (all_a ? va[1][e] + va[2][e] : 0.f)) * s_corr[r];
-                        if (n_b > 0) o = fmaf(vb[0][e] + (all_b ? vb[1][e] + vb[2][e] : 0.f), s_corr[NB + r], o);
-                        if (whole)
-                            store1(static_cast<uint16_t*>(a.out) + ((size_t)s.b * w.N * a.Hq + s_row[r]) * D + key, o);
-                        else
-                            a.part_o[(part + r) * D + key] = o;
+                        o[e] = va[0][e];
+                        if (all_a) {
+#pragma unroll
+                            for (int p = 1; p < OP; ++p) o[e] += va[p][e];
+                        }
+                        o[e] *= cf[e];
+                    }
+                    if (n_b > 0) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float y = vb[0][e];
+                            if (all_b) {
+#pragma unroll
+                                for (int p = 1; p < OP; ++p) y += vb[p][e];
+                            }
+                            o[e] = fmaf(y, s_corr[NB + first_row + c + e], o[e]);
+                        }
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (first_row + c + e < nrows) store1(out + (size_t)(uint32_t)rf[e] * D, o[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) part_o[(c + e) * D] = o[e];
                     }
                 }
             }
             fence_before_sync();
+            bar_sync(3, kUSoftmax);  // O is free for the next segment's products
+            s = next;
         }
     }
     const bool bad = __syncthreads_or(gave_up);
     if (bad) {
         // what this CTA was to give from the segment on that it could not finish
         if (tid == 0) atomicExch(&g_wait_gave_up, 1);
-        for (long long g = g_failed; g < g_end && tid < kUSoftmax;) {
-            const q8::Segment s = q8::segment_at(w, first, g, g_end);
-            g += s.t1 - s.t0;
+        uint32_t g = g_failed;
+        for (q8::Segment s; tid < kUSoftmax && q8::next_segment(w, first, g, g_end, s); g = s.end) {
             const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * L::kRowsBlock;
             const int nrows = min(L::kRowsBlock, rows_all - row0);
             if (!s.whole()) {
@@ -1191,16 +1286,15 @@ __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const Attn
     pdl_wait();
     pdl_trigger();
     q8::tile_offsets(w, a.kv_len, first);
-    const long long total = first.total(w);
+    const uint32_t total = first.total(w);
     const int c = blockIdx.x + 1;
-    const long long g = w.cta_begin(total, c);
+    const uint32_t g = w.cta_begin(total, c);
     if (g >= total || w.cta_begin(total, c + 1) == g) return;  // an empty share
     const q8::Segment s = q8::segment_at(w, first, g, g);
     if (s.t0 == 0) return;                         // the boundary falls between units
-    const long long u0 = g - s.t0, u1 = u0 + s.tiles;
-    const int c0 = w.cta_of(total, u0);            // share that begins the unit
+    const int c0 = w.cta_of(total, s.begin + w.V);  // share that begins the unit
     if (c0 != w.cta_of(total, g - 1)) return;      // an earlier boundary is the first
-    const int c1 = w.cta_of(total, u1 - 1);
+    const int c1 = w.cta_of(total, s.end - 1);
     const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * rows_block;
     const int i = blockIdx.y * (kMergeThreads / (D / 4)) + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
     if (i >= min(rows_block, w.N * a.G - row0)) return;
@@ -1243,17 +1337,16 @@ __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const Attn
 }
 
 struct Plan {
-    int rows, keys, ctas;
-    bool shared;
+    int rows, keys, setup, ctas;
 };
 // Rows per block, by the rows a KV head has: 16 (plain decoding), 64, or 128 in
 // two streams.
 Plan plan_q8(medusa_dtype dtype, int N, int G) {
     const int rows = N * G, sms = sm_count();
-    if (dtype == MEDUSA_F32) return Plan{kRows, kKeys, 2 * sms, false};
-    if (rows <= 16) return Plan{16, kTile, sms, false};
-    if (rows <= 64) return Plan{64, kTile, sms, false};
-    return Plan{128, kTile, sms, true};
+    if (dtype == MEDUSA_F32) return Plan{kRows, kKeys, 1, 2 * sms};
+    if (rows <= 16) return Plan{16, kTile, kSetup, sms};
+    if (rows <= 64) return Plan{64, kTile, kSetup, sms};
+    return Plan{128, kTile, kSetup, sms};
 }
 
 int check_attn_q8(int B, int N, int Hq, int Hkv, int D, int P, int n_pages, int M) {
@@ -1367,8 +1460,8 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     a.part_ml = (float2*)((float*)ws + (size_t)2 * p.ctas * p.rows * D);
     a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.P = P; a.M = M; a.n_pages = n_pages; a.W = (N + 63) / 64;
     a.qblocks = (N * a.G + p.rows - 1) / p.rows;
-    a.work = q8::Work{B, N, Hkv * a.qblocks, p.keys, M * P, p.ctas};
-    if ((long long)B * a.work.U * (((long long)M * P + p.keys - 1) / p.keys + (N + p.keys - 1) / p.keys) > 0x7fffffffll)
+    a.work = q8::Work{B, N, Hkv * a.qblocks, p.keys, p.setup, M * P, p.ctas};
+    if ((long long)B * a.work.U * (((long long)M * P + p.keys - 1) / p.keys + (N + p.keys - 1) / p.keys + p.setup) > 0x7fffffffll)
         return fail(MEDUSA_ERR_UNSUPPORTED, "tree_attention_q8: %d sequences of up to %lld tokens are too many tiles", B,
                     (long long)M * P);
     a.scale_log2 = scale * kLog2e;

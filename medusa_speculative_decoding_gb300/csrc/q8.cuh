@@ -60,24 +60,29 @@ __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo 
 // Attention work.  A unit is (sequence, KV head, block of query rows); its keys
 // are cut into tiles of T: first the prefix's, then the tree's.  The tiles of all
 // units, laid end to end, are shared out evenly over the CTAs (the lengths are
-// known on the device only, so the host cannot choose a split).  A CTA's share
-// is a run of segments, each a range of one unit's tiles; a unit that several
-// CTAs share leaves one partial result per CTA, joined by a merge kernel.
+// known on the device only, so the host cannot choose a split); a unit counts V
+// tiles more, in front of its own, for what taking it up and handing its result out
+// costs.  A CTA's share is a run of segments, each a range of one unit's tiles; a
+// unit that several CTAs share leaves one partial result per CTA, joined by a merge
+// kernel.
 struct Work {
-    int B, N, U, T, cap, ctas;  // U units per sequence, T keys per tile, cap slots per sequence
+    int B, N, U, T, V, cap, ctas;  // U units per sequence, T keys per tile, cap slots per sequence
     __device__ __forceinline__ int len(const int32_t* kv_len, int b) const { return clamp_int(kv_len[b], 0, cap); }
     __device__ __forceinline__ int prefix_tiles(int L) const { return (L + T - 1) / T; }
     __device__ __forceinline__ int tree_tiles() const { return (N + T - 1) / T; }
-    __device__ __forceinline__ int tiles(int L) const { return prefix_tiles(L) + tree_tiles(); }
-    __device__ __forceinline__ long long cta_begin(long long total, int c) const { return total * c / ctas; }
-    // the CTA whose share holds tile g: the largest c with total * c / ctas <= g
-    __device__ __forceinline__ int cta_of(long long total, long long g) const {
-        return (int)(((g + 1) * ctas - 1) / total);
+    __device__ __forceinline__ int span(int L) const { return V + prefix_tiles(L) + tree_tiles(); }
+    // total * c / ctas, in 32 bits
+    __device__ __forceinline__ uint32_t cta_begin(uint32_t total, int c) const {
+        const uint32_t q = total / (uint32_t)ctas, r = total - q * (uint32_t)ctas;
+        return q * (uint32_t)c + r * (uint32_t)c / (uint32_t)ctas;
+    }
+    // the CTA whose share holds position g: the largest c with total * c / ctas <= g
+    __device__ __forceinline__ int cta_of(uint32_t total, uint32_t g) const {
+        return (int)((((unsigned long long)g + 1) * ctas - 1) / total);
     }
 };
 
-// Two tables in shared memory: first[b] (b <= B), the number of tiles of sequences
-// before b, and rest[b], the length of b less the whole tiles before its last one.
+// Two tables in shared memory: first[b] (b <= B), where the units of sequence b begin, and rest[b], the length of b less the whole tiles before its last one.
 // (Tiles are counted in 32 bits: the entry point bounds their number.)
 __host__ __device__ __forceinline__ int offsets_bytes(int B) { return (B + 1) * 4 + (B + 3) / 4 * 4; }
 struct Offsets {
@@ -85,7 +90,7 @@ struct Offsets {
     uint8_t* rest;
     __device__ __forceinline__ Offsets(void* smem, int B)
         : first(static_cast<uint32_t*>(smem)), rest(reinterpret_cast<uint8_t*>(first + B + 1)) {}
-    __device__ __forceinline__ long long total(const Work& w) const { return first[w.B]; }
+    __device__ __forceinline__ uint32_t total(const Work& w) const { return first[w.B]; }
 };
 
 // Fills the tables; called by every thread of the block.
@@ -93,7 +98,7 @@ __device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __res
     for (int b = threadIdx.x; b < w.B; b += blockDim.x) {
         const int L = w.len(kv_len, b);
         t.rest[b] = (uint8_t)(L ? (L - 1) % w.T : 0);
-        t.first[b + 1] = (uint32_t)w.U * w.tiles(L);
+        t.first[b + 1] = (uint32_t)w.U * w.span(L);
     }
     if (threadIdx.x == 0) t.first[0] = 0;
     __syncthreads();
@@ -115,8 +120,8 @@ __device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __res
     __syncthreads();
 }
 
-// The sequence whose tiles hold g (first[b] <= g < first[b + 1]).
-__device__ __forceinline__ int find_sequence(const uint32_t* first, int B, long long g) {
+// The sequence whose units hold g (first[b] <= g < first[b + 1]).
+__device__ __forceinline__ int find_sequence(const uint32_t* first, int B, uint32_t g) {
     int lo = 0, hi = B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -125,26 +130,39 @@ __device__ __forceinline__ int find_sequence(const uint32_t* first, int B, long 
     return lo;
 }
 
-// A CTA's next segment: tiles [t0, t1) of unit `unit` of sequence b.
+// Tiles [t0, t1) of unit `unit` of sequence b.
 struct Segment {
     int b, unit, t0, t1, tiles, L;
+    uint32_t begin, end;  // positions of the unit's span
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
     // a CTA has at most one segment that begins inside a unit (its first) and one
     // that begins a unit without ending it (its last): its two partial slots
     __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 > 0 ? 0 : 1); }
 };
-__device__ __forceinline__ Segment segment_at(const Work& w, const Offsets& t, long long g, long long g_end) {
+// The segment at position g of a share that ends at g_end.
+__device__ __forceinline__ Segment segment_at(const Work& w, const Offsets& t, uint32_t g, uint32_t g_end) {
     Segment s;
     s.b = find_sequence(t.first, w.B, g);
-    s.tiles = (int)((t.first[s.b + 1] - t.first[s.b]) / (uint32_t)w.U);
+    const int span = (int)((t.first[s.b + 1] - t.first[s.b]) / (uint32_t)w.U);
+    s.tiles = span - w.V;
     const int pt = s.tiles - w.tree_tiles();
     s.L = pt ? (pt - 1) * w.T + t.rest[s.b] + 1 : 0;
-    const uint32_t x = (uint32_t)g - t.first[s.b];
-    s.unit = (int)(x / (uint32_t)s.tiles);
-    s.t0 = (int)(x - (uint32_t)s.unit * s.tiles);
-    const long long left = g_end - g;
-    s.t1 = left < s.tiles - s.t0 ? s.t0 + (int)left : s.tiles;
+    const uint32_t x = g - t.first[s.b];
+    s.unit = (int)(x / (uint32_t)span);
+    s.begin = t.first[s.b] + (uint32_t)s.unit * span;
+    s.end = s.begin + span;
+    s.t0 = max(0, (int)(g - s.begin) - w.V);
+    s.t1 = max(0, (int)(min(g_end, s.end) - s.begin) - w.V);
     return s;
+}
+// Moves g to the next segment that has tiles; false: the share has none left.
+__device__ __forceinline__ bool next_segment(const Work& w, const Offsets& t, uint32_t& g, uint32_t g_end, Segment& s) {
+    while (g < g_end) {
+        s = segment_at(w, t, g, g_end);
+        if (s.t1 > s.t0) return true;
+        g = s.end;
+    }
+    return false;
 }
 
 }  // namespace q8

@@ -348,6 +348,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
     return done != 0;
 }
 
+// The same without suspending the thread.
+__device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Waits for the mbarrier phase with the given parity; gives up after about
 // `max_cycles` SM cycles and returns false.  The common case (phase already
 // complete) costs one try_wait.
