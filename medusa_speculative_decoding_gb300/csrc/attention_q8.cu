@@ -292,11 +292,12 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 //   SHARED = true   blocks of 2 NB rows; each stream has NB of them, both use
 //                   every tile
 // Steps x = 0, 1, 2, ...: stream x & 1, tile x (or x / 2).  S has two buffers a
-// stream, so the MMA warp forms scores up to two steps ahead, and a stream waits
+// stream, so its MMA warp forms scores up to two steps ahead, and a stream waits
 // for its last PV only before it writes the next weights or rescales O.
 //
-// Warps 0-7 softmax, warp 8 MMA, warp 9 TMA (page tables, scales and tiles run
-// ahead through a ring of R slots; a slot is K and V of one tile of 128 keys).
+// Warps 0-7 softmax, warps 8 and 9 MMA (one per stream), warp 10 TMA (page tables,
+// scales and tiles run ahead through a ring of slots; a slot is K and V of one tile
+// of 128 keys).
 // The tree's rows are bf16: such a tile takes two slots, and its products are
 // kind::f16 with q and P in bf16, added to the same sums.
 // Every wait is bounded; a CTA that gives up marks its results NaN.
@@ -305,7 +306,10 @@ constexpr int kTile = 128;  // keys per tile
 constexpr int kUSoftmax = 256, kUThreads = kUSoftmax + 96;
 constexpr int kUMmaWarp = kUSoftmax / 32, kUTmaWarp = kUMmaWarp + 2;  // an MMA warp per stream
 constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
-constexpr int kSetup = 3;               // tiles that a unit counts more (q8.cuh, Work)
+// Tiles that a unit counts more (q8.cuh, Work): first references, tree tile and results
+// cost about as much as five tiles.  Measured with 3 / 4 / 5 / 6: 119 / 115 / 112 / 111 us
+// for eight ragged sequences of 64 rows, 25.7 / 27.2 / 26.3 / 27.2 us for one of 2048 keys.
+constexpr int kSetup = 5;
 constexpr float kTau = 4.f;              // log2 by which weights may exceed 1
 constexpr float kPScale = 2048.f;        // planes hold weight * vs / v_ref * kPScale <= 2^15
 constexpr float kVHead = 4.f;            // v_ref = kVHead * the largest V scale when set
@@ -397,18 +401,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Two weights (times V scale) into their planes.  e5m2 is the upper byte of f16,
-// so a plane is the f16 value rounded to that byte (adding half a step; the sign is
-// apart, so this rounds magnitudes), and what it leaves is exact in f16.  Returns
-// the three planes' values in the upper bytes of each half.
+// Two weights (times V scale) into their planes.  e5m2 is the upper byte of f16: the
+// first two planes cut the f16 value off behind that byte (three bits each, and what
+// is left is exact in f16), the third rounds.  Returns the planes' values in the upper
+// bytes of each half.
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t (&plane)[3]) {
-    uint32_t x;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(b), "f"(a));
-    plane[0] = (x + 0x00800080u) & 0xff00ff00u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(plane[0]));
-    plane[1] = (x + 0x00800080u) & 0xff00ff00u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(plane[1]));
-    plane[2] = x + 0x00800080u;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(plane[0]) : "f"(b), "f"(a));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(plane[1]) : "r"(plane[0]), "r"(plane[0] & 0xff00ff00u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(plane[2]) : "r"(plane[1]), "r"(plane[1] & 0xff00ff00u));
+    plane[2] += 0x00800080u;
 }
 __device__ __forceinline__ bool not_finite(const uint4& v) {  // any of eight bf16 values
     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -454,9 +455,9 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_misc);
     volatile int* flag = reinterpret_cast<volatile int*>(s_misc + 1);      // a wait gave up
     volatile int* s_fail = reinterpret_cast<volatile int*>(s_misc + 2);    // [2] per stream
-    float* s_qmax = s_misc + 4;                                            // [kUSoftmax / 32] per warp
-    float* s_vmax = s_misc + 20;                                           // [2][4] largest V scale per quarter
-    float* s_vref = s_misc + 28;                                           // [2] at the end of a segment
+    float* s_vmax = s_misc + 4;                                            // [2][4] largest V scale per quarter
+    float* s_vref = s_misc + 12;                                           // [2] at the end of a segment
+    float* s_qmax = s_misc + 16;                                           // [2][kUSoftmax / 32] per warp
     const q8::Offsets first(base + L::kOffFirst, w.B);
     const long long lim = g_wait_limit;
 
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         }
     } else if (warp < kUMmaWarp) {
         // ------------------------------ softmax warps ------------------------------
-        constexpr int CW = NB;
+        constexpr int CW = NB;  // rows (columns of S^T) per thread
         const int st = warp >> 2, quarter = warp & 3;
         const int key = quarter * 32 + lane;  // TMEM lane: key of a tile, then output column
         const int stid = tid & (kUStream - 1);
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 }
             }
             qmax = redux_max(qmax);
-            if (lane == 0) s_qmax[(seg & 1) * 8 + warp] = qmax;
+            if (lane == 0) s_qmax[(seg & 1) * (kUSoftmax / 32) + warp] = qmax;
             if (tid < L::kRowsBlock) {
                 const int gr = row0 + tid;
                 s_row[(seg & 1) * L::kRowsBlock + tid] = gr / a.G * a.Hq + hk * a.G + gr % a.G;
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             const bool tree = s.t1 > w.prefix_tiles(s.L);
             float qmax = 0.f;
 #pragma unroll
-            for (int i = 0; i < kUSoftmax / 32; ++i) qmax = fmaxf(qmax, s_qmax[(seg & 1) * 8 + i]);
+            for (int i = 0; i < kUSoftmax / 32; ++i) qmax = fmaxf(qmax, s_qmax[(seg & 1) * (kUSoftmax / 32) + i]);
             // factor 2^k with qmax * 2^k in [128, 256)
             const int qe = q8::clamp_int(254 + 7 - (int)(__float_as_uint(qmax) >> 23), 1, 253);
             const float qf = __uint_as_float((uint32_t)qe << 23);
@@ -924,18 +925,24 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
                     float top = -INFINITY;
                     if constexpr (!tree) {
-                        // eight columns at a time, the next ones on their way from TMEM
-                        float x[2][8];
-                        tmem_ld8(tS, x[0]);
+                        // sixteen columns at a time.  Shared blocks have many such tiles one after
+                        // the other and load the next columns ahead (450 us against 466 for 341
+                        // rows over 8192 keys); the others have a stream's last and first tiles
+                        // side by side and gain more from the registers (119 us against 123 for
+                        // eight sequences of 64 rows).
+                        constexpr int W = 16, kAhead = SHARED ? 1 : 0;
+                        float x[1 + kAhead][W];
+                        if constexpr (kAhead) tmem_ld16(tS, x[0]);
 #pragma unroll
-                        for (int c0 = 0; c0 < CW; c0 += 8) {
-                            float(&y)[8] = x[(c0 >> 3) & 1];
+                        for (int c0 = 0; c0 < CW; c0 += W) {
+                            float(&y)[W] = x[(c0 / W) & kAhead];
+                            if constexpr (!kAhead) tmem_ld16(tS + c0, y);
                             tmem_wait_ld();
-                            if (c0 + 8 < CW) tmem_ld8(tS + c0 + 8, x[((c0 >> 3) & 1) ^ 1]);
-                            relative(c0, y, 8);
-                            uint32_t pw[3][2];
+                            if (kAhead && c0 + W < CW) tmem_ld16(tS + c0 + W, x[((c0 / W) & 1) ^ kAhead]);
+                            relative(c0, y, W);
+                            uint32_t pw[3][W / 4];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
+                            for (int e = 0; e < W / 4; ++e) {
                                 uint32_t two[2][3];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
@@ -955,9 +962,9 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                                 // NB = 64: one plane of 64 bytes a key after the other; NB = 16:
                                 // the planes are the key's 16-byte chunks 0, 1, 2
                                 const int chunk = NB == 64 ? c0 >> 4 : p;
-                                *reinterpret_cast<uint2*>(p_row + (NB == 64 ? p * L::kPlane : 0) + key * 64 +
-                                                          ((chunk ^ ((key >> 1) & 3)) << 4) + (c0 & 8)) =
-                                    make_uint2(pw[p][0], pw[p][1]);
+                                uint8_t* to = p_row + (NB == 64 ? p * L::kPlane : 0) + key * 64 +
+                                              ((chunk ^ ((key >> 1) & 3)) << 4);
+                                *reinterpret_cast<uint4*>(to) = make_uint4(pw[p][0], pw[p][1], pw[p][2], pw[p][3]);
                             }
                         }
                     } else {
@@ -981,14 +988,18 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     }
                     return top;
                 };
-                bool move = true;
-                if (i > 0) {
-                    const float top = weights();
-                    __syncwarp();
-                    move = named_barrier_or(1 + st, kUStream, !ok || vs > v_ref || top > kTau);
-                    // l + p - p is off by half a unit of l + p at most, and p falls to at most 1
-                    // on the new references: the error is one rounding of the row's sum.
-                    if (move) {
+                // A V scale above the reference would leave e5m2's range; bf16 (the tree, whose
+                // V has scale 1) has more, and moving the references for it took 17 us of 139.
+                const bool large = vs > (tree ? v_ref * 4096.f : v_ref);
+                bool move = i == 0;
+                for (;;) {
+                    if (!move) {
+                        const float top = weights();
+                        __syncwarp();
+                        if (!named_barrier_or(1 + st, kUStream, !ok || large || top > kTau)) break;
+                        // Taken back: l + p - p is off by half a unit of l + p at most, and p falls
+                        // to at most 1 on the new references, so the error is one rounding of the
+                        // row's sum.
                         if constexpr (!tree) {
 #pragma unroll
                             for (int c0 = 0; c0 < CW; c0 += 8) {
@@ -1009,11 +1020,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                             }
                         }
                     }
-                } else {
-                    __syncwarp();
-                    move = named_barrier_or(1 + st, kUStream, true);
-                }
-                if (move) {
                     // The references move: largest score per row over the tile's keys.
 #pragma unroll 1
                     for (int c0 = 0; c0 < CW; c0 += 8) {
@@ -1073,6 +1079,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         tmem_wait_st();
                     }
                     weights();
+                    break;
                 }
                 // A key that is not there has no V either: whatever the slot holds (stale
                 // codes may be NaN) is cleared, by each stream that multiplies it.
