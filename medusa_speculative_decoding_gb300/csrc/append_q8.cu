@@ -40,18 +40,47 @@ struct AppendArgs {
     int B, T, R, Hkv, P, M, n_pages, h16;
 };
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-    const uint4 w = ld_stream16(p);
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+// Eight neighbouring elements of a row, as they were loaded.
+struct Bf16x8 {
+    uint4 w;
+    __device__ __forceinline__ void load(const uint16_t* p) { w = ld_stream16(p); }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_lo(v[i]); x[2 * i + 1] = bf16_hi(v[i]); }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const uint4 a = ld_stream16(p), b = ld_stream16(p + 4);
-    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_lo(v[i]); x[2 * i + 1] = bf16_hi(v[i]); }
+    }
+    // largest |x|, NaN left out
+    __device__ __forceinline__ float top() const {
+        uint32_t m = abs2(w.x);
+        m = max2(max2(m, abs2(w.y)), max2(abs2(w.z), abs2(w.w)));
+        return fmaxf(fmaxf(bf16_lo(m), bf16_hi(m)), 0.f);
+    }
+    static __device__ __forceinline__ uint32_t abs2(uint32_t v) { return v & 0x7fff7fffu; }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+};
+struct F32x8 {
+    uint4 w[2];
+    __device__ __forceinline__ void load(const float* p) { w[0] = ld_stream16(p); w[1] = ld_stream16(p + 4); }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+        const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
-}
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
+    }
+    __device__ __forceinline__ float top() const {
+        float x[8], m = 0.f;
+        unpack(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+        return m;
+    }
+};
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> { using type = Bf16x8; };
+template <> struct Raw8<float> { using type = F32x8; };
 
 // the smallest 2^e with top <= 448 * 2^e, e held to [-64, 64]
 __device__ __forceinline__ float page_scale(float top) {
@@ -79,6 +108,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_q8_kernel(const AppendA
     const int w0 = ok ? L / P : 0;  // first page that receives a row
     const int windows = ok && n > 0 ? (L + n - 1) / P - w0 + 1 : 0;
     const int32_t* table = a.page_table + (size_t)b * a.M;
+
+    // This CTA's rows, asked for before the check's own loads have come back.
+    const bool rows_cta = blockIdx.x < 2 * a.Hkv && (int)blockIdx.y < windows;
+    const int h = blockIdx.x >> 1, kv = blockIdx.x & 1;
+    const int first = (w0 + (int)blockIdx.y) * P - L;  // new row that the page's slot 0 takes
+    const int chunks = P * C8;
+    typename Raw8<T>::type x[CHUNKS];
+    if (rows_cta) {
+        const T* rows = static_cast<const T*>(a.rows[kv]) + ((size_t)b * a.T * a.Hkv + h) * D;
+        const size_t row_stride = (size_t)a.Hkv * D;
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) {
+            const int c = tid + k * kAppendThreads;
+            const int i = first + c / C8;
+            x[k] = {};
+            if (c < chunks && i >= 0 && i < n) {
+                const int r = a.index ? a.index[(size_t)b * a.R + i] : i;
+                if (r >= 0 && r < a.T) x[k].load(rows + (size_t)r * row_stride + (c % C8) * 8);
+            }
+        }
+    }
+
     bool mine = true;
     for (int i = tid; i < windows; i += kAppendThreads) {
         const int p = table[w0 + i];
@@ -104,46 +155,36 @@ __global__ void __launch_bounds__(kAppendThreads) append_q8_kernel(const AppendA
         }
         return;
     }
-    if (!ok || (int)blockIdx.y >= windows) return;
+    if (!ok || !rows_cta) return;
 
-    const int h = blockIdx.x >> 1, kv = blockIdx.x & 1;
-    const T* rows = static_cast<const T*>(a.rows[kv]) + ((size_t)b * a.T * a.Hkv + h) * D;
-    const size_t row_stride = (size_t)a.Hkv * D;
-    const int page = table[w0 + blockIdx.y];
-    const size_t unit = (size_t)page * a.Hkv + h;
+    const size_t unit = (size_t)table[w0 + blockIdx.y] * a.Hkv + h;
     uint8_t* codes = a.pages[kv] + unit * P * D;
-    const int first = (w0 + (int)blockIdx.y) * P - L;  // new row that the page's slot 0 takes
-    const int chunks = P * C8;
-
-    float x[CHUNKS][8];
+    const bool had = first < 0;  // the page holds earlier rows
+    const float s0 = had ? a.scale[kv][unit] : 0.f;
     float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) {
-        const int c = tid + k * kAppendThreads;
-        const int i = first + c / C8;
-        if (c < chunks && i >= 0 && i < n) {
-            const int r = a.index ? a.index[(size_t)b * a.R + i] : i;
-            load8(rows + (size_t)r * row_stride + (c % C8) * 8, x[k]);
+    for (int k = 0; k < CHUNKS; ++k) top = fmaxf(top, x[k].top());
+    if (top == INFINITY) {  // the scale is set by finite values
+        top = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float m = fabsf(x[k][e]);
-                if (m < INFINITY) top = fmaxf(top, m);  // the scale is set by finite values
-            }
+        for (int k = 0; k < CHUNKS; ++k) {
+            float y[8];
+            x[k].unpack(y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (fabsf(y[e]) < INFINITY) top = fmaxf(top, fabsf(y[e]));
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if ((tid & 31) == 0) s_top[tid >> 5] = top;
-    __syncthreads();
+    __syncthreads();  // every thread has read the page's scale, too
 #pragma unroll
     for (int i = 0; i < kAppendThreads / 32; ++i) top = fmaxf(top, s_top[i]);
 
-    const bool had = first < 0;  // the page holds earlier rows
-    const float s0 = had ? a.scale[kv][unit] : 0.f;
     const bool readable = !had || q8::scale_ok(s0);  // an unreadable page stays one
     const bool keep = had && (!readable || top <= q8::kE4m3Max * s0);
     const float s1 = keep ? s0 : page_scale(top);
-    __syncthreads();  // every thread has read the scale
     if (tid == 0 && !keep) a.scale[kv][unit] = s1;
     if (!readable) return;
     // 1 / s1 is exact for the powers of two written here; a caller's own scale is divided by
@@ -155,6 +196,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_q8_kernel(const AppendA
         const int i = first + c / C8;
         if (c >= chunks || i >= n) continue;
         uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)c * 8);
+        float y[8];
         if (i < 0) {
             if (keep) continue;
             const uint2 w = *dst;
@@ -162,15 +204,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_q8_kernel(const AppendA
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 f = q8::e4m3x2_to_float2(old[e]);
-                x[k][2 * e] = f.x * s0;
-                x[k][2 * e + 1] = f.y * s0;
+                y[2 * e] = f.x * s0;
+                y[2 * e + 1] = f.y * s0;
             }
+        } else {
+            x[k].unpack(y);
         }
         uint16_t q[4];
+        if (pow2) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            q[e] = pow2 ? q8::float2_to_e4m3x2(x[k][2 * e] * inv, x[k][2 * e + 1] * inv)
-                        : q8::float2_to_e4m3x2(x[k][2 * e] / s1, x[k][2 * e + 1] / s1);
+            for (int e = 0; e < 4; ++e) q[e] = q8::float2_to_e4m3x2(y[2 * e] * inv, y[2 * e + 1] * inv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = q8::float2_to_e4m3x2(y[2 * e] / s1, y[2 * e + 1] / s1);
+        }
         *dst = make_uint2((uint32_t)q[0] | (uint32_t)q[1] << 16, (uint32_t)q[2] | (uint32_t)q[3] << 16);
     }
 }
