@@ -371,7 +371,17 @@ def _raw_stream(stream, dev):
 
 @functools.lru_cache(maxsize=256)
 def _attention_q8_bytes(dev, B, N, Hq, Hkv, D, dtype):
-    return int(lib().medusa_tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype))
+    return max(16, lib().medusa_tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _fork_bytes(B, n_pages):
+    return max(16, kv_pages_fork_workspace(B, n_pages))
+
+
+@functools.lru_cache(maxsize=256)
+def _compact_bytes(n_pages):
+    return max(16, kv_pages_compact_workspace(n_pages))
 
 
 def tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype=torch.bfloat16):
@@ -398,7 +408,7 @@ def tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, pag
     _need_shape(mask, "mask", (N, (N + 63) // 64), torch.int64, dev)
     o = torch.empty_like(q) if out is None else _need_shape(out, "out", q.shape, dtype, dev)
     if ws is None:
-        ws = _ws(_attention_q8_bytes(dev, B, N, Hq, Hkv, D, code), q.device)
+        ws = torch.empty(_attention_q8_bytes(dev, B, N, Hq, Hkv, D, code), dtype=torch.uint8, device=q.device)
     check(lib().medusa_tree_attention_q8(q.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), code, k_pages.data_ptr(),
                                          v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                          page_table.data_ptr(), kv_len.data_ptr(), mask.data_ptr(), B, N, Hq, Hkv, D, P,
@@ -439,8 +449,7 @@ def kv_append_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table,
         _need_shape(hidden_rows, "hidden_rows", (B, T, H), dtype, dev)
         _need_shape(best_node, "best_node", (B,), _I32, dev)
     if out is None:
-        both = torch.empty((2, B), dtype=_I32, device=kv_len.device)
-        out = dict(kv_len=both[0], appended=both[1],
+        out = dict(kv_len=torch.empty_like(kv_len), appended=torch.empty_like(kv_len),
                    h_next=torch.empty((B, H), dtype=dtype, device=kv_len.device) if H else None)
     else:
         _need_shape(out["kv_len"], "out kv_len", (B,), _I32, dev)
@@ -476,14 +485,13 @@ def kv_pages_fork(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, src=No
     if held is not None:
         _need_shape(held, "held", (n_pages,), _I32, dev)
     if out is None:
-        both = torch.empty((2, B), dtype=_I32, device=kv_len.device)
-        out = dict(page_table=torch.empty_like(page_table), kv_len=both[0],
-                   refs=torch.empty(n_pages, dtype=_I32, device=kv_len.device), taken=both[1])
+        out = dict(page_table=torch.empty_like(page_table), kv_len=torch.empty_like(kv_len),
+                   refs=torch.empty(n_pages, dtype=_I32, device=kv_len.device), taken=torch.empty_like(kv_len))
     else:
         for n, shape in (("page_table", (B, M)), ("kv_len", (B,)), ("refs", (n_pages,)), ("taken", (B,))):
             _need_shape(out[n], f"out {n}", shape, _I32, dev)
     if ws is None:
-        ws = _ws(kv_pages_fork_workspace(B, n_pages), kv_len.device)
+        ws = torch.empty(_fork_bytes(B, n_pages), dtype=torch.uint8, device=kv_len.device)
     check(lib().medusa_kv_pages_fork(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                      page_table.data_ptr(), kv_len.data_ptr(), _ptr(src), _ptr(need), _ptr(held), B,
                                      Hkv, D, P, n_pages, M, out["page_table"].data_ptr(), out["kv_len"].data_ptr(),
@@ -513,7 +521,7 @@ def kv_pages_compact(k_pages, v_pages, k_scale, v_scale, page_table, held=None, 
         for n, shape in (("page_table", (B, M)), ("new_page", (n_pages,)), ("live", (1,))):
             _need_shape(out[n], f"out {n}", shape, _I32, dev)
     if ws is None:
-        ws = _ws(kv_pages_compact_workspace(n_pages), page_table.device)
+        ws = torch.empty(_compact_bytes(n_pages), dtype=torch.uint8, device=page_table.device)
     check(lib().medusa_kv_pages_compact(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                         page_table.data_ptr(), _ptr(held), B, Hkv, D, P, n_pages, M,
                                         out["page_table"].data_ptr(), out["new_page"].data_ptr(),
