@@ -453,7 +453,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     uint32_t* s_mask = reinterpret_cast<uint32_t*>(base + L::kOffMask);
     float* s_misc = reinterpret_cast<float*>(base + L::kOffMisc);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_misc);
-    volatile int* flag = reinterpret_cast<volatile int*>(s_misc + 1);      // a wait gave up
     volatile int* s_fail = reinterpret_cast<volatile int*>(s_misc + 2);    // [2] per stream
     float* s_vmax = s_misc + 4;                                            // [2][4] largest V scale per quarter
     float* s_vref = s_misc + 12;                                           // [2] at the end of a segment
@@ -472,7 +471,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         mbar_init(checked0, 4);
         mbar_init(checked0 + 8, 4);
         mbar_init_fence();
-        *flag = 0;
         s_fail[0] = s_fail[1] = 0;
         prefetch_tmap(&tmk);
         prefetch_tmap(&tmv);
@@ -599,18 +597,16 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     ++np;
                     p_par ^= 1;
                     spins = 0;
-                } else if ((++spins & 63) == 0) {
-                    if (spins == 64) t_last = clock64();
+                } else if ((++spins & 7) == 0) {
+                    if (spins == 8) t_last = clock64();
                     fail = __any_sync(0xffffffffu, clock64() - t_last > lim);
                 }
             }
-            if (fail) *flag = 1;
             slot0 += n_pre + 2 * n_tree;
         }
-        if (fail) {  // let everything in flight complete before TMEM is freed
-            commit_warp(drain + 8 * st);
-            mbar_wait(drain + 8 * st, 0, kDrainCycles);
-        }
+        // Everything in flight completes before TMEM is freed, whoever gave up.
+        commit_warp(drain + 8 * st);
+        warp_wait(drain + 8 * st, 0, kDrainCycles);
     } else if (warp == kUTmaWarp) {
         // -------------------------------- TMA warp --------------------------------
         int slot = 0;
@@ -681,14 +677,10 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 }
             }
         }
-        if (fail) {
-            if (lane == 0) {
-                *flag = 1;
-                // every slot that was asked for lands before the CTA leaves
-                for (int sl = max(0, slot - R); sl < slot; ++sl)
-                    mbar_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), kDrainCycles);
-            }
-        }
+        // Every slot that was asked for lands before the CTA leaves, whoever gave up.
+        if (lane == 0)
+            for (int sl = max(0, slot - R); sl < slot; ++sl)
+                mbar_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), kDrainCycles);
     } else if (warp < kUMmaWarp) {
         // ------------------------------ softmax warps ------------------------------
         constexpr int CW = NB;  // rows (columns of S^T) per thread

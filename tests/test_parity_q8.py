@@ -103,7 +103,7 @@ def tolerance(c, ref):
     rounds once, relative to the sum of magnitudes.  exp2: 2 units, its argument's
     rounding is part of e (arguments stay below 2^7 in units of the score).
     bf16: q enters to 2^-17 of the largest |q| of the row block (all of q here);
-    weights of tree rows are bf16, 2^-8, those of pages have 9 bits, 2^-10 (both are
+    weights of tree rows are bf16, 2^-8, those of pages have 9 bits, 2^-9 (both are
     held to 2^-8 here), and half of e5m2's least step, 2^-17, in
     planes that hold at least 2^9 for a weight of 1 on the largest V scale: 2^-26,
     times a code of at most 448, for each key; the output rounds to bf16: 2^-8."""
