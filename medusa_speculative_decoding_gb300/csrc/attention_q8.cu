@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 // owns one key: its scale is one register, the work is in proportion to the
 // query rows (from 16 on) rather than to the 128 rows of a matrix tile, and the
 // row sums are added up per thread and joined once per segment.  What crosses
-// threads is the rows' maximum, and that only when a score rises 2^4 above the
+// threads is the rows' maximum, and that only when a score rises 2^4.9 above the
 // reference it is held against (the first tile and few others), which one
 // barrier vote per tile finds out.
 //
@@ -310,8 +310,11 @@ constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
 // cost about as much as five tiles.  Measured with 3 / 4 / 5 / 6: 119 / 115 / 112 / 111 us
 // for eight ragged sequences of 64 rows, 25.7 / 27.2 / 26.3 / 27.2 us for one of 2048 keys.
 constexpr int kSetup = 5;
-constexpr float kTau = 4.f;              // log2 by which weights may exceed 1
-constexpr float kPScale = 2048.f;        // planes hold weight * vs / v_ref * kPScale <= 2^15
+// Planes hold weight * vs / v_ref * kPScale <= 2^15.9, below f16's largest 65504; weights
+// may exceed 1 by 2^kTau before the references move (126 us with 2^3, 112 with 2^4.9 for
+// eight ragged sequences of 64 rows).
+constexpr float kTau = 4.9f;
+constexpr float kPScale = 2048.f;
 constexpr float kVHead = 4.f;            // v_ref = kVHead * the largest V scale when set
 constexpr long long kDrainCycles = kDefaultWaitCycles;
 
@@ -907,13 +910,21 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         for (int e = 0; e < n; ++e) x[e] = valid ? x[e] : -INFINITY;
                     }
                 };
-                // the stream's last PV: P and O are free behind it
-                if (i > 0) ok = warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + i - 1) & 1), lim) && ok;
-                if (!ok && lane == 0) s_fail[st] = 1;
+                // The stream's last PV, behind which P and O are free.  Shared blocks form the
+                // first columns' weights before this wait and write them after it (410 us
+                // against 441 for 341 rows over 8192 keys); the others wait for tiles rather
+                // than for products and keep the registers (113 us against 118).
+                constexpr bool late = SHARED;
+                auto wait_pv = [&]() {
+                    if (i > 0) ok = warp_wait(pv_done0 + 8 * st, (uint32_t)((n_s + i - 1) & 1), lim) && ok;
+                    if (!ok && lane == 0) s_fail[st] = 1;
+                };
+                if (!late || i == 0) wait_pv();
                 // Weights, their sums and their planes; returns the largest score.  They are
                 // written on the old references; where a score turns out to lie too far above
                 // them they are taken back and written again.
-                auto weights = [&]() -> float {
+                auto weights = [&](auto again) -> float {
+                    constexpr bool wait_here = late && !decltype(again)::value;
                     const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
                     float top = -INFINITY;
                     if constexpr (!tree) {
@@ -949,6 +960,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 #pragma unroll
                                 for (int p = 0; p < 3; ++p) pw[p][e] = __byte_perm(two[0][p], two[1][p], 0x7531);
                             }
+                            if (wait_here && c0 == 0) wait_pv();
 #pragma unroll
                             for (int p = 0; p < 3; ++p) {
                                 // NB = 64: one plane of 64 bytes a key after the other; NB = 16:
@@ -974,6 +986,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                                 h[e] = pack_bf16x2(p0 * f, p1 * f);
                                 add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], bad_v && see0 ? NAN : p0, bad_v && see1 ? NAN : p1);
                             }
+                            if (wait_here && c0 == 0) wait_pv();
                             *reinterpret_cast<uint4*>(p_row + key * 128 + (((c0 >> 3) ^ (key & 7)) << 4)) =
                                 make_uint4(h[0], h[1], h[2], h[3]);
                         }
@@ -986,7 +999,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 bool move = i == 0;
                 for (;;) {
                     if (!move) {
-                        const float top = weights();
+                        const float top = weights(std::false_type{});
                         __syncwarp();
                         if (!named_barrier_or(1 + st, kUStream, !ok || large || top > kTau)) break;
                         // Taken back: l + p - p is off by half a unit of l + p at most, and p falls
@@ -1070,7 +1083,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         }
                         tmem_wait_st();
                     }
-                    weights();
+                    weights(std::true_type{});
                     break;
                 }
                 // A key that is not there has no V either: whatever the slot holds (stale
