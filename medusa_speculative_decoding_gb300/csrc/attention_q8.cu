@@ -39,6 +39,7 @@ struct AttnQ8Args {
     void* out;
     float* part_o;   // ws [2 * ctas][rows][D]: sums relative to the row's reference
     float2* part_ml;  // ws [2 * ctas][rows]: (reference in log2 units, sum)
+    int4* plan;       // ws [ctas]: see plan_share
     q8::Work work;
     int Hq, Hkv, G, P, M, n_pages, W, qblocks;
     float scale_log2;
@@ -64,6 +65,23 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 
 // 2^x with x <= 0 or -inf; exp2f is within 2 units in the last place
 __device__ __forceinline__ float weight(float x) { return exp2f(x); }
+
+// What the merge has to know about share c = blockIdx.x: the unit that it begins and
+// leaves to others to finish, as (last share of it, sequence, KV head, first row); x =
+// -1: none.  One thread; it is off every path that others wait for.
+__device__ __forceinline__ void plan_share(const AttnQ8Args& a, const q8::Offsets& first, int rows_block) {
+    const q8::Work& w = a.work;
+    const uint32_t total = first.total(w);
+    const uint32_t g_begin = w.cta_begin(total, blockIdx.x), g_end = w.cta_begin(total, blockIdx.x + 1);
+    int4 p = make_int4(-1, 0, 0, 0);
+    if (g_begin < g_end) {
+        const q8::Segment s = q8::segment_at(w, first, g_end - 1, g_end);
+        const uint32_t tiles = s.begin + w.V;  // the unit's first tile
+        if (g_begin <= tiles && tiles < g_end && g_end < s.end)
+            p = make_int4(w.cta_of(total, s.end - 1), s.b, s.unit / a.qblocks, s.unit % a.qblocks * rows_block);
+    }
+    a.plan[blockIdx.x] = p;
+}
 
 // ---------------------------------------------------------------------------
 // One CTA works through its share of (unit, tile) pairs; a unit's block has
@@ -258,6 +276,10 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
         }
         __syncthreads();  // q, statistics free again
     }
+    // an empty share gives nothing to the units around it
+    if (tid < kRows && w.cta_begin(total, blockIdx.x) == g_end)
+        a.part_ml[(size_t)2 * blockIdx.x * kRows + tid] = make_float2(-INFINITY, 0.f);
+    if (tid == 0) plan_share(a, first, kRows);
 }
 
 // ---------------------------------------------------------------------------
@@ -684,6 +706,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         if (lane == 0)
             for (int sl = max(0, slot - R); sl < slot; ++sl)
                 mbar_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), kDrainCycles);
+        if (lane == 0) plan_share(a, first, L::kRowsBlock);
     } else if (warp < kUMmaWarp) {
         // ------------------------------ softmax warps ------------------------------
         constexpr int CW = NB;  // rows (columns of S^T) per thread
@@ -801,6 +824,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             bar_sync(3, kUSoftmax);
             take_q(s, 0);
             bar_sync(3, kUSoftmax);
+        } else if (g_begin == g_end && tid < L::kRowsBlock) {  // an empty share gives nothing to the units around it
+            a.part_ml[(size_t)2 * blockIdx.x * L::kRowsBlock + tid] = make_float2(-INFINITY, 0.f);
         }
         for (int seg = 0; more; ++seg) {
             int n_pre, n_tree;
@@ -1284,35 +1309,22 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     if (warp == 0) tmem_dealloc(tmem, kCols);
 }
 
-// Joins the partial results.  Block (c, y): the unit that share c leaves
-// unfinished, if that is the first share boundary inside it; rows from y *
-// kMergeThreads / (D / 4) on, four columns a thread.  All of a thread's loads are
-// in flight at once (a loop of dependent loads took 16 rows x 10 round trips to
-// memory, 80 us).
+// Joins the partial results.  Block (c, y): the unit that share c begins and others
+// finish (plan_share); rows from y * kMergeThreads / (D / 4) on, four columns a
+// thread.  All of a thread's loads are in flight at once (a loop of dependent loads
+// took 16 rows x 10 round trips to memory, 80 us).  What a block joins is worked out
+// by the shares themselves: each block doing it anew, with a scan over the sequences
+// and divisions by the number of tiles, took 7 to 15 us.
 constexpr int kMergeThreads = 256, kMergeBatch = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const AttnQ8Args a, int rows_block) {
-    extern __shared__ uint32_t merge_smem[];
-    const q8::Work w = a.work;
-    const q8::Offsets first(merge_smem, w.B);
     pdl_wait();
     pdl_trigger();
-    q8::tile_offsets(w, a.kv_len, first);
-    const uint32_t total = first.total(w);
-    const int c = blockIdx.x + 1;
-    const uint32_t g = w.cta_begin(total, c);
-    if (g >= total || w.cta_begin(total, c + 1) == g) return;  // an empty share
-    const q8::Segment s = q8::segment_at(w, first, g, g);
-    if (s.t0 == 0) return;                         // the boundary falls between units
-    const int c0 = w.cta_of(total, s.begin + w.V);  // share that begins the unit
-    if (c0 != w.cta_of(total, g - 1)) return;      // an earlier boundary is the first
-    const int c1 = w.cta_of(total, s.end - 1);
-    const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * rows_block;
+    const int c0 = blockIdx.x;
+    const int4 plan = a.plan[c0];
+    const int c1 = plan.x;
     const int i = blockIdx.y * (kMergeThreads / (D / 4)) + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
-    if (i >= min(rows_block, w.N * a.G - row0)) return;
-    // (shares are only empty when there are fewer tiles than CTAs; one left a slot
-    // unwritten then)
-    auto there = [&](int j) { return j <= c1 && w.cta_begin(total, j) != w.cta_begin(total, j + 1); };
+    if (c1 < 0 || i >= min(rows_block, a.work.N * a.G - plan.w)) return;
     auto slot = [&](int j) { return (size_t)(2 * j + (j == c0 ? 1 : 0)) * rows_block + i; };
     float top = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1323,7 +1335,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const Attn
         for (int k = 0; k < kMergeBatch; ++k) {
             ml[k] = make_float2(-INFINITY, 0.f);
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (there(j0 + k)) {
+            if (j0 + k <= c1) {
                 ml[k] = a.part_ml[slot(j0 + k)];
                 v[k] = *reinterpret_cast<const float4*>(a.part_o + slot(j0 + k) * D + d);
             }
@@ -1338,14 +1350,16 @@ __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const Attn
         o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
 #pragma unroll
         for (int k = 0; k < kMergeBatch; ++k) {
+            // no key seen there, or an empty share, which writes no sums (a NaN row keeps its l)
+            if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
             const float f = weight(ml[k].x - ref);
             l += ml[k].y * f;
             o.x += v[k].x * f; o.y += v[k].y * f; o.z += v[k].z * f; o.w += v[k].w * f;
         }
     }
-    const int r = row0 + i;
+    const int r = plan.w + i;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    store4(static_cast<T*>(a.out) + (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + d, o, inv);
+    store4(static_cast<T*>(a.out) + (((size_t)plan.y * a.work.N + r / a.G) * a.Hq + plan.z * a.G + r % a.G) * D + d, o, inv);
 }
 
 struct Plan {
@@ -1370,14 +1384,13 @@ int check_attn_q8(int B, int N, int Hq, int Hkv, int D, int P, int n_pages, int 
     return MEDUSA_OK;
 }
 
-size_t ws_bytes_q8(const Plan& p, int D) { return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float); }
+size_t ws_bytes_q8(const Plan& p, int D) { return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float) + p.ctas * sizeof(int4); }
 
 template <typename T, int D>
 cudaError_t launch_merge(const AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     constexpr int rows = kMergeThreads / (D / 4);  // of a block
     const int all = a.work.N * a.G, most = all < p.rows ? all : p.rows;
-    return launch(attn_q8_merge_kernel<T, D>, dim3(p.ctas - 1, (most + rows - 1) / rows), dim3(kMergeThreads),
-                  q8::offsets_bytes(a.work.B), st, a, p.rows);
+    return launch(attn_q8_merge_kernel<T, D>, dim3(p.ctas, (most + rows - 1) / rows), dim3(kMergeThreads), 0, st, a, p.rows);
 }
 
 template <typename T, int D>
@@ -1470,6 +1483,7 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     a.page_table = page_table; a.kv_len = kv_len; a.mask = mask; a.out = out;
     a.part_o = (float*)ws;
     a.part_ml = (float2*)((float*)ws + (size_t)2 * p.ctas * p.rows * D);
+    a.plan = (int4*)(a.part_ml + (size_t)2 * p.ctas * p.rows);
     a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.P = P; a.M = M; a.n_pages = n_pages; a.W = (N + 63) / 64;
     a.qblocks = (N * a.G + p.rows - 1) / p.rows;
     a.work = q8::Work{B, N, Hkv * a.qblocks, p.keys, p.setup, M * P, p.ctas};
