@@ -329,9 +329,11 @@ constexpr int kUSoftmax = 256, kUThreads = kUSoftmax + 96;
 constexpr int kUMmaWarp = kUSoftmax / 32, kUTmaWarp = kUMmaWarp + 2;  // an MMA warp per stream
 constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
 // Tiles that a unit counts more (q8.cuh, Work): first references, tree tile and results
-// cost about as much as five tiles.  Measured with 3 / 4 / 5 / 6: 119 / 115 / 112 / 111 us
-// for eight ragged sequences of 64 rows, 25.7 / 27.2 / 26.3 / 27.2 us for one of 2048 keys.
-constexpr int kSetup = 5;
+// cost as much as several tiles, and more where they are of more rows.  Measured with
+// 3 / 5 / 7 / 9 / 12 / 16: eight ragged sequences of 64 rows 108 / 105 / 102 / 99 / 99 /
+// 102 us, one of 2048 keys 20 / 21 / 22 / 22 / 23 / 23 us; sixteen sequences of one token
+// 55 / 54 / 55 / 56 / 57 / 60 us.
+constexpr int kSetup = 9, kSetup16 = 5;
 // Planes hold weight * vs / v_ref * kPScale <= 2^15.9, below f16's largest 65504; weights
 // may exceed 1 by 2^kTau before the references move (126 us with 2^3, 112 with 2^4.9 for
 // eight ragged sequences of 64 rows).
@@ -1370,7 +1372,7 @@ struct Plan {
 Plan plan_q8(medusa_dtype dtype, int N, int G) {
     const int rows = N * G, sms = sm_count();
     if (dtype == MEDUSA_F32) return Plan{kRows, kKeys, 1, 2 * sms};
-    if (rows <= 16) return Plan{16, kTile, kSetup, sms};
+    if (rows <= 16) return Plan{16, kTile, kSetup16, sms};
     if (rows <= 64) return Plan{64, kTile, kSetup, sms};
     return Plan{128, kTile, kSetup, sms};
 }
