@@ -62,7 +62,7 @@ const char* medusa_last_error(void);
 int medusa_abi_version(void);
 
 /* Device status of the tensor-core kernels (heads at bf16 batches 3-64, bf16
- * tree attention, the fused verification projection).  Their mbarrier waits
+ * tree attention over either cache, the fused verification projection).  Their mbarrier waits
  * are bounded (about one second each).  A kernel whose wait gives up lets its
  * own copies and MMAs in flight complete, frees its tensor memory, marks the
  * outputs it owns (NaN attention rows, -1 top-k entries or -1 acceptance
@@ -367,8 +367,9 @@ int medusa_kv_compact(void* k_cache, void* v_cache, int32_t* kv_len, const int32
 /* (dtype float32).                                                            */
 /* kv_len is clamped to [0, M*P].  Keys of a page that is not in               */
 /* [0, n_pages) or whose scale is not readable count as absent.  A row that    */
-/* sees no key is zero.  A row that sees a tree row with a non-finite V is     */
-/* NaN; rows that do not see it are not affected.                              */
+/* sees no key is zero.  A row that sees a tree row with a non-finite V (in    */
+/* bf16: or one of 2^91 and more, whose sums could overflow) is NaN; rows that */
+/* do not see it are not affected.                                             */
 /* Limits: N <= 512, Hq % Hkv == 0, N * (Hq/Hkv) <= 4096; scale > 0, finite.   */
 size_t medusa_tree_attention_q8_workspace(int B, int N, int Hq, int Hkv, int D, medusa_dtype dtype);
 int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype,

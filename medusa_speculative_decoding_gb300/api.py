@@ -359,6 +359,11 @@ def _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len=None):
     return (*page_table.shape, *shape, dev)
 
 
+def _need_ws(ws, dev):
+    if ws.get_device() != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
+
+
 def _elsewhere(dev):
     """Whether CUDA device number dev is not the current one (the library works on
     the current device)."""
@@ -409,6 +414,8 @@ def tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, pag
     o = torch.empty_like(q) if out is None else _need_shape(out, "out", q.shape, dtype, dev)
     if ws is None:
         ws = torch.empty(_attention_q8_bytes(dev, B, N, Hq, Hkv, D, code), dtype=torch.uint8, device=q.device)
+    else:
+        _need_ws(ws, dev)
     check(lib().medusa_tree_attention_q8(q.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), code, k_pages.data_ptr(),
                                          v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                          page_table.data_ptr(), kv_len.data_ptr(), mask.data_ptr(), B, N, Hq, Hkv, D, P,
@@ -492,6 +499,8 @@ def kv_pages_fork(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, src=No
             _need_shape(out[n], f"out {n}", shape, _I32, dev)
     if ws is None:
         ws = torch.empty(_fork_bytes(B, n_pages), dtype=torch.uint8, device=kv_len.device)
+    else:
+        _need_ws(ws, dev)
     check(lib().medusa_kv_pages_fork(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                      page_table.data_ptr(), kv_len.data_ptr(), _ptr(src), _ptr(need), _ptr(held), B,
                                      Hkv, D, P, n_pages, M, out["page_table"].data_ptr(), out["kv_len"].data_ptr(),
@@ -522,6 +531,8 @@ def kv_pages_compact(k_pages, v_pages, k_scale, v_scale, page_table, held=None, 
             _need_shape(out[n], f"out {n}", shape, _I32, dev)
     if ws is None:
         ws = torch.empty(_compact_bytes(n_pages), dtype=torch.uint8, device=page_table.device)
+    else:
+        _need_ws(ws, dev)
     check(lib().medusa_kv_pages_compact(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                         page_table.data_ptr(), _ptr(held), B, Hkv, D, P, n_pages, M,
                                         out["page_table"].data_ptr(), out["new_page"].data_ptr(),

@@ -438,11 +438,13 @@ __device__ __forceinline__ void split_weights(float a, float b, uint32_t (&plane
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(plane[2]) : "r"(plane[1]), "r"(plane[1] & 0xff00ff00u));
     plane[2] += 0x00800080u;
 }
-__device__ __forceinline__ bool not_finite(const uint4& v) {  // any of eight bf16 values
+// Any of eight bf16 values infinite, NaN or of 2^91 and more: a weight may be 2^27.9 in the
+// sums' units, and 512 of them times 2^91 stay below float32's 2^128.
+__device__ __forceinline__ bool too_large(const uint4& v) {
     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
     bool bad = false;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bad = bad || (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+    for (int e = 0; e < 4; ++e) bad = bad || (x[e] & 0x7f80u) >= 0x6d00u || (x[e] & 0x7f800000u) >= 0x6d000000u;
     return bad;
 }
 __device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) { return (uint32_t)lo | (uint32_t)hi << 16; }
@@ -881,14 +883,14 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     ok = warp_wait(full0 + 8 * ((sl + 1) % R), (uint32_t)(((sl + 1) / R) & 1), lim) && ok;
                     const int m = (s.t0 + t - pt) * kTile + key;  // tree row
                     valid = m < w.N;
-                    // A tree row whose V is not finite: 0 * inf of a query row that does not see
+                    // A tree row whose V is not finite (or too large): 0 * inf of a query row that does not see
                     // it would spoil that one, so its V counts as zero and rows that see it get
                     // NaN.  Of two streams that share the tile stream 0 looks.
                     if (!SHARED || st == 0) {
                         const uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
 #pragma unroll 4
                         for (int c = 0; c < D / 8; ++c)
-                            bad_v = not_finite(*reinterpret_cast<const uint4*>(v + (c >> 3) * kTile * 128 +
+                            bad_v = too_large(*reinterpret_cast<const uint4*>(v + (c >> 3) * kTile * 128 +
                                                                                (((c + lane) & 7) << 4))) || bad_v;
                         if constexpr (SHARED) {
                             const unsigned bad = __ballot_sync(0xffffffffu, bad_v);

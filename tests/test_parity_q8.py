@@ -261,6 +261,42 @@ def test_attention_infinities_where_the_mask_hides_them(medusa, dtype):
         assert np.isnan(got[0, hurt, h]).all()
 
 
+@pytest.mark.parametrize("N", [6, 70])
+def test_attention_large_tree_values(medusa, N):
+    """V of the tree up to 2^91 is summed without overflow, over pages of small scales
+    too; from there on it counts as infinite."""
+    c = attention_case(42, 1, N, 2, 2, 64, 16, [300], "bf16")
+    c["v_scale"] = c["v_scale"] * np.float32(2.0 ** -20)
+    c["v_tree"] = as_dtype(c["v_tree"] * 2.0 ** 88, "bf16")
+    c["v_tree"][0, 0] = 2.0 ** 90.9
+    c["v_tree"] = as_dtype(c["v_tree"], "bf16")
+    assert np.abs(c["v_tree"]).max() < 2.0 ** 91
+    check(c, attend(medusa, c), reference(c))
+    c["v_tree"][0, 2, 1, 5] = -2.0 ** 91
+    got, seen = attend(medusa, c), R.sees(c["mask"], N)
+    assert np.isnan(got[0, seen[:, 2], 1]).all() and np.isfinite(got[0, ~seen[:, 2]]).all() and np.isfinite(got[0, :, 0]).all()
+
+
+def test_attention_two_streams_at_once(medusa):
+    """Calls on two streams, each with its workspace, do not disturb one another."""
+    cases = [attention_case(43, 2, 64, 4, 4, 128, 64, [900, 400], "bf16"), attention_case(44, 3, 1, 8, 2, 128, 32, [3000, 1, 700], "bf16")]
+    alone = [attend(medusa, c) for c in cases]
+    t = [[dev(c[n], "bf16") for n in ("q", "k_tree", "v_tree")] + [to_dev(c[n]) for n in NAMES + ("table", "kv_len", "mask")] for c in cases]
+    outs = [[torch.empty_like(x[0]) for _ in range(20)] for x in t]
+    ws = [torch.empty(medusa.tree_attention_q8_workspace(*x[0].shape[:3], x[3].shape[1], x[0].shape[3]), dtype=torch.uint8, device="cuda")
+          for x in t]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for i in range(20):
+        for x, o, w, c, s in zip(t, outs, ws, cases, streams):
+            medusa.tree_attention_q8(*x, c["scale"], out=o[i], ws=w, stream=s)
+    torch.cuda.synchronize()
+    medusa.device_status()
+    for a, o in zip(alone, outs):
+        for x in o:
+            assert np.array_equal(x.double().cpu().numpy(), a)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attention_same_call_same_bits_and_other_stream(medusa, dtype):
     c = attention_case(17, 3, 64, 4, 4, 128, 64, [700, 1300, 20], dtype)
