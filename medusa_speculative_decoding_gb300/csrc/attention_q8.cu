@@ -398,9 +398,7 @@ __device__ __forceinline__ void bar_sync(int id, int n) {
 }
 // All lanes wait; the same answer in all of them.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long lim) {
-    const bool ok = umma::mbar_wait(bar, parity, lim);
-    __syncwarp();
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, umma::mbar_wait(bar, parity, lim));
 }
 // pairs of floats on the paired float32 pipe
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
@@ -495,6 +493,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         mbar_init(p_full0 + 8, kUStream / 32);
         if (SHARED)  // a slot is free when both streams' products are through
             for (int i = 0; i < R; ++i) mbar_init(empty0 + 8 * i, 2);
+        for (int i = 0; i < 4; ++i) mbar_init(s_full0 + 8 * i, 2);  // the products, and the MMA warp itself
         mbar_init(qfull, kUSoftmax / 32);
         mbar_init(seen, 2);
         mbar_init(checked0, 4);
@@ -588,6 +587,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                                           dq + (((ks >> 2) * (NB * 128) + (ks & 3) * 32) >> 4), id_st, ks > 0);
                     }
                     commit_warp(s_full + 8 * (ns & 1));
+                    // (this arrival hands on the scales, which came with the slot)
+                    if (lane == 0) mbar_arrive(s_full + 8 * (ns & 1));
                     ++ns;
                     sl = slot_of(tile_of(ns));
                     s_stage = sl % R;
@@ -871,8 +872,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 bool valid, bad_v = false;
                 uint64_t sees = ~0ull;  // rows that see the key
                 if constexpr (!tree) {
-                    // the slot is in since the scores are; this wait makes the scales visible
-                    ok = warp_wait(full0 + 8 * (sl % R), (uint32_t)((sl / R) & 1), lim) && ok;
                     const float2 sc = s_info[(sl % R) * 8 + (key >> page_shift)];
                     valid = sc.y > 0.f && (s.t0 + t) * kTile + key < s.L;
                     kc = kq * sc.x;
