@@ -86,7 +86,9 @@ __device__ __forceinline__ void plan_share(const AttnQ8Args& a, const q8::Offset
 // ---------------------------------------------------------------------------
 // One CTA works through its share of (unit, tile) pairs; a unit's block has
 // kRows query rows.  Each tile of kKeys keys is dequantised into shared memory
-// once for all rows; scores, softmax and sums are float32.
+// once for all rows; scores, softmax and sums are float32.  What bounds it at the
+// sizes that float32 is for is latency: 13 us with the merge for nine rows, four
+// heads of 64 and 128 keys.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 16, kKeys = 64, kSimpleThreads = 256;
 
@@ -323,6 +325,13 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
 // The tree's rows are bf16: such a tile takes two slots, and its products are
 // kind::f16 with q and P in bf16, added to the same sums.
 // Every wait is bounded; a CTA that gives up marks its results NaN.
+//
+// Measured, merge included: 99 us for eight sequences of 1024 to 4096 keys, 40 heads, 64
+// rows (231 MB, 2.3 TB/s); 385 us for four of 8192 keys, 32 heads, 341 rows (191 GFLOP, 495
+// TFLOP/s); 54 us for sixteen of 777 to 16384 keys, 8 heads of 4 rows (282 MB, 5.2 TB/s); 22
+// us for one of 2048 keys, 32 heads, 64 rows.  With 64 rows and more what bounds it is the
+// issue of the softmax warps: 13.5 cycles per 32 weights and scheduler for weights and
+// planes alone, 9 of them without the planes; with 16 rows, the tiles under way.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;  // keys per tile
 constexpr int kUSoftmax = 256, kUThreads = kUSoftmax + 96;
@@ -923,9 +932,9 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     }
                 };
                 const bool partial = tree || __any_sync(0xffffffffu, !valid);
-                // The scores are formed twice from TMEM, for the check and for the weights, WX
-                // columns at a time: held in between they would not fit next to the sums, and
-                // what the compiler then spills does not fit L1 next to this much shared memory.
+                // Scores less the references.  They are read from TMEM again wherever they are
+                // needed: held in between they would not fit next to the sums, and what the
+                // compiler then spills does not fit L1 next to this much shared memory.
                 auto relative = [&](int c0, auto& x, int n) {
 #pragma unroll
                     for (int e = 0; e < n; e += 4) {
@@ -956,11 +965,9 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
                     float top = -INFINITY;
                     if constexpr (!tree) {
-                        // sixteen columns at a time.  Shared blocks have many such tiles one after
-                        // the other and load the next columns ahead (450 us against 466 for 341
-                        // rows over 8192 keys); the others have a stream's last and first tiles
-                        // side by side and gain more from the registers (119 us against 123 for
-                        // eight sequences of 64 rows).
+                        // Sixteen columns at a time.  Shared blocks load the next ones ahead (409 us
+                        // against 423 for 341 rows over 8192 keys); the others gain more from the
+                        // registers (119 us against 123 for eight sequences of 64 rows).
                         constexpr int W = 16, kAhead = SHARED ? 1 : 0;
                         float x[1 + kAhead][W];
                         if constexpr (kAhead) tmem_ld16(tS, x[0]);
