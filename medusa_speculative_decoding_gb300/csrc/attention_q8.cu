@@ -28,6 +28,8 @@ namespace {
 
 MEDUSA_WAIT_CONTROL()
 
+using q8::mul2;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnQ8Args {
@@ -414,11 +416,6 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
     asm("{\n.reg .b64 ra, rb, rc, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\nmov.b64 rc, {%5, %6};\n"
         "fma.rn.f32x2 rd, ra, rb, rc;\nmov.b64 {%0, %1}, rd;\n}"
         : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
-}
-__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b) {
-    asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\n"
-        "mul.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}"
-        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b));
 }
 __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
     asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%0, %1};\nmov.b64 rb, {%2, %3};\n"

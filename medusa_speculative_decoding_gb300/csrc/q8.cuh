@@ -54,6 +54,13 @@ __device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
     return c;
 }
 
+// two products on the paired float32 pipe
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b) {
+    asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %4};\n"
+        "mul.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b));
+}
+
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // ---------------------------------------------------------------------------
