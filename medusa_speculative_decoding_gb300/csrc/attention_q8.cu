@@ -73,6 +73,7 @@ __device__ __forceinline__ float weight(float x) { return exp2f(x); }
 // -1: none.  One thread; it is off every path that others wait for.
 __device__ __forceinline__ void plan_share(const AttnQ8Args& a, const q8::Offsets& first, int rows_block) {
     const q8::Work& w = a.work;
+    if (w.whole) return;  // there is no merge
     const uint32_t total = first.total(w);
     const uint32_t g_begin = w.cta_begin(total, blockIdx.x), g_end = w.cta_begin(total, blockIdx.x + 1);
     int4 p = make_int4(-1, 0, 0, 0);
@@ -124,9 +125,8 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
     pdl_wait();
     pdl_trigger();
     q8::tile_offsets(w, a.kv_len, first);
-    const uint32_t total = first.total(w);
-    uint32_t g = w.cta_begin(total, blockIdx.x);
-    const uint32_t g_end = w.cta_begin(total, blockIdx.x + 1);
+    const uint32_t g_begin = q8::share_begin(w, first, blockIdx.x), g_end = q8::share_begin(w, first, blockIdx.x + 1);
+    uint32_t g = g_begin;
     const int rows_all = w.N * a.G;
     constexpr int ACC = kRows * D / kSimpleThreads;  // output rows per thread (one column)
     const int d = tid % D, r0 = tid / D * ACC;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
         __syncthreads();  // q, statistics free again
     }
     // an empty share gives nothing to the units around it
-    if (tid < kRows && w.cta_begin(total, blockIdx.x) == g_end)
+    if (tid < kRows && g_begin == g_end)
         a.part_ml[(size_t)2 * blockIdx.x * kRows + tid] = make_float2(-INFINITY, 0.f);
     if (tid == 0) plan_share(a, first, kRows);
 }
@@ -519,8 +519,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t total = first.total(w);
-    const uint32_t g_begin = w.cta_begin(total, blockIdx.x), g_end = w.cta_begin(total, blockIdx.x + 1);
+    const uint32_t g_begin = q8::share_begin(w, first, blockIdx.x), g_end = q8::share_begin(w, first, blockIdx.x + 1);
     const int ppt = kTile / a.P;  // pages per tile
     const int rows_all = w.N * a.G;
     uint32_t g_failed = g_end;   // first segment whose results are not there
@@ -1370,16 +1369,20 @@ __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const Attn
 }
 
 struct Plan {
-    int rows, keys, setup, ctas;
+    int rows, keys, setup, ctas, whole;
 };
 // Rows per block, by the rows a KV head has: 16 (plain decoding), 64, or 128 in
-// two streams.
+// two streams.  Units that the table's width holds to `whole` tiles are not cut, which
+// saves the merge.  bf16, cut against whole: at three tiles 17.1 / 13.8 us (one sequence, 32
+// heads, 64 rows), 42 / 38 (eight, 40 heads), 9.4 / 8.0 (one of one token, 8 heads), 24.7 /
+// 22.1 (one, 8 heads, 200 rows); at four and five 24.8 / 27.5 (the last), 19.0 / 19.5 (the
+// first).  float32: at two tiles 12.5 / 12.3 us, at three 13.7 / 17.0.
 Plan plan_q8(medusa_dtype dtype, int N, int G) {
     const int rows = N * G, sms = sm_count();
-    if (dtype == MEDUSA_F32) return Plan{kRows, kKeys, 1, 2 * sms};
-    if (rows <= 16) return Plan{16, kTile, kSetup16, sms};
-    if (rows <= 64) return Plan{64, kTile, kSetup, sms};
-    return Plan{128, kTile, kSetup, sms};
+    if (dtype == MEDUSA_F32) return Plan{kRows, kKeys, 1, 2 * sms, 2};
+    if (rows <= 16) return Plan{16, kTile, kSetup16, sms, 3};
+    if (rows <= 64) return Plan{64, kTile, kSetup, sms, 3};
+    return Plan{128, kTile, kSetup, sms, 3};
 }
 
 int check_attn_q8(int B, int N, int Hq, int Hkv, int D, int P, int n_pages, int M) {
@@ -1397,7 +1400,7 @@ template <typename T, int D>
 cudaError_t launch_merge(const AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     constexpr int rows = kMergeThreads / (D / 4);  // of a block
     const int all = a.work.N * a.G, most = all < p.rows ? all : p.rows;
-    return launch(attn_q8_merge_kernel<T, D>, dim3(p.ctas, (most + rows - 1) / rows), dim3(kMergeThreads), 0, st, a, p.rows);
+    return launch(attn_q8_merge_kernel<T, D>, dim3(a.work.ctas, (most + rows - 1) / rows), dim3(kMergeThreads), 0, st, a, p.rows);
 }
 
 template <typename T, int D>
@@ -1405,9 +1408,8 @@ cudaError_t launch_simple(AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     auto kern = tree_attn_q8_simple_kernel<T, D>;
     const int smem = SimpleSmem<D>::bytes(a.work.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch(kern, dim3(p.ctas), dim3(kSimpleThreads), smem, st, a);
-    if (e == cudaSuccess)
-        e = launch_merge<T, D>(a, p, st);
+    if (e == cudaSuccess) e = launch(kern, dim3(a.work.ctas), dim3(kSimpleThreads), smem, st, a);
+    if (e == cudaSuccess && !a.work.whole) e = launch_merge<T, D>(a, p, st);
     return e;
 }
 
@@ -1446,9 +1448,8 @@ cudaError_t launch_umma(const CUtensorMap (&m)[4], AttnQ8Args& a, const Plan& p,
     auto kern = tree_attn_q8_umma_kernel<D, NB, SHARED>;
     const int smem = USmem<D, NB, SHARED>::bytes(a.work.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch(kern, dim3(p.ctas), dim3(kUThreads), smem, st, m[0], m[1], m[2], m[3], a);
-    if (e == cudaSuccess)
-        e = launch_merge<uint16_t, D>(a, p, st);
+    if (e == cudaSuccess) e = launch(kern, dim3(a.work.ctas), dim3(kUThreads), smem, st, m[0], m[1], m[2], m[3], a);
+    if (e == cudaSuccess && !a.work.whole) e = launch_merge<uint16_t, D>(a, p, st);
     return e;
 }
 
@@ -1493,7 +1494,10 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     a.plan = (int4*)(a.part_ml + (size_t)2 * p.ctas * p.rows);
     a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.P = P; a.M = M; a.n_pages = n_pages; a.W = (N + 63) / 64;
     a.qblocks = (N * a.G + p.rows - 1) / p.rows;
-    a.work = q8::Work{B, N, Hkv * a.qblocks, p.keys, p.setup, M * P, p.ctas};
+    const long long tiles = ((long long)M * P + p.keys - 1) / p.keys + (N + p.keys - 1) / p.keys;  // of the longest unit
+    const long long units = (long long)B * Hkv * a.qblocks;
+    const bool whole = tiles <= p.whole && units <= 1 << 20;  // (share_begin counts in 32 bits)
+    a.work = q8::Work{B, N, Hkv * a.qblocks, p.keys, p.setup, M * P, whole && units < p.ctas ? (int)units : p.ctas, whole};
     if ((long long)B * a.work.U * (((long long)M * P + p.keys - 1) / p.keys + (N + p.keys - 1) / p.keys + p.setup) > 0x7fffffffll)
         return fail(MEDUSA_ERR_UNSUPPORTED, "tree_attention_q8: %d sequences of up to %lld tokens are too many tiles", B,
                     (long long)M * P);

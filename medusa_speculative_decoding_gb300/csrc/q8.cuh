@@ -71,9 +71,11 @@ __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo 
 // tiles more, in front of its own, for what taking it up and handing its result out
 // costs.  A CTA's share is a run of segments, each a range of one unit's tiles; a
 // unit that several CTAs share leaves one partial result per CTA, joined by a merge
-// kernel.
+// kernel.  Where no unit can have more than a few tiles (the tables' width bounds them on
+// the host) the units themselves are shared out, and there is nothing to join.
 struct Work {
-    int B, N, U, T, V, cap, ctas;  // U units per sequence, T keys per tile, cap slots per sequence
+    // U units per sequence, T keys per tile, cap slots per sequence, whole: no unit is cut
+    int B, N, U, T, V, cap, ctas, whole;
     __device__ __forceinline__ int len(const int32_t* kv_len, int b) const { return clamp_int(kv_len[b], 0, cap); }
     __device__ __forceinline__ int prefix_tiles(int L) const { return (L + T - 1) / T; }
     __device__ __forceinline__ int tree_tiles() const { return (N + T - 1) / T; }
@@ -135,6 +137,16 @@ __device__ __forceinline__ int find_sequence(const uint32_t* first, int B, uint3
         if (first[mid] <= g) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// Where the share of CTA c begins (c = ctas: where the last one ends).
+__device__ __forceinline__ uint32_t share_begin(const Work& w, const Offsets& t, int c) {
+    const uint32_t total = t.total(w);
+    if (!w.whole) return w.cta_begin(total, c);
+    const uint32_t units = (uint32_t)w.B * w.U, u = (uint32_t)c * units / (uint32_t)w.ctas;
+    if (u == units) return total;
+    const uint32_t b = u / (uint32_t)w.U;
+    return t.first[b] + (u - b * w.U) * ((t.first[b + 1] - t.first[b]) / (uint32_t)w.U);
 }
 
 // Tiles [t0, t1) of unit `unit` of sequence b.

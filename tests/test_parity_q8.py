@@ -261,6 +261,20 @@ def test_attention_infinities_where_the_mask_hides_them(medusa, dtype):
         assert np.isnan(got[0, hurt, h]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,P,lens", [(1, 1, 2, 1, 64, 16, [1]), (3, 1, 8, 2, 128, 32, [40, 0, 64]),
+                                                 (70, 9, 4, 4, 64, 16, [37] * 70), (2, 64, 40, 40, 128, 64, [64, 17]),
+                                                 (5, 33, 80, 80, 64, 64, [3, 64, 20, 0, 1]), (2, 90, 3, 3, 128, 16, [50, 64])])
+def test_attention_narrow_and_wide_tables(medusa, B, N, Hq, Hkv, D, P, lens, dtype):
+    """Short texts in tables that hold no more (units are not cut then) and in wide ones."""
+    c = attention_case(45, B, N, Hq, Hkv, D, P, lens, dtype)
+    c["table"] = c["table"][:, :-(-64 // P)]
+    ref = reference(c)
+    check(c, attend(medusa, c), ref)
+    wide = dict(c, table=np.concatenate([c["table"], np.full((B, 3000 // P), -1, np.int32)], 1))
+    check(wide, attend(medusa, wide), ref)
+
+
 @pytest.mark.parametrize("N", [6, 70])
 def test_attention_large_tree_values(medusa, N):
     """V of the tree up to 2^91 is summed without overflow, over pages of small scales

@@ -17,6 +17,7 @@ pytestmark = pytest.mark.gpu
     (2, 1, 8, 2, 128, 64, [900, 30]),         # blocks of 16 rows
     (3, 40, 4, 4, 64, 16, [2000, 0, 333]),    # of 64
     (2, 150, 4, 4, 128, 32, [1500, 77]),      # of 128, the streams share tiles
+    (2, 20, 4, 2, 128, 64, [100, 30]),        # units that are not cut
 ])
 def test_wait_give_up_is_reported_and_the_next_calls_are_correct(medusa, B, N, Hq, Hkv, D, P, lens):
     M = medusa
