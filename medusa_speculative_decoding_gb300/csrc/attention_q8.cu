@@ -88,37 +88,41 @@ __device__ __forceinline__ void plan_share(const AttnQ8Args& a, const q8::Offset
 
 // ---------------------------------------------------------------------------
 // One CTA works through its share of (unit, tile) pairs; a unit's block has
-// kRows query rows.  Each tile of kKeys keys is dequantised into shared memory
-// once for all rows; scores, softmax and sums are float32.  What bounds it at the
-// sizes that float32 is for is latency: 13 us with the merge for nine rows, four
-// heads of 64 and 128 keys.
+// ROWS query rows, 16 or 64.  Each tile of kKeys keys is dequantised into shared
+// memory once for all rows; scores, softmax and sums are float32.  A thread has four
+// rows and KT keys (then CP columns) of each product.  Small calls are bound by
+// latency: 13 us with the merge for nine rows, four heads of 64 and 128 keys.  Large
+// ones by issue and shared memory: with blocks of 16 rows, whose every key is
+// dequantised anew, 147 us for three sequences of 2730 keys, 8 heads of 64 and 64 rows, with
+// 64 rows 68 (85 with 512 threads); at D = 128, 2000 keys and two sequences 83 and 69 (78
+// with 256 threads, of which an SM holds one block).
 // ---------------------------------------------------------------------------
-constexpr int kRows = 16, kKeys = 64, kSimpleThreads = 256;
+constexpr int kKeys = 64;
 
-template <int D>
+template <int D, int ROWS>
 struct SimpleSmem {
-    static constexpr int kStrideK = D + 4;  // rows 16 bytes apart in the banks
-    static constexpr int kOffV = kKeys * kStrideK * 4;
+    static constexpr int kStride = D + 4, kStrideP = kKeys + 4;  // rows 16 bytes apart in the banks
+    static constexpr int kOffV = kKeys * kStride * 4;
     static constexpr int kOffQ = kOffV + kKeys * D * 4;
-    static constexpr int kOffP = kOffQ + kRows * D * 4;
-    static constexpr int kOffStat = kOffP + kRows * kKeys * 4;  // corr, m, l
-    static constexpr int kOffFirst = kOffStat + 3 * kRows * 4;  // tile offsets
+    static constexpr int kOffP = kOffQ + ROWS * kStride * 4;
+    static constexpr int kOffStat = kOffP + ROWS * kStrideP * 4;  // corr, m, l
+    static constexpr int kOffFirst = kOffStat + 3 * ROWS * 4;  // tile offsets
     static int bytes(int B) { return kOffFirst + q8::offsets_bytes(B); }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(const AttnQ8Args a) {
-    using L = SimpleSmem<D>;
+template <typename T, int D, int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const AttnQ8Args a) {
+    using L = SimpleSmem<D, ROWS>;
     extern __shared__ __align__(16) uint8_t smem[];
     float* sk = reinterpret_cast<float*>(smem);
     float* sv = reinterpret_cast<float*>(smem + L::kOffV);
     float* sq = reinterpret_cast<float*>(smem + L::kOffQ);
     float* sp = reinterpret_cast<float*>(smem + L::kOffP);
     float* s_corr = reinterpret_cast<float*>(smem + L::kOffStat);
-    float* s_m = s_corr + kRows;
-    float* s_l = s_m + kRows;
+    float* s_m = s_corr + ROWS;
+    float* s_l = s_m + ROWS;
     const q8::Offsets first(smem + L::kOffFirst, a.work.B);
-    __shared__ uint32_t s_seen[kKeys];  // rows that see the key, one bit each
+    __shared__ uint64_t s_seen[kKeys];  // rows that see the key, one bit each
     __shared__ int s_bad[kKeys];        // tree key whose V row holds an infinity or NaN
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const q8::Work w = a.work;
@@ -128,24 +132,28 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
     const uint32_t g_begin = q8::share_begin(w, first, blockIdx.x), g_end = q8::share_begin(w, first, blockIdx.x + 1);
     uint32_t g = g_begin;
     const int rows_all = w.N * a.G;
-    constexpr int ACC = kRows * D / kSimpleThreads;  // output rows per thread (one column)
-    const int d = tid % D, r0 = tid / D * ACC;
+    // this thread's four rows; its KT keys, KL apart; its CP columns, CW side by side
+    constexpr int KT = ROWS * kKeys / (4 * THREADS), KL = kKeys / KT, CP = D * ROWS / (4 * THREADS), CW = CP < 4 ? CP : 4;
+    const int r0 = tid / KL * 4, kl = tid % KL;
+    auto column = [&](int j) { return (j / CW * KL + kl) * CW + j % CW; };
     for (q8::Segment s; q8::next_segment(w, first, g, g_end, s); g = s.end) {
-        const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * kRows;
-        const int nrows = min(kRows, rows_all - row0);
-        for (int i = tid; i < kRows * D; i += kSimpleThreads) {
+        const int hk = s.unit / a.qblocks, row0 = s.unit % a.qblocks * ROWS;
+        const int nrows = min(ROWS, rows_all - row0);
+        for (int i = tid; i < ROWS * D; i += THREADS) {
             const int r = row0 + i / D;
             float v = 0.f;
             if (i / D < nrows)
                 v = load1(static_cast<const T*>(a.q) +
                           (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + i % D);
-            sq[i] = v;
+            sq[i / D * L::kStride + i % D] = v;
         }
-        if (tid < kRows) { s_m[tid] = -INFINITY; s_l[tid] = 0.f; }
+        if (tid < ROWS) { s_m[tid] = -INFINITY; s_l[tid] = 0.f; }
         if (tid < kKeys) s_bad[tid] = 0;
-        float acc[ACC];
+        float acc[4][CP];
 #pragma unroll
-        for (int i = 0; i < ACC; ++i) acc[i] = 0.f;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < CP; ++j) acc[i][j] = 0.f;
         const int pt = w.prefix_tiles(s.L);
         for (int t = s.t0; t < s.t1; ++t) {
             __syncthreads();
@@ -153,7 +161,7 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
             const int k0 = tree ? (t - pt) * kKeys : t * kKeys;
             const int nk = min(kKeys, (tree ? w.N : s.L) - k0);
             // keys of the tile, 8 elements a step; absent ones read zero
-            for (int i = tid; i < kKeys * (D / 8); i += kSimpleThreads) {
+            for (int i = tid; i < kKeys * (D / 8); i += THREADS) {
                 const int key = i / (D / 8), c = i % (D / 8) * 8;
                 float kx[8], vx[8];
 #pragma unroll
@@ -193,42 +201,54 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
                 }
 #pragma unroll
                 for (int e = 0; e < 8; e += 4) {
-                    *reinterpret_cast<float4*>(sk + key * L::kStrideK + c + e) = make_float4(kx[e], kx[e + 1], kx[e + 2], kx[e + 3]);
+                    *reinterpret_cast<float4*>(sk + key * L::kStride + c + e) = make_float4(kx[e], kx[e + 1], kx[e + 2], kx[e + 3]);
                     *reinterpret_cast<float4*>(sv + key * D + c + e) = make_float4(vx[e], vx[e + 1], vx[e + 2], vx[e + 3]);
                 }
                 if (c == 0) {
-                    uint32_t seen = there ? 0xffffu : 0u;
+                    uint64_t seen = there ? ~0ull : 0ull;
                     if (there && tree) {
                         seen = 0;
                         const int m = k0 + key;
                         for (int r = 0; r < nrows; ++r)
-                            seen |= (uint32_t)((a.mask[(size_t)((row0 + r) / a.G) * a.W + (m >> 6)] >> (m & 63)) & 1) << r;
+                            seen |= ((a.mask[(size_t)((row0 + r) / a.G) * a.W + (m >> 6)] >> (m & 63)) & 1) << r;
                     }
                     s_seen[key] = seen;
                 }
             }
             __syncthreads();
-            {   // scores: thread = (key, four rows)
-                const int key = tid % kKeys, rq = tid / kKeys * 4;
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-                for (int c = 0; c < D; c += 4) {
-                    const float4 kx = *reinterpret_cast<const float4*>(sk + key * L::kStrideK + c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 qx = *reinterpret_cast<const float4*>(sq + (rq + i) * D + c);
-                        z[i] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, z[i]))));
-                    }
-                }
-                const uint32_t seen = s_seen[key];
+            {
+                float z[4][KT];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sp[(rq + i) * kKeys + key] = (seen >> (rq + i)) & 1 ? z[i] * a.scale_log2 : -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) z[i][j] = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D; c += 4) {
+                    float4 kx[KT], qx[4];
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) kx[j] = *reinterpret_cast<const float4*>(sk + (kl + j * KL) * L::kStride + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qx[i] = *reinterpret_cast<const float4*>(sq + (r0 + i) * L::kStride + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < KT; ++j)
+                            z[i][j] = fmaf(qx[i].x, kx[j].x, fmaf(qx[i].y, kx[j].y, fmaf(qx[i].z, kx[j].z, fmaf(qx[i].w, kx[j].w, z[i][j]))));
+                }
+#pragma unroll
+                for (int j = 0; j < KT; ++j) {
+                    const uint64_t seen = s_seen[kl + j * KL];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sp[(r0 + i) * L::kStrideP + kl + j * KL] = (seen >> (r0 + i)) & 1 ? z[i][j] * a.scale_log2 : -INFINITY;
+                }
             }
             __syncthreads();
-            // running maximum and sum: two rows per warp
-            for (int r = 2 * warp; r < 2 * warp + 2; ++r) {
-                const float x0 = sp[r * kKeys + lane], x1 = sp[r * kKeys + lane + 32];
+            // running maximum and sum, several rows per warp
+            constexpr int RW = ROWS * 32 / THREADS;
+#pragma unroll 4
+            for (int r = RW * warp; r < RW * (warp + 1); ++r) {
+                const float x0 = sp[r * L::kStrideP + lane], x1 = sp[r * L::kStrideP + lane + 32];
                 float mx = fmaxf(x0, x1);
                 // a NaN score makes the row NaN: the sum below carries it
 #pragma unroll
@@ -239,8 +259,8 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
                 float sum = warp_sum(p0 + p1);
                 const bool bad = (s_bad[lane] && (s_seen[lane] >> r & 1)) || (s_bad[lane + 32] && (s_seen[lane + 32] >> r & 1));
                 if (__any_sync(0xffffffffu, bad)) sum = NAN;
-                sp[r * kKeys + lane] = p0;
-                sp[r * kKeys + lane + 32] = p1;
+                sp[r * L::kStrideP + lane] = p0;
+                sp[r * L::kStrideP + lane + 32] = p1;
                 if (lane == 0) {
                     const float c = weight(m0 - ref);  // 0 where nothing was seen before
                     s_corr[r] = c;
@@ -251,39 +271,55 @@ __global__ void __launch_bounds__(kSimpleThreads) tree_attn_q8_simple_kernel(con
             __syncthreads();
             if (tid < kKeys) s_bad[tid] = 0;
 #pragma unroll
-            for (int i = 0; i < ACC; ++i) acc[i] *= s_corr[r0 + i];
-#pragma unroll 4
+            for (int i = 0; i < 4; ++i) {
+                const float c = s_corr[r0 + i];
+#pragma unroll
+                for (int j = 0; j < CP; ++j) acc[i][j] *= c;
+            }
+#pragma unroll 2
             for (int k = 0; k < kKeys; k += 4) {
-                const float v0 = sv[k * D + d], v1 = sv[(k + 1) * D + d], v2 = sv[(k + 2) * D + d], v3 = sv[(k + 3) * D + d];
+                float p[4][4], v[4][CP];
 #pragma unroll
-                for (int i = 0; i < ACC; ++i) {
-                    const float4 p = *reinterpret_cast<const float4*>(sp + (r0 + i) * kKeys + k);
-                    acc[i] = fmaf(p.x, v0, fmaf(p.y, v1, fmaf(p.z, v2, fmaf(p.w, v3, acc[i]))));
-                }
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(sp + (r0 + i) * L::kStrideP + k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < CP; j += CW) {
+                        const float* from = sv + (k + e) * D + column(j);
+                        if constexpr (CW == 4) *reinterpret_cast<float4*>(v[e] + j) = *reinterpret_cast<const float4*>(from);
+                        else if constexpr (CW == 2) *reinterpret_cast<float2*>(v[e] + j) = *reinterpret_cast<const float2*>(from);
+                        else v[e][j] = *from;
+                    }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < CP; ++j) acc[i][j] = fmaf(p[i][e], v[e][j], acc[i][j]);
             }
         }
-        if (s.whole()) {
+        const bool whole = s.whole();
+        const size_t part = (size_t)s.slot(blockIdx.x) * ROWS;
 #pragma unroll
-            for (int i = 0; i < ACC; ++i) {
-                const int r = row0 + r0 + i;
-                if (r0 + i < nrows) {
-                    const float l = s_l[r0 + i];
-                    store1(static_cast<T*>(a.out) + (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + d,
-                           l == 0.f ? 0.f : acc[i] / l);
-                }
+        for (int i = 0; i < 4; ++i) {
+            const int r = row0 + r0 + i;
+            const float l = s_l[r0 + i];
+            if (whole && r0 + i >= nrows) continue;
+            T* out = static_cast<T*>(a.out) + (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D;
+#pragma unroll
+            for (int j = 0; j < CP; ++j) {
+                if (whole) store1(out + column(j), l == 0.f ? 0.f : acc[i][j] / l);
+                else a.part_o[(part + r0 + i) * D + column(j)] = acc[i][j];
             }
-        } else {
-            const size_t base = (size_t)s.slot(blockIdx.x) * kRows;
-#pragma unroll
-            for (int i = 0; i < ACC; ++i) a.part_o[(base + r0 + i) * D + d] = acc[i];
-            if (tid < kRows) a.part_ml[base + tid] = make_float2(s_m[tid], s_l[tid]);
         }
+        if (!whole && tid < ROWS) a.part_ml[part + tid] = make_float2(s_m[tid], s_l[tid]);
         __syncthreads();  // q, statistics free again
     }
     // an empty share gives nothing to the units around it
-    if (tid < kRows && g_begin == g_end)
-        a.part_ml[(size_t)2 * blockIdx.x * kRows + tid] = make_float2(-INFINITY, 0.f);
-    if (tid == 0) plan_share(a, first, kRows);
+    if (tid < ROWS && g_begin == g_end)
+        a.part_ml[(size_t)2 * blockIdx.x * ROWS + tid] = make_float2(-INFINITY, 0.f);
+    if (tid == 0) plan_share(a, first, ROWS);
 }
 
 // ---------------------------------------------------------------------------
@@ -1377,9 +1413,9 @@ struct Plan {
 // heads, 64 rows), 42 / 38 (eight, 40 heads), 9.4 / 8.0 (one of one token, 8 heads), 24.7 /
 // 22.1 (one, 8 heads, 200 rows); at four and five 24.8 / 27.5 (the last), 19.0 / 19.5 (the
 // first).  float32: at two tiles 12.5 / 12.3 us, at three 13.7 / 17.0.
-Plan plan_q8(medusa_dtype dtype, int N, int G) {
+Plan plan_q8(medusa_dtype dtype, int N, int G, int D) {
     const int rows = N * G, sms = sm_count();
-    if (dtype == MEDUSA_F32) return Plan{kRows, kKeys, 1, 2 * sms, 2};
+    if (dtype == MEDUSA_F32) return rows <= 32 ? Plan{16, kKeys, 1, 2 * sms, 2} : Plan{64, kKeys, 1, D == 64 ? 2 * sms : sms, 2};
     if (rows <= 16) return Plan{16, kTile, kSetup16, sms, 3};
     if (rows <= 64) return Plan{64, kTile, kSetup, sms, 3};
     return Plan{128, kTile, kSetup, sms, 3};
@@ -1403,12 +1439,12 @@ cudaError_t launch_merge(const AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     return launch(attn_q8_merge_kernel<T, D>, dim3(a.work.ctas, (most + rows - 1) / rows), dim3(kMergeThreads), 0, st, a, p.rows);
 }
 
-template <typename T, int D>
+template <typename T, int D, int ROWS, int THREADS>
 cudaError_t launch_simple(AttnQ8Args& a, const Plan& p, cudaStream_t st) {
-    auto kern = tree_attn_q8_simple_kernel<T, D>;
-    const int smem = SimpleSmem<D>::bytes(a.work.B);
+    auto kern = tree_attn_q8_simple_kernel<T, D, ROWS, THREADS>;
+    const int smem = SimpleSmem<D, ROWS>::bytes(a.work.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch(kern, dim3(a.work.ctas), dim3(kSimpleThreads), smem, st, a);
+    if (e == cudaSuccess) e = launch(kern, dim3(a.work.ctas), dim3(THREADS), smem, st, a);
     if (e == cudaSuccess && !a.work.whole) e = launch_merge<T, D>(a, p, st);
     return e;
 }
@@ -1460,7 +1496,7 @@ using namespace medusa;
 
 extern "C" size_t medusa_tree_attention_q8_workspace(int B, int N, int Hq, int Hkv, int D, medusa_dtype dtype) {
     if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128)) return 0;
-    return ws_bytes_q8(plan_q8(dtype, N, Hq / Hkv), D);
+    return ws_bytes_q8(plan_q8(dtype, N, Hq / Hkv, D), D);
 }
 
 extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype,
@@ -1479,7 +1515,7 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
         return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: q, tree rows, pages and out must be 16-byte aligned");
     if (!(scale > 0.f) || scale > 3.0e38f)
         return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: scale must be positive and finite");
-    const Plan p = plan_q8(dtype, N, Hq / Hkv);
+    const Plan p = plan_q8(dtype, N, Hq / Hkv, D);
     const size_t need = ws_bytes_q8(p, D);
     if (!ws || ws_bytes < need)
         return fail(MEDUSA_ERR_WORKSPACE, "tree_attention_q8: workspace of %zu bytes needed", need);
@@ -1505,7 +1541,8 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     cudaStream_t st = as_stream(stream);
     cudaError_t e;
     if (dtype == MEDUSA_F32) {
-        e = D == 64 ? launch_simple<float, 64>(a, p, st) : launch_simple<float, 128>(a, p, st);
+        e = p.rows == 16 ? (D == 64 ? launch_simple<float, 64, 16, 256>(a, p, st) : launch_simple<float, 128, 16, 256>(a, p, st))
+                         : (D == 64 ? launch_simple<float, 64, 64, 256>(a, p, st) : launch_simple<float, 128, 64, 512>(a, p, st));
     } else {
         CUtensorMap m[4];
         const long long rows = (long long)n_pages * Hkv * P;
