@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const ForkArgs
     umma::cluster_sync();
 
     // 5. rows take their pages; a row's share begins at its offset, so a row that
-    // finds too few leaves them to no one
-    const bool served = fits && (long long)first + takes <= free_pages;
+    // finds too few leaves them to no one.  A row that needs none lacks none.
+    const bool served = fits && (takes == 0 || (long long)first + takes <= free_pages);
     if (b_own < B && rank == 0) {
         int2 c = make_int2(-1, -1);
         if (copies && served) c = make_int2(a.table[(long long)src * M + whole], __ldcg(&a.free_list[first]));

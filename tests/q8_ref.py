@@ -180,7 +180,7 @@ def fork(table, kv_len, n_pages, P, src=None, need=None, held=None):
         copy = keeper[s] != b and length[b] % P != 0
         want = -(-(length[b] + need[b]) // P)
         n = max(want - len(rows[b]), 1 if copy else 0) if want <= M else 0
-        if want > M or asked + n > len(free):
+        if want > M or (n and asked + n > len(free)):
             taken[b] = -1
             if copy:
                 length[b] = length[b] // P * P
