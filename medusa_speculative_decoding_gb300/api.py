@@ -3,12 +3,14 @@
 Argument marshalling only: checks device, dtype and contiguity, allocates the
 outputs and workspaces with torch, and passes raw pointers plus the current CUDA
 stream to libmedusa_gb300.so.  Every step of the computation runs in the
-library's kernels.
+library's kernels.  With `stream` given a call works on that stream, and what it
+allocates belongs to it; inputs have to be ready there.
 """
 from __future__ import annotations
 
 import ctypes as C
 import functools
+import inspect
 
 import numpy as np
 import torch
@@ -49,6 +51,37 @@ def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
+def _tensors(x):
+    if torch.is_tensor(x):
+        yield x
+    elif x is not None:
+        for y in x.values() if isinstance(x, dict) else x:
+            yield from _tensors(y)
+
+
+def _in_stream(f):
+    """Makes `stream`, where one is given, the current one while f allocates and
+    launches.  Memory belongs to the stream that it was allocated on: a workspace of
+    another stream would go to that stream's next tensors when f returns, with the
+    call's kernels still to come.  Results may be used on either stream; the caller
+    orders the two, as for the inputs."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        s = args[at] if len(args) > at else kw.get("stream")
+        if s is None or s == torch.cuda.current_stream():
+            return f(*args, **kw)
+        outer = torch.cuda.current_stream(s.device)
+        with torch.cuda.stream(s):
+            result = f(*args, **kw)
+        for t in _tensors(result):
+            t.record_stream(outer)
+        return result
+
+    return call
+
+
 # ----------------------------------------------------------------------------
 def device_status(stream=None):
     """Synchronises the stream and raises MedusaError (code MEDUSA_ERR_TIMEOUT,
@@ -68,6 +101,7 @@ def heads_topk_workspace(B, K, H, V, topk):
     return int(lib().medusa_heads_topk_workspace(B, K, H, V, topk))
 
 
+@_in_stream
 def heads_topk(h, w1, b1, w2, topk, want_logits=False, out=None, ws=None, stream=None):
     """Medusa heads + per-head top-k.  Returns (topk_idx [B,K,topk] int32,
     topk_val [B,K,topk] float32, logits [B,K,V] float32 or None)."""
@@ -94,6 +128,7 @@ def heads_topk(h, w1, b1, w2, topk, want_logits=False, out=None, ws=None, stream
 HEADS_STATIC_SCRATCH_BYTES = 4 << 20
 
 
+@_in_stream
 def heads_topk_static(h, w1, b1, w2, topk, want_logits=False, out=None, stream=None):
     """heads_topk without a workspace, for callers that cannot allocate device
     memory: the library's own 4 MiB device scratch array is used instead.  Calls
@@ -144,6 +179,7 @@ def tree_layout(paths, max_depth, cap_nodes=4096):
                 retrieve=retrieve[:npth].copy(), max_depth=max_depth)
 
 
+@_in_stream
 def build_tree(topk_idx, root_tok, depth, rank, out=None, stream=None):
     _need(topk_idx, "topk_idx", torch.int32)
     _need(root_tok, "root_tok", torch.int32)
@@ -162,6 +198,7 @@ def tree_attention_workspace(B, N, Hq, Hkv, D, Lmax):
     return int(lib().medusa_tree_attention_workspace(B, N, Hq, Hkv, D, Lmax))
 
 
+@_in_stream
 def tree_attention(q, k_cache, v_cache, kv_len, mask, scale, out=None, ws=None, stream=None):
     """Tree attention; `scale` multiplies q.k inside the softmax (the model's
     choice, usually 1/sqrt(head dim)); it is passed to the library as given."""
@@ -187,6 +224,7 @@ def verify_accept_workspace(B, N, V):
     return int(lib().medusa_verify_accept_workspace(B, N, V))
 
 
+@_in_stream
 def verify_accept_tree(logits, cand, parent, depth, max_depth, mode="greedy", temperature=1.0,
                        eps=0.09, delta=0.3, out=None, ws=None, stream=None):
     _need(logits, "logits", torch.float32)
@@ -216,6 +254,7 @@ def verify_sample_workspace(B, N, V):
     return int(lib().medusa_verify_sample_workspace(B, N, V))
 
 
+@_in_stream
 def verify_accept_tree_sample(logits, cand, parent, depth, max_depth, seed, round_, temperature=1.0,
                               eps=0.09, delta=0.3, out=None, ws=None, stream=None):
     """Typical acceptance; the next token drawn from the best node's softmax."""
@@ -245,6 +284,7 @@ def verify_project_workspace(B, N, H, V):
     return int(lib().medusa_verify_project_workspace(B, N, H, V))
 
 
+@_in_stream
 def verify_project_tree(hidden_tree, lm_head, cand, parent, depth, max_depth, mode="greedy",
                         temperature=1.0, eps=0.09, delta=0.3, out=None, ws=None, stream=None):
     """verify_accept_tree with the verifier logits defined as lm_head . hidden_tree,
@@ -279,6 +319,7 @@ def verify_chain_workspace(B, gamma, V):
     return int(lib().medusa_verify_chain_workspace(B, gamma, V))
 
 
+@_in_stream
 def verify_accept_chain(p, q, draft, seed, round_, out=None, ws=None, stream=None):
     _need(p, "p", torch.float32)
     B, g1, V = p.shape
@@ -301,6 +342,7 @@ def verify_accept_chain(p, q, draft, seed, round_, out=None, ws=None, stream=Non
 
 
 # ----------------------------------------------------------------------------
+@_in_stream
 def kv_compact(k_cache, v_cache, kv_len, path_nodes, accept_len, best_node, N, max_depth,
                hidden_tree=None, h_next=None, src_idx=None, stream=None):
     _need(k_cache, "k_cache")
@@ -364,10 +406,14 @@ def _need_ws(ws, dev):
         raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
 
 
-def _elsewhere(dev):
+def _elsewhere(dev, stream):
     """Whether CUDA device number dev is not the current one (the library works on
     the current device)."""
-    return dev != torch.cuda.current_device()
+    if dev == torch.cuda.current_device():
+        return False
+    if stream is not None:
+        raise ValueError(f"stream must be on cuda:{dev}")
+    return True
 
 
 def _raw_stream(stream, dev):
@@ -393,13 +439,14 @@ def tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype=torch.bfloat16):
     return int(lib().medusa_tree_attention_q8_workspace(B, N, Hq, Hkv, D, _DT[dtype]))
 
 
+@_in_stream
 def tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, mask, scale,
                       out=None, ws=None, stream=None):
     """Tree attention over the 8-bit paged cache: q [B,N,Hq,D] against the pages'
     prefix and the tree rows k_tree, v_tree [B,N,Hkv,D] under mask [N, ceil(N/64)].
     Returns out [B,N,Hq,D] in q's type.  N = 1 with mask [[1]] is plain decoding."""
     B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
-    if _elsewhere(dev):
+    if _elsewhere(dev, stream):
         with torch.cuda.device(dev):
             return tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, mask,
                                      scale, out, ws, stream)
@@ -424,13 +471,14 @@ def tree_attention_q8(q, k_tree, v_tree, k_pages, v_pages, k_scale, v_scale, pag
     return o
 
 
+@_in_stream
 def kv_append_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, rows=None, last=None,
                  best_node=None, hidden_rows=None, out=None, stream=None):
     """Quantises rows 0..last[b] of `rows` (tree nodes; None: rows in order) of
     k_rows, v_rows [B,T,Hkv,D] into the pages behind kv_len.  `last` None takes
     all.  Returns dict(kv_len, appended, h_next); the pools change in place."""
     B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
-    if _elsewhere(dev):
+    if _elsewhere(dev, stream):
         with torch.cuda.device(dev):
             return kv_append_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, rows, last,
                                 best_node, hidden_rows, out, stream)
@@ -476,13 +524,14 @@ def kv_pages_fork_workspace(B, n_pages):
     return int(lib().medusa_kv_pages_fork_workspace(B, n_pages))
 
 
+@_in_stream
 def kv_pages_fork(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, src=None, need=None, held=None,
                   out=None, ws=None, stream=None):
     """Forks, frees and reserves: row b goes on from row src[b] (-1: freed; None:
     every row from itself) with room for need[b] more tokens.  Returns
     dict(page_table, kv_len, refs, taken); open pages are copied in the pools."""
     B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
-    if _elsewhere(dev):
+    if _elsewhere(dev, stream):
         with torch.cuda.device(dev):
             return kv_pages_fork(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, src, need, held, out, ws, stream)
     if src is not None:
@@ -513,11 +562,12 @@ def kv_pages_compact_workspace(n_pages):
     return int(lib().medusa_kv_pages_compact_workspace(n_pages))
 
 
+@_in_stream
 def kv_pages_compact(k_pages, v_pages, k_scale, v_scale, page_table, held=None, out=None, ws=None, stream=None):
     """Moves the pages in use into [0, live).  Returns dict(page_table, new_page,
     live); the pools change in place."""
     B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table)
-    if _elsewhere(dev):
+    if _elsewhere(dev, stream):
         with torch.cuda.device(dev):
             return kv_pages_compact(k_pages, v_pages, k_scale, v_scale, page_table, held, out, ws, stream)
     if held is not None:
