@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     float* s_vmax = s_misc + 4;                                            // [2][4] largest V scale per quarter
     float* s_vref = s_misc + 12;                                           // [2] at the end of a segment
     float* s_qmax = s_misc + 16;                                           // [2][kUSoftmax / 32] per warp
+    uint32_t* s_hurt = reinterpret_cast<uint32_t*>(s_misc + 32);           // [2][2] rows of a stream that saw a bad V, one bit each
     const q8::Offsets first(base + L::kOffFirst, w.B);
     const long long lim = g_wait_limit;
 
@@ -542,6 +543,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
         mbar_init(checked0 + 8, 4);
         mbar_init_fence();
         s_fail[0] = s_fail[1] = 0;
+        for (int i = 0; i < 4; ++i) s_hurt[i] = 0;
         prefetch_tmap(&tmk);
         prefetch_tmap(&tmv);
         prefetch_tmap(&tmkt);
@@ -924,8 +926,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     const int m = (s.t0 + t - pt) * kTile + key;  // tree row
                     valid = m < w.N;
                     // A tree row whose V is not finite (or too large): 0 * inf of a query row that does not see
-                    // it would spoil that one, so its V counts as zero and rows that see it get
-                    // NaN.  Of two streams that share the tile stream 0 looks.
+                    // it would spoil that one, so its V counts as zero and rows that see it are
+                    // marked (s_hurt), which makes them NaN at the end.  Of two streams that share the tile stream 0 looks.
                     if (!SHARED || st == 0) {
                         const uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
 #pragma unroll 4
@@ -1051,7 +1053,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                                 top = max3(top, x0, x1);
                                 const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
                                 h[e] = pack_bf16x2(p0 * f, p1 * f);
-                                add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], bad_v && see0 ? NAN : p0, bad_v && see1 ? NAN : p1);
+                                add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], p0, p1);
                             }
                             if (wait_here && c0 == 0) wait_pv();
                             *reinterpret_cast<uint4*>(p_row + key * 128 + (((c0 >> 3) ^ (key & 7)) << 4)) =
@@ -1127,7 +1129,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
 #pragma unroll
                         for (int c = 0; c < CW; c += 4) {
                             const float4 r = *reinterpret_cast<const float4*>(corr_row + c);
-                            // (0, not l * 0: where p was infinite l is none)
+                            // (0, not l * 0: where p was infinite l is NaN)
                             l[c] = r.x == 0.f ? 0.f : l[c] * r.x;
                             l[c + 1] = r.y == 0.f ? 0.f : l[c + 1] * r.y;
                             l[c + 2] = r.z == 0.f ? 0.f : l[c + 2] * r.z;
@@ -1162,6 +1164,9 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
                     }
                     if (bad_v) {
+                        // (a mark of its own: sums may be dropped when references move later)
+                        atomicOr(s_hurt + 2 * st, (uint32_t)sees);
+                        if constexpr (NB > 32) atomicOr(s_hurt + 2 * st + 1, (uint32_t)(sees >> 32));
                         uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
 #pragma unroll 1
                         for (int c = 0; c < D / 8; ++c)
@@ -1249,6 +1254,9 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     c0 = wa * s_vref[0] / kPScale;
                     c1 = wb * s_vref[1] / kPScale;
                 }
+                const int hc = SHARED ? tid % NB : tid;
+                const uint32_t hurt = SHARED ? s_hurt[2 * (tid / NB) + (hc >> 5)] : s_hurt[hc >> 5] | s_hurt[2 + (hc >> 5)];
+                if (hurt >> (hc & 31) & 1) sum = NAN;
                 if (whole) {
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     c0 *= inv;
@@ -1260,6 +1268,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 if (!SHARED) s_corr[NB + tid] = c1;
             }
             bar_sync(3, kUSoftmax);
+            if (tid < 4) s_hurt[tid] = 0;
             // O^T: this thread's output column of the stream's own rows (shared) or of half
             // of the block's
             constexpr int COLS = SHARED ? NB : NB / 2;
