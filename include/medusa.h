@@ -362,9 +362,12 @@ int medusa_kv_compact(void* k_cache, void* v_cache, int32_t* kv_len, const int32
 /*   out            [B,N,Hq,D]   dtype, rounded once from float32              */
 /* Scores, softmax and sums are float32; codes, q and tree rows enter the      */
 /* products exactly (bf16 q to 2^-17 of the largest |q| of a block of 64 or    */
-/* 128 query rows), the weights of the sum over V with 9 bits down to 2^-17 of  */
-/* the largest and, for tree rows, as bf16 (dtype bf16), or in float32          */
-/* (dtype float32).                                                            */
+/* 128 query rows).  In the sum over V, dtype float32 takes the weights as they */
+/* are; dtype bf16 takes weight * V scale with 9 bits down to 2^-17 of the row's */
+/* largest such product (fewer down to 2^-26), the weights of tree rows as bf16. */
+/* A key with less than 2^-100 of that product may be left out of the row       */
+/* altogether (dtype bf16; its weight is then below 2^-36 of another's wherever */
+/* the V scales of a sequence and head differ by 2^64 at most).                 */
 /* kv_len is clamped to [0, M*P].  Keys of a page that is not in               */
 /* [0, n_pages) or whose scale is not readable count as absent.  A row that    */
 /* sees no key is zero.  A row that sees a tree row with a non-finite V (in    */

@@ -28,8 +28,6 @@ namespace {
 
 MEDUSA_WAIT_CONTROL()
 
-using q8::mul2;
-
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnQ8Args {
@@ -332,9 +330,9 @@ __global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const Attn
 //            two for the block (exact down to 2^-17 of its largest |q|), both added
 //            into S = K q; the page's scale multiplies S
 //   output   weight times V scale = p_1 + p_2 + p_3, three e5m2 planes side by side
-//            in one product: 9 bits, for weights down to 2^-17 of the largest, and
-//            fewer from there to 2^-26 (e5m2 has the range that a softmax needs: with
-//            an attention sink the weights that count can be 2^-12 of the largest)
+//            in one product: 9 bits, down to 2^-17 of the row's largest, and fewer from
+//            there to 2^-26 (e5m2 has the range that a softmax needs: with an
+//            attention sink the weights that count can be 2^-12 of the largest)
 // so no key or value is ever converted: converting them would cost more
 // instructions than the whole softmax of 64 rows, and twice the shared memory.
 //
@@ -343,9 +341,9 @@ __global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const Attn
 // owns one key: its scale is one register, the work is in proportion to the
 // query rows (from 16 on) rather than to the 128 rows of a matrix tile, and the
 // row sums are added up per thread and joined once per segment.  What crosses
-// threads is the rows' maximum, and that only when a score rises 2^4.9 above the
-// reference it is held against (the first tile and few others), which one
-// barrier vote per tile finds out.
+// threads is the rows' maximum, and that only when a weight times its V scale rises
+// 2^6.9 above the reference it is held against (the first tile and few others), which
+// one barrier vote per tile finds out.
 //
 // Two streams per CTA (four warps each, one per lane quarter), each with its own S and O in
 // TMEM, so that one stream's softmax runs while the other's products do:
@@ -381,12 +379,19 @@ constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
 // 102 us, one of 2048 keys 20 / 21 / 22 / 22 / 23 / 23 us; sixteen sequences of one token
 // 55 / 54 / 55 / 56 / 57 / 60 us.
 constexpr int kSetup = 9, kSetup16 = 5;
-// Planes hold weight * vs / v_ref * kPScale <= 2^15.9, below f16's largest 65504; weights
-// may exceed 1 by 2^kTau before the references move (126 us with 2^3, 112 with 2^4.9 for
-// eight ragged sequences of 64 rows).
-constexpr float kTau = 4.9f;
-constexpr float kPScale = 2048.f;
-constexpr float kVHead = 4.f;            // v_ref = kVHead * the largest V scale when set
+// What enters the sum over V is weight * V scale, w = 2^(x + log2 vs - m) with x the score
+// in log2 units and m the row's reference, the largest x + log2 vs when set.  So a page's
+// scale counts only as far as its weight does, row by row.  The planes hold w * 2^kLift,
+// which may grow to 2^15.9, below f16's largest 65504, before the references move; a tree
+// row's (vs = 1, bf16) to 2^27.9: 512 of them times 2^91 stay below 2^128 (too_large).
+// The row sums hold w / vs * 2^(kLift - kUnit), from 2^-112 for the largest scale to
+// 2^116 for the smallest and a w that is taken back.
+constexpr float kLift = 9.f, kUnit = 57.f;
+constexpr float kTopPage = 15.9f, kTopTree = 27.9f;
+// A reference that moves by more drops what was summed up before, the weights' sum as
+// well: keys whose w is below 2^-100 of a later one's.  (Their weight is below 2^-36 of its
+// weight where the scales of the two differ by 2^64 at most.)
+constexpr float kDrop = 100.f;
 constexpr long long kDrainCycles = kDefaultWaitCycles;
 
 template <int D, int NB, bool SHARED>
@@ -412,7 +417,7 @@ struct USmem {
     static constexpr int kOffRed = kOffCorr + 2 * NB * 4;      // float red[2][4][NB]
     static constexpr int kOffRow = kOffRed + 8 * NB * 4;       // int [2][kRowsBlock]: (node, head) of a row, in rows of D
     static constexpr int kOffMask = kOffRow + 2 * kRowsBlock * 4;      // uint32 [kRowsBlock][16]: mask rows
-    static constexpr int kOffInfo = kOffMask + kRowsBlock * 64;  // float2 (k, v scale)[kRing][8]
+    static constexpr int kOffInfo = kOffMask + kRowsBlock * 64;  // float2 (k scale, log2 of v scale)[kRing][8]
     static constexpr int kOffBad = kOffInfo + kRing * 8 * 8;   // uint32 [2][4]: keys of a tree tile with a non-finite V
     static constexpr int kOffMisc = kOffBad + 32;              // see below, 256 bytes
     static constexpr int kOffBar = kOffMisc + 256;
@@ -523,8 +528,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     float* s_misc = reinterpret_cast<float*>(base + L::kOffMisc);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_misc);
     volatile int* s_fail = reinterpret_cast<volatile int*>(s_misc + 2);    // [2] per stream
-    float* s_vmax = s_misc + 4;                                            // [2][4] largest V scale per quarter
-    float* s_vref = s_misc + 12;                                           // [2] at the end of a segment
     float* s_qmax = s_misc + 16;                                           // [2][kUSoftmax / 32] per warp
     uint32_t* s_hurt = reinterpret_cast<uint32_t*>(s_misc + 32);           // [2][2] rows of a stream that saw a bad V, one bit each
     const q8::Offsets first(base + L::kOffFirst, w.B);
@@ -728,7 +731,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 }
                 const unsigned m = __ballot_sync(0xffffffffu, there);
                 if (in)
-                    s_info[st * 8 + j] = there && q8::scale_ok(sc.x) && q8::scale_ok(sc.y) ? sc : make_float2(0.f, 0.f);
+                    s_info[st * 8 + j] = there && q8::scale_ok(sc.x) && q8::scale_ok(sc.y) ? make_float2(sc.x, log2f(sc.y))
+                                                                                            : make_float2(0.f, -INFINITY);
                 __syncwarp();
                 if (lane == 0) mbar_expect_tx(full0 + 8 * st, (uint32_t)(__popc(m) * a.P * D * 2));
             }
@@ -887,7 +891,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
             float l[CW];
 #pragma unroll
             for (int c = 0; c < CW; ++c) l[c] = 0.f;
-            float v_ref = 0.f;
             bool fail = false;
             const int pt = w.prefix_tiles(s.L);
             const int i_tree = min(steps, SHARED ? n_pre : (n_pre + 1 - st) >> 1);  // first step of the tree's
@@ -911,23 +914,24 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 const int sl = slot0 + t + (tree ? t - n_pre : 0);
                 const uint32_t tS = tmem + lane_off + (2 * st + (i & 1)) * NB;
                 bool ok = warp_wait(s_full0 + 8 * (2 * st + (i & 1)), (uint32_t)((n_buf[i & 1] + (i >> 1)) & 1), lim);
-                float kc = kq, vs = 1.f;
+                float kc = kq, lv = 0.f;  // lv: log2 of the V scale
                 bool valid, bad_v = false;
                 uint64_t sees = ~0ull;  // rows that see the key
                 if constexpr (!tree) {
                     const float2 sc = s_info[(sl % R) * 8 + (key >> page_shift)];
-                    valid = sc.y > 0.f && (s.t0 + t) * kTile + key < s.L;
+                    valid = sc.y > -INFINITY && (s.t0 + t) * kTile + key < s.L;
                     kc = kq * sc.x;
-                    vs = valid ? sc.y : 0.f;
+                    lv = valid ? sc.y : 0.f;
                     sees = valid ? sees : 0;
                 } else {
                     kc = scale;
                     ok = warp_wait(full0 + 8 * ((sl + 1) % R), (uint32_t)(((sl + 1) / R) & 1), lim) && ok;
                     const int m = (s.t0 + t - pt) * kTile + key;  // tree row
                     valid = m < w.N;
-                    // A tree row whose V is not finite (or too large): 0 * inf of a query row that does not see
-                    // it would spoil that one, so its V counts as zero and rows that see it are
-                    // marked (s_hurt), which makes them NaN at the end.  Of two streams that share the tile stream 0 looks.
+                    // A tree row whose V is not finite (or too large): 0 * inf of a query row that
+                    // does not see it would spoil that one, so its V counts as zero and rows that
+                    // see it are marked (s_hurt), which makes them NaN at the end.  Of two streams
+                    // that share the tile stream 0 looks.
                     if (!SHARED || st == 0) {
                         const uint8_t* v = base + L::kOffRing + ((sl + 1) % R) * L::kSlot + key * 128;
 #pragma unroll 4
@@ -951,34 +955,29 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     if (!valid) sees = 0;
                 }
                 fence_after_sync();
-                // Eight columns of scores from c0 on, in log2 units, less the rows'
-                // references or as they are.
-                auto scores8 = [&](int c0, bool relative, float* x) {
-                    float y[8];
-                    tmem_ld8(tS + c0, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4) {
-                        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (relative) m = *reinterpret_cast<const float4*>(m_row + c0 + e);
-                        fma2(x[e], x[e + 1], y[e], y[e + 1], kc, m.x, m.y);
-                        fma2(x[e + 2], x[e + 3], y[e + 2], y[e + 3], kc, m.z, m.w);
-                    }
-                };
-                const bool partial = tree || __any_sync(0xffffffffu, !valid);
-                // Scores less the references.  They are read from TMEM again wherever they are
-                // needed: held in between they would not fit next to the sums, and what the
-                // compiler then spills does not fit L1 next to this much shared memory.
+                const bool partial = !tree && __any_sync(0xffffffffu, !valid);
+                const float lift = lv + kLift;
+                const float unit = exp2_approx(-kUnit - lv);  // from w * 2^kLift to the row sums
+                // log2 of w * 2^kLift, n columns of scores from c0 on.  They are read from TMEM
+                // again wherever they are needed: held in between they would not fit next to the
+                // sums, and what the compiler then spills does not fit L1 next to this much shared
+                // memory.
                 auto relative = [&](int c0, auto& x, int n) {
 #pragma unroll
                     for (int e = 0; e < n; e += 4) {
                         const float4 m = *reinterpret_cast<const float4*>(m_row + c0 + e);
-                        fma2(x[e], x[e + 1], x[e], x[e + 1], kc, m.x, m.y);
-                        fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], kc, m.z, m.w);
+                        fma2(x[e], x[e + 1], x[e], x[e + 1], kc, lift, lift);
+                        fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], kc, lift, lift);
+                        add2(x[e], x[e + 1], m.x, m.y);
+                        add2(x[e + 2], x[e + 3], m.z, m.w);
                     }
                     if (partial) {
 #pragma unroll
                         for (int e = 0; e < n; ++e) x[e] = valid ? x[e] : -INFINITY;
+                    }
+                    if constexpr (tree) {
+#pragma unroll
+                        for (int e = 0; e < n; ++e) x[e] = (sees >> (c0 + e)) & 1 ? x[e] : -INFINITY;
                     }
                 };
                 // The stream's last PV, behind which P and O are free.  Shared blocks form the
@@ -996,7 +995,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 // them they are taken back and written again.
                 auto weights = [&](auto again) -> float {
                     constexpr bool wait_here = late && !decltype(again)::value;
-                    const float f = v_ref > 0.f ? vs * (kPScale / v_ref) : 0.f;
                     float top = -INFINITY;
                     if constexpr (!tree) {
                         // Sixteen columns at a time.  Shared blocks load the next ones ahead (409 us
@@ -1020,10 +1018,8 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                                 for (int k = 0; k < 2; ++k) {
                                     const int c = 4 * e + 2 * k;
                                     top = max3(top, y[c], y[c + 1]);
-                                    const float p0 = exp2_approx(y[c]), p1 = exp2_approx(y[c + 1]);
-                                    add2(l[c0 + c], l[c0 + c + 1], p0, p1);
-                                    float w0, w1;
-                                    mul2(w0, w1, p0, p1, f);
+                                    const float w0 = exp2_approx(y[c]), w1 = exp2_approx(y[c + 1]);
+                                    fma2(l[c0 + c], l[c0 + c + 1], w0, w1, unit, l[c0 + c], l[c0 + c + 1]);
                                     split_weights(w0, w1, two[k]);
                                 }
 #pragma unroll
@@ -1045,15 +1041,16 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         for (int c0 = 0; c0 < CW; c0 += 8) {
                             uint32_t h[4];
                             float x[8];
-                            scores8(c0, true, x);
+                            tmem_ld8(tS + c0, x);
+                            tmem_wait_ld();
+                            relative(c0, x, 8);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const bool see0 = (sees >> (c0 + 2 * e)) & 1, see1 = (sees >> (c0 + 2 * e + 1)) & 1;
-                                const float x0 = see0 ? x[2 * e] : -INFINITY, x1 = see1 ? x[2 * e + 1] : -INFINITY;
-                                top = max3(top, x0, x1);
-                                const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
-                                h[e] = pack_bf16x2(p0 * f, p1 * f);
-                                add2(l[c0 + 2 * e], l[c0 + 2 * e + 1], p0, p1);
+                                const int c = 2 * e;
+                                top = max3(top, x[c], x[c + 1]);
+                                const float w0 = exp2_approx(x[c]), w1 = exp2_approx(x[c + 1]);
+                                h[e] = pack_bf16x2(w0, w1);
+                                fma2(l[c0 + c], l[c0 + c + 1], w0, w1, unit, l[c0 + c], l[c0 + c + 1]);
                             }
                             if (wait_here && c0 == 0) wait_pv();
                             *reinterpret_cast<uint4*>(p_row + key * 128 + (((c0 >> 3) ^ (key & 7)) << 4)) =
@@ -1062,51 +1059,40 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     }
                     return top;
                 };
-                // A V scale above the reference would leave e5m2's range; bf16 (the tree, whose
-                // V has scale 1) has more, and moving the references for it took 17 us of 139.
-                const bool large = vs > (tree ? v_ref * 4096.f : v_ref);
                 bool move = i == 0;
                 for (;;) {
                     if (!move) {
                         const float top = weights(std::false_type{});
                         __syncwarp();
-                        if (!named_barrier_or(1 + st, kUStream, !ok || large || top > kTau)) break;
+                        if (!named_barrier_or(1 + st, kUStream, !ok || top > (tree ? kTopTree : kTopPage))) break;
                         // Taken back: l + p - p is off by half a unit of l + p at most, and p falls
-                        // to at most 1 on the new references, so the error is one rounding of the
-                        // row's sum.
-                        if constexpr (!tree) {
+                        // to the key's own share of the sum on the new references, so the error is
+                        // one rounding of the row's sum.
 #pragma unroll
-                            for (int c0 = 0; c0 < CW; c0 += 8) {
-                                float y[8];
-                                tmem_ld8(tS + c0, y);
-                                tmem_wait_ld();
-                                relative(c0, y, 8);
+                        for (int c0 = 0; c0 < CW; c0 += 8) {
+                            float y[8];
+                            tmem_ld8(tS + c0, y);
+                            tmem_wait_ld();
+                            relative(c0, y, 8);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) l[c0 + e] -= exp2_approx(y[e]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int c0 = 0; c0 < CW; c0 += 8) {
-                                float x[8];
-                                scores8(c0, true, x);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) l[c0 + e] -= (sees >> (c0 + e)) & 1 ? exp2_approx(x[e]) : 0.f;
-                            }
+                            for (int e = 0; e < 8; e += 2)
+                                fma2(l[c0 + e], l[c0 + e + 1], exp2_approx(y[e]), exp2_approx(y[e + 1]), -unit, l[c0 + e], l[c0 + e + 1]);
                         }
                     }
-                    // The references move: largest score per row over the tile's keys.
+                    // The references move: largest score and scale per row over the tile's keys.
 #pragma unroll 1
                     for (int c0 = 0; c0 < CW; c0 += 8) {
                         float y[8];
-                        scores8(c0, false, y);
+                        tmem_ld8(tS + c0, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) fma2(y[e], y[e + 1], y[e], y[e + 1], kc, lv, lv);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float m = redux_max_nan((sees >> (c0 + e)) & 1 ? y[e] : -INFINITY);
                             if (lane == e) s_red[(st * 4 + quarter) * NB + c0 + e] = m;
                         }
                     }
-                    const float vm = redux_max(vs);
-                    if (lane == 0) s_vmax[st * 4 + quarter] = vm;
                     bar_sync(1 + st, kUStream);
                     const bool fail = s_fail[st] != 0;
                     if (stid < NB) {
@@ -1114,15 +1100,10 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                         const float m0 = -m_row[stid];
                         // (a NaN score makes the reference, and with it the row, NaN)
                         const float m1 = max_nan(max_nan(max_nan(r[0], r[NB]), max_nan(r[2 * NB], r[3 * NB])), m0);
-                        // (what is 2^100 too small to count is dropped: no weight that a
-                        // factor above 0 belongs to was infinite)
-                        corr_row[stid] = m0 == -INFINITY || m0 - m1 < -100.f ? 0.f : exp2f(m0 - m1);
+                        // (no w that a factor above 0 belongs to was infinite)
+                        corr_row[stid] = m0 == -INFINITY || m0 - m1 < -kDrop ? 0.f : exp2f(m0 - m1);
                         m_row[stid] = -m1;
                     }
-                    float v1 = fmaxf(fmaxf(s_vmax[st * 4], s_vmax[st * 4 + 1]), fmaxf(s_vmax[st * 4 + 2], s_vmax[st * 4 + 3]));
-                    v1 = v1 > v_ref ? v1 * kVHead : v_ref;
-                    const float vf = v1 > 0.f ? v_ref / v1 : 0.f;
-                    v_ref = v1;
                     bar_sync(1 + st, kUStream);
                     if (fail) return false;
                     if (i > 0) {  // what was added up so far
@@ -1146,7 +1127,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                             for (int p = 0; p < OP; ++p) {
                                 uint32_t ow[8];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) ow[e] = __float_as_uint(o[p][e] * (corr_row[c + e] * vf));
+                                for (int e = 0; e < 8; ++e) ow[e] = __float_as_uint(o[p][e] * corr_row[c + e]);
                                 tmem_st8(tO + p * NB + c, ow);
                             }
                         }
@@ -1205,7 +1186,6 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     if (lane == c) s_red[(st * 4 + quarter) * NB + c] = v;
                 }
             }
-            if (stid == 0) s_vref[st] = v_ref;
             // the next segment's Q, asked for now; its products start while this one's
             // results go out
             q8::Segment next = s;
@@ -1239,20 +1219,21 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                     const float* r = s_red + x * 4 * NB + c;
                     return (r[0] + r[NB]) + (r[2 * NB] + r[3 * NB]);
                 };
+                constexpr float kToSums = 1.f / (1ull << (int)kUnit);  // from O to the units of the sums
                 float m, sum, c0, c1 = 0.f;
                 if (SHARED) {
                     const int x = tid / NB, c = tid % NB;
                     m = -s_m[x * NB + c];
                     sum = sum_of(x, c);
-                    c0 = s_vref[x] / kPScale;
+                    c0 = kToSums;
                 } else {
                     const float ma = -s_m[tid], mb = -s_m[NB + tid];
                     m = fmaxf(ma, mb);
                     const float ref = m == -INFINITY ? 0.f : m;
                     const float wa = exp2f(ma - ref), wb = exp2f(mb - ref);
                     sum = sum_of(0, tid) * wa + sum_of(1, tid) * wb;
-                    c0 = wa * s_vref[0] / kPScale;
-                    c1 = wb * s_vref[1] / kPScale;
+                    c0 = wa * kToSums;
+                    c1 = wb * kToSums;
                 }
                 const int hc = SHARED ? tid % NB : tid;
                 const uint32_t hurt = SHARED ? s_hurt[2 * (tid / NB) + (hc >> 5)] : s_hurt[hc >> 5] | s_hurt[2 + (hc >> 5)];
