@@ -75,6 +75,16 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     });
+    // The encoder is a driver call and needs a current context, which the runtime binds to a
+    // thread with its first call that works on the device.  A thread's first call of the
+    // library may come before any such call.
+    static thread_local bool bound = false;
+    if (!bound) {
+        unsigned long long id = 0;
+        int d = 0;
+        bound = current_context_id(&id) == MEDUSA_OK &&
+                (id || (cudaGetDevice(&d) == cudaSuccess && cudaSetDevice(d) == cudaSuccess));
+    }
     return fn;
 }
 
