@@ -105,7 +105,7 @@ struct SimpleSmem {
     static constexpr int kOffP = kOffQ + ROWS * kStride * 4;
     static constexpr int kOffStat = kOffP + ROWS * kStrideP * 4;  // corr, m, l
     static constexpr int kOffFirst = kOffStat + 3 * ROWS * 4;  // tile offsets
-    static int bytes(int B) { return kOffFirst + q8::offsets_bytes(B); }
+    static constexpr int bytes(int B) { return kOffFirst + q8::offsets_bytes(B); }
 };
 
 template <typename T, int D, int ROWS, int THREADS>
@@ -424,7 +424,7 @@ struct USmem {
     // full[R] empty[R] s_full[2][2] p_full[2] pv_done[2] qfull seen checked[2] drain[2]
     static constexpr int kNumBar = 2 * kRing + 14;
     static constexpr int kOffFirst = (kOffBar + kNumBar * 8 + 15) / 16 * 16;
-    static int bytes(int B) { return kOffFirst + q8::offsets_bytes(B) + 1024; }  // + alignment slack
+    static constexpr int bytes(int B) { return kOffFirst + q8::offsets_bytes(B) + 1024; }  // + alignment slack
 };
 
 __device__ __forceinline__ float redux_max_nan(float v) {  // NaN if any is
@@ -1429,11 +1429,20 @@ cudaError_t launch_merge(const AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     return launch(attn_q8_merge_kernel<T, D>, dim3(a.work.ctas, (most + rows - 1) / rows), dim3(kMergeThreads), 0, st, a, p.rows);
 }
 
+// The attribute is the kernel's, not the call's, so it is always what the largest batch
+// takes: a call of few sequences on another thread must not lower it under this one.
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, int most) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 template <typename T, int D, int ROWS, int THREADS>
 cudaError_t launch_simple(AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     auto kern = tree_attn_q8_simple_kernel<T, D, ROWS, THREADS>;
+    constexpr int most = SimpleSmem<D, ROWS>::bytes(q8::kMaxBatch);
+    static_assert(most + 1024 <= q8::kMaxSmem, "the largest batch does not fit (1024: static arrays)");
     const int smem = SimpleSmem<D, ROWS>::bytes(a.work.B);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(kern, most);
     if (e == cudaSuccess) e = launch(kern, dim3(a.work.ctas), dim3(THREADS), smem, st, a);
     if (e == cudaSuccess && !a.work.whole) e = launch_merge<T, D>(a, p, st);
     return e;
@@ -1472,8 +1481,10 @@ int rows_map(CUtensorMap* m, const void* rows, int D, int Hkv, int N, int B) {
 template <int D, int NB, bool SHARED>
 cudaError_t launch_umma(const CUtensorMap (&m)[4], AttnQ8Args& a, const Plan& p, cudaStream_t st) {
     auto kern = tree_attn_q8_umma_kernel<D, NB, SHARED>;
+    constexpr int most = USmem<D, NB, SHARED>::bytes(q8::kMaxBatch);
+    static_assert(most <= q8::kMaxSmem, "the largest batch does not fit");
     const int smem = USmem<D, NB, SHARED>::bytes(a.work.B);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(kern, most);
     if (e == cudaSuccess) e = launch(kern, dim3(a.work.ctas), dim3(kUThreads), smem, st, m[0], m[1], m[2], m[3], a);
     if (e == cudaSuccess && !a.work.whole) e = launch_merge<uint16_t, D>(a, p, st);
     return e;

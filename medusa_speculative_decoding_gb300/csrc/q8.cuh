@@ -93,7 +93,8 @@ struct Work {
 
 // Two tables in shared memory: first[b] (b <= B), where the units of sequence b begin, and rest[b], the length of b less the whole tiles before its last one.
 // (Tiles are counted in 32 bits: the entry point bounds their number.)
-__host__ __device__ __forceinline__ int offsets_bytes(int B) { return (B + 1) * 4 + (B + 3) / 4 * 4; }
+constexpr int kMaxSmem = 232448;  // shared memory of a CTA on sm_103
+__host__ __device__ constexpr int offsets_bytes(int B) { return (B + 1) * 4 + (B + 3) / 4 * 4; }
 struct Offsets {
     uint32_t* first;
     uint8_t* rest;
