@@ -403,7 +403,7 @@ int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tr
 /* The pages that receive rows must be in the table and belong to one          */
 /* sequence only (6c sees to both).  A sequence whose last, rows, best_node,    */
 /* kv_len or pages are out of range is left unchanged: kv_len_out = kv_len,    */
-/* appended = -2.  Limits: R <= T where rows is NULL.                          */
+/* appended = -2, h_next[b] zero.  Limits: R <= T where rows is NULL.          */
 int medusa_kv_append_q8(const void* k_rows, const void* v_rows, medusa_dtype dtype, void* k_pages,
                         void* v_pages, float* k_scale, float* v_scale, const int32_t* page_table,
                         const int32_t* kv_len, const int32_t* rows, const int32_t* last, int B, int T,

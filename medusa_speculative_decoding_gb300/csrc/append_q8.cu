@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_q8_kernel(cons
             a.kv_len_out[b] = ok ? L + n : L;
             if (a.appended) a.appended[b] = ok ? n : -2;
         }
-        if (ok && a.hidden) {
-            const uint4* src = a.hidden + ((size_t)b * a.T + a.best_node[b]) * a.h16;
-            for (int i = tid; i < a.h16; i += THREADS) a.h_next[(size_t)b * a.h16 + i] = src[i];
+        if (a.hidden) {  // zero where the sequence is rejected: never what memory held before
+            const uint4* src = a.hidden + ((size_t)b * a.T + (ok ? a.best_node[b] : 0)) * a.h16;
+            for (int i = tid; i < a.h16; i += THREADS)
+                a.h_next[(size_t)b * a.h16 + i] = ok ? src[i] : make_uint4(0, 0, 0, 0);
         }
         return;
     }
