@@ -392,8 +392,8 @@ int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tr
 /*   k_rows, v_rows [B,T,Hkv,D] dtype; rows [B,R] int32; last [B] int32        */
 /*   best_node [B], hidden_rows [B,T,H] dtype, h_next [B,H] dtype: all or none; */
 /*             h_next[b] = hidden_rows[b, best_node[b]]                        */
-/*   kv_len_out [B] (not kv_len itself); appended [B] out, may be NULL: rows   */
-/*             written                                                         */
+/*   kv_len_out [B]; appended [B] out, may be NULL: rows written; neither may  */
+/*             be an array that is read                                        */
 /* The scale of a page and head is the smallest power of two 2^e (-64 <= e <=  */
 /* 64) with |x| <= 448 * 2^e for the finite values written there; rows append  */
 /* under the page's present scale while they fit it, and otherwise raise it:   */

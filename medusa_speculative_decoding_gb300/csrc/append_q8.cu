@@ -297,8 +297,11 @@ extern "C" int medusa_kv_append_q8(const void* k_rows, const void* v_rows, medus
     if (!aligned16(k_rows) || !aligned16(v_rows) || !aligned16(k_pages) || !aligned16(v_pages) ||
         (hid && (!aligned16(hidden_rows) || !aligned16(h_next))))
         return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: rows, pages and hidden states must be 16-byte aligned");
-    if (kv_len_out == kv_len)
-        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: kv_len_out must not be kv_len");
+    for (const int32_t* read : {kv_len, last, best_node, rows, page_table})
+        if (read && (read == kv_len_out || read == appended))
+            return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: kv_len_out and appended must not be what is read");
+    if (appended == kv_len_out)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: kv_len_out and appended must differ");
     const int windows = (R + P - 2) / P + 1;  // pages that R rows can touch
     if (windows > 65535) return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_q8: %d rows span too many pages", R);
     AppendArgs a{};

@@ -1,0 +1,18 @@
+"""More arguments that the 8-bit paged cache's entry points refuse: checked on the host,
+with nothing enqueued.  No test here launches a kernel."""
+import ctypes as C
+
+import pytest
+
+from test_q8_refusals import M, X, Y, append  # noqa: F401  (M: fixture)
+
+Z, V = C.c_void_p(12288), C.c_void_p(16384)
+
+
+@pytest.mark.parametrize("args", [
+    dict(last=Y, out=Y), dict(best=Y, hidden=X, h_next=Z, H=64, out=Y), dict(appended=X), dict(appended=Z, last=Z),
+    dict(appended=Z, best=Z, hidden=X, h_next=V, H=64), dict(appended=Y), dict(out=Y, rows=Y), dict(appended=Z, rows=Z),
+    dict(out=Y, table=Y), dict(appended=Z, table=Z)], ids=str)
+def test_append_outputs_are_none_of_what_it_reads(M, args):  # noqa: F811
+    """Every block reads lengths, rows and pages while one writes the new lengths."""
+    assert append(M, **args) == -1
