@@ -302,7 +302,7 @@ extern "C" int medusa_kv_append_q8(const void* k_rows, const void* v_rows, medus
             return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: kv_len_out and appended must not be what is read");
     if (appended == kv_len_out)
         return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_q8: kv_len_out and appended must differ");
-    const int windows = (R + P - 2) / P + 1;  // pages that R rows can touch
+    const int windows = (int)(((long long)R + P - 2) / P + 1);  // pages that R rows can touch
     if (windows > 65535) return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_q8: %d rows span too many pages", R);
     AppendArgs a{};
     a.rows[0] = k_rows; a.rows[1] = v_rows;

@@ -16,3 +16,9 @@ Z, V = C.c_void_p(12288), C.c_void_p(16384)
 def test_append_outputs_are_none_of_what_it_reads(M, args):  # noqa: F811
     """Every block reads lengths, rows and pages while one writes the new lengths."""
     assert append(M, **args) == -1
+
+
+@pytest.mark.parametrize("R", [2 ** 31 - 1, 2 ** 31 - 65])
+def test_append_of_too_many_rows(M, R):  # noqa: F811
+    """The number of pages that R rows span is counted in 64 bits."""
+    assert append(M, R=R) == -2
