@@ -373,7 +373,8 @@ int medusa_kv_compact(void* k_cache, void* v_cache, int32_t* kv_len, const int32
 /* sees no key is zero.  A row that sees a tree row with a non-finite V (in    */
 /* bf16: or one of 2^91 and more, whose sums could overflow) is NaN; rows that */
 /* do not see it are not affected.                                             */
-/* Limits: N <= 512, Hq % Hkv == 0, N * (Hq/Hkv) <= 4096; scale > 0, finite.   */
+/* Limits: N <= 512, Hq % Hkv == 0, N * (Hq/Hkv) <= 4096; scale > 0 and         */
+/* scale * log2(e) finite; scores within float32's range.                       */
 size_t medusa_tree_attention_q8_workspace(int B, int N, int Hq, int Hkv, int D, medusa_dtype dtype);
 int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype,
                              const void* k_pages, const void* v_pages, const float* k_scale,

@@ -1514,8 +1514,8 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_pages) || !aligned16(v_pages) ||
         !aligned16(out))
         return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: q, tree rows, pages and out must be 16-byte aligned");
-    if (!(scale > 0.f) || scale > 3.0e38f)
-        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: scale must be positive and finite");
+    if (!(scale > 0.f) || !(scale * kLog2e <= FLT_MAX))
+        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: scale must be positive, scale * log2(e) finite");
     const Plan p = plan_q8(dtype, N, Hq / Hkv, D);
     const size_t need = ws_bytes_q8(p, D);
     if (!ws || ws_bytes < need)
