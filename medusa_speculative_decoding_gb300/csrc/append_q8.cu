@@ -95,6 +95,32 @@ __device__ __forceinline__ float page_scale(float top) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// q is a quotient or product rounded to float32, r what the exact one lies above it: the
+// exact one's neighbour with an odd last bit (or itself).  The middle of two codes ends in
+// zeros, so rounding the result to a code is rounding the exact value.
+__device__ __forceinline__ float to_odd(float q, float r) {
+    uint32_t u = __float_as_uint(q);
+    if (r != 0.f) {
+        if ((r < 0.f) != (q < 0.f)) u -= 1;  // towards zero first
+        u |= 1;
+    }
+    return __uint_as_float(u);
+}
+__device__ __forceinline__ float divide_to_odd(float x, float s) {
+    const float q = x / s;
+    // (below, the code is zero whatever the bits; above, it is held at 448)
+    return fabsf(q) > 0x1p-12f && fabsf(q) < 1024.f ? to_odd(q, fmaf(-q, s, x)) : q;
+}
+__device__ __forceinline__ float multiply_to_odd(float x, float s) {
+    const float p = x * s;
+    return to_odd(p, fmaf(x, s, -p));
+}
+// top <= 448 * s, of the exact product
+__device__ __forceinline__ bool fits(float top, float s) {
+    const float p = q8::kE4m3Max * s;
+    return top < p || (top == p && fmaf(q8::kE4m3Max, s, -p) >= 0.f);
+}
+
 // THREADS * CHUNKS pieces of eight elements make a page of one head.
 template <typename T, int D, int THREADS, int CHUNKS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_q8_kernel(const AppendArgs a) {
@@ -202,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_q8_kernel(cons
         for (int i = 0; i < THREADS / 32; ++i) top = fmaxf(top, s_top[id & 1][i]);
 
         const bool readable = !had || q8::scale_ok(s0);  // an unreadable page stays one
-        const bool keep = had && (!readable || top <= q8::kE4m3Max * s0);
+        const bool keep = had && (!readable || fits(top, s0));
         const float s1 = keep ? s0 : page_scale(top);
         if (tid == 0 && !keep) a.scale[kv][unit] = s1;
         if (readable) {
@@ -223,8 +249,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_q8_kernel(cons
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 f = q8::e4m3x2_to_float2(old[e]);
-                        y[2 * e] = f.x * s0;
-                        y[2 * e + 1] = f.y * s0;
+                        y[2 * e] = multiply_to_odd(f.x, s0);
+                        y[2 * e + 1] = multiply_to_odd(f.y, s0);
                     }
                 } else {
                     x[k].unpack(y);
@@ -238,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_q8_kernel(cons
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) q[e] = q8::float2_to_e4m3x2(y[2 * e] / s1, y[2 * e + 1] / s1);
+                    for (int e = 0; e < 4; ++e) q[e] = q8::float2_to_e4m3x2(divide_to_odd(y[2 * e], s1), divide_to_odd(y[2 * e + 1], s1));
                 }
                 *dst = make_uint2((uint32_t)q[0] | (uint32_t)q[1] << 16, (uint32_t)q[2] | (uint32_t)q[3] << 16);
             }
