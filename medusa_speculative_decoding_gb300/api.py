@@ -385,7 +385,10 @@ def _need_shape(t, name, shape, dtype, dev):
     raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len=None):
+_NO_LENGTHS = object()  # the call takes none
+
+
+def _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len=_NO_LENGTHS):
     _need(k_pages, "k_pages")
     if k_pages.dtype not in _CODES or k_pages.dim() != 4:
         raise ValueError("k_pages must be [n_pages, Hkv, P, D] e4m3 codes (uint8 or float8_e4m3fn)")
@@ -396,7 +399,7 @@ def _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len=None):
     if page_table is None or page_table.dim() != 2:
         raise ValueError("page_table must be [B, M]")
     _need_shape(page_table, "page_table", page_table.shape, _I32, dev)
-    if kv_len is not None:
+    if kv_len is not _NO_LENGTHS:
         _need_shape(kv_len, "kv_len", page_table.shape[:1], _I32, dev)
     return (*page_table.shape, *shape, dev)
 
