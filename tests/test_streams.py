@@ -168,3 +168,31 @@ def test_pages(medusa):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_a_side_stream_inside_a_capture(medusa):
+    """A graph whose calls work on two streams, workspaces and outputs from its own memory."""
+    cases = [attention_case(180, 2, 64, 4, 4, 128, 64, [900, 400], "bf16"), attention_case(181, 3, 9, 4, 2, 64, 16, [300, 1, 70], "f32")]
+    t = [[dev(c[n], c["dtype"]) for n in ("q", "k_tree", "v_tree")] + [to_dev(c[n]) for n in NAMES + ("table", "kv_len", "mask")] for c in cases]
+    want = [medusa.tree_attention_q8(*x, c["scale"]) for x, c in zip(t, cases)]
+    forked = medusa.kv_pages_fork(*t[0][3:9])
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = [medusa.tree_attention_q8(*t[0], cases[0]["scale"]), medusa.tree_attention_q8(*t[1], cases[1]["scale"], stream=side)]
+        again = medusa.kv_pages_fork(*t[0][3:9], stream=side)
+        got.append(medusa.tree_attention_q8(*t[0], cases[0]["scale"], stream=side))
+        main.wait_stream(side)
+    for _ in range(5):
+        for x in got:
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for x, w in zip(got, (*want, want[0])):
+            assert torch.equal(x, w)
+        for k in forked:
+            assert torch.equal(again[k], forked[k])
+    medusa.device_status()
