@@ -45,8 +45,6 @@ struct AttnQ8Args {
     float scale_log2;
 };
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) {
     uint16_t r;
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
@@ -108,7 +106,7 @@ struct SimpleSmem {
     static constexpr int bytes(int B) { return kOffFirst + q8::offsets_bytes(B); }
 };
 
-template <typename T, int D, int ROWS, int THREADS>
+template <int D, int ROWS, int THREADS>
 __global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const AttnQ8Args a) {
     using L = SimpleSmem<D, ROWS>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -141,8 +139,7 @@ __global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const Attn
             const int r = row0 + i / D;
             float v = 0.f;
             if (i / D < nrows)
-                v = load1(static_cast<const T*>(a.q) +
-                          (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + i % D);
+                v = static_cast<const float*>(a.q)[(((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + i % D];
             sq[i / D * L::kStride + i % D] = v;
         }
         if (tid < ROWS) { s_m[tid] = -INFINITY; s_l[tid] = 0.f; }
@@ -169,8 +166,8 @@ __global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const Attn
                     const size_t o = (((size_t)s.b * w.N + k0 + key) * a.Hkv + hk) * D + c;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        kx[e] = load1(static_cast<const T*>(a.k_tree) + o + e);
-                        vx[e] = load1(static_cast<const T*>(a.v_tree) + o + e);
+                        kx[e] = static_cast<const float*>(a.k_tree)[o + e];
+                        vx[e] = static_cast<const float*>(a.v_tree)[o + e];
                         // 0 * inf of a masked row would spoil rows that do not see it
                         if (!isfinite(vx[e])) { vx[e] = 0.f; s_bad[key] = 1; }
                     }
@@ -304,10 +301,10 @@ __global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const Attn
             const int r = row0 + r0 + i;
             const float l = s_l[r0 + i];
             if (whole && r0 + i >= nrows) continue;
-            T* out = static_cast<T*>(a.out) + (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D;
+            float* out = static_cast<float*>(a.out) + (((size_t)s.b * w.N + r / a.G) * a.Hq + hk * a.G + r % a.G) * D;
 #pragma unroll
             for (int j = 0; j < CP; ++j) {
-                if (whole) store1(out + column(j), l == 0.f ? 0.f : acc[i][j] / l);
+                if (whole) out[column(j)] = l == 0.f ? 0.f : acc[i][j] / l;
                 else a.part_o[(part + r0 + i) * D + column(j)] = acc[i][j];
             }
         }
@@ -1436,15 +1433,15 @@ cudaError_t allow_smem(Kern kern, int most) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
-template <typename T, int D, int ROWS, int THREADS>
+template <int D, int ROWS, int THREADS>
 cudaError_t launch_simple(AttnQ8Args& a, const Plan& p, cudaStream_t st) {
-    auto kern = tree_attn_q8_simple_kernel<T, D, ROWS, THREADS>;
+    auto kern = tree_attn_q8_simple_kernel<D, ROWS, THREADS>;
     constexpr int most = SimpleSmem<D, ROWS>::bytes(q8::kMaxBatch);
     static_assert(most + 1024 <= q8::kMaxSmem, "the largest batch does not fit (1024: static arrays)");
     const int smem = SimpleSmem<D, ROWS>::bytes(a.work.B);
     cudaError_t e = allow_smem(kern, most);
     if (e == cudaSuccess) e = launch(kern, dim3(a.work.ctas), dim3(THREADS), smem, st, a);
-    if (e == cudaSuccess && !a.work.whole) e = launch_merge<T, D>(a, p, st);
+    if (e == cudaSuccess && !a.work.whole) e = launch_merge<float, D>(a, p, st);
     return e;
 }
 
@@ -1542,8 +1539,8 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     cudaStream_t st = as_stream(stream);
     cudaError_t e;
     if (dtype == MEDUSA_F32) {
-        e = p.rows == 16 ? (D == 64 ? launch_simple<float, 64, 16, 256>(a, p, st) : launch_simple<float, 128, 16, 256>(a, p, st))
-                         : (D == 64 ? launch_simple<float, 64, 64, 256>(a, p, st) : launch_simple<float, 128, 64, 512>(a, p, st));
+        e = p.rows == 16 ? (D == 64 ? launch_simple<64, 16, 256>(a, p, st) : launch_simple<128, 16, 256>(a, p, st))
+                         : (D == 64 ? launch_simple<64, 64, 256>(a, p, st) : launch_simple<128, 64, 512>(a, p, st));
     } else {
         CUtensorMap m[4];
         const long long rows = (long long)n_pages * Hkv * P;
