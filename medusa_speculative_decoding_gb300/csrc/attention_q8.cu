@@ -87,11 +87,13 @@ __device__ __forceinline__ void plan_share(const AttnQ8Args& a, const q8::Offset
 // ROWS query rows, 16 or 64.  Each tile of kKeys keys is dequantised into shared
 // memory once for all rows; scores, softmax and sums are float32.  A thread has four
 // rows and KT keys (then CP columns) of each product.  Small calls are bound by
-// latency: 13 us with the merge for nine rows, four heads of 64 and 128 keys.  Large
+// latency: 14 us with the merge for nine rows, four heads of 64 and 128 keys.  Large
 // ones by issue and shared memory: with blocks of 16 rows, whose every key is
 // dequantised anew, 147 us for three sequences of 2730 keys, 8 heads of 64 and 64 rows, with
-// 64 rows 68 (85 with 512 threads); at D = 128, 2000 keys and two sequences 83 and 69 (78
-// with 256 threads, of which an SM holds one block).
+// 64 rows 67 (85 with 512 threads); at D = 128, 2000 keys and two sequences 83 and 69 (78
+// with 256 threads, of which an SM holds one block).  One token goes through a block
+// of 16 rows, most of them zero: 509 us for sixteen sequences of 777 to 16384 keys, 8 heads
+// of 4 rows, where reading the codes takes 42.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64;
 
@@ -359,12 +361,13 @@ __global__ void __launch_bounds__(THREADS) tree_attn_q8_simple_kernel(const Attn
 // kind::f16 with q and P in bf16, added to the same sums.
 // Every wait is bounded; a CTA that gives up marks its results NaN.
 //
-// Measured, merge included: 99 us for eight sequences of 1024 to 4096 keys, 40 heads, 64
-// rows (231 MB, 2.3 TB/s); 385 us for four of 8192 keys, 32 heads, 341 rows (191 GFLOP, 495
-// TFLOP/s); 54 us for sixteen of 777 to 16384 keys, 8 heads of 4 rows (282 MB, 5.2 TB/s); 22
-// us for one of 2048 keys, 32 heads, 64 rows.  With 64 rows and more what bounds it is the
-// issue of the softmax warps: 13.5 cycles per 32 weights and scheduler for weights and
-// planes alone, 9 of them without the planes; with 16 rows, the tiles under way.
+// Measured, merge included: 96 us for eight sequences of 1024 to 4096 keys, 40 heads, 64
+// rows (231 MB, 2.4 TB/s); 386 us for four of 8192 keys, 32 heads, 341 rows (191 GFLOP, 494
+// TFLOP/s); 50 us for sixteen of 777 to 16384 keys, 8 heads of 4 rows (282 MB, 5.6 TB/s); 22
+// us for one of 2048 keys, 32 heads, 64 rows.  With 64 rows and more no unit is near full
+// (341 rows: issue slots 44%, tensor pipe 31%, DRAM 30%; eight sequences: 33, 16 and 29%): a
+// scheduler has two softmax warps, and both wait in turn for a tile's vote, the stream's
+// last PV and the scores' way out of TMEM.  With 16 rows it is the tiles under way.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;  // keys per tile
 constexpr int kUSoftmax = 256, kUThreads = kUSoftmax + 96;
@@ -372,9 +375,10 @@ constexpr int kUMmaWarp = kUSoftmax / 32, kUTmaWarp = kUMmaWarp + 2;  // an MMA 
 constexpr int kUStream = kUSoftmax / 2;  // threads of a stream
 // Tiles that a unit counts more (q8.cuh, Work): first references, tree tile and results
 // cost as much as several tiles, and more where they are of more rows.  Measured with
-// 3 / 5 / 7 / 9 / 12 / 16: eight ragged sequences of 64 rows 108 / 105 / 102 / 99 / 99 /
-// 102 us, one of 2048 keys 20 / 21 / 22 / 22 / 23 / 23 us; sixteen sequences of one token
-// 55 / 54 / 55 / 56 / 57 / 60 us.
+// 3 / 5 / 7 / 9 / 12 / 16: eight ragged sequences of 64 rows 103 / 100 / 97 / 96 / 97 / 97
+// us, four of 341 rows 392 / 390 / 388 / 386 / 386 / 386 us, one of 2048 keys 20 / 20 / 22 /
+// 22 / 22 / 22 us (the price of 9 where there are few units a CTA); sixteen sequences of
+// one token 51 / 50 / 51 / 52 / 53 / 55 us.
 constexpr int kSetup = 9, kSetup16 = 5;
 // What enters the sum over V is weight * V scale, w = 2^(x + log2 vs - m) with x the score
 // in log2 units and m the row's reference, the largest x + log2 vs when set.  So a page's

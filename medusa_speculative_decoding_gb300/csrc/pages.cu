@@ -20,7 +20,7 @@
 // The planning kernels are bound by the latency of six dependent steps (14 us for 64
 // rows of 8192 tokens in pages of 16, 16 us to compact a pool of 8192 pages); a cluster
 // barrier costs less than a launch between two of them would.  The move is bound by
-// HBM: 2048 pages of 128 KB in 82 us, 6.5 TB/s read and written.
+// HBM: 2048 pages of 128 KB in 82 to 86 us, 6.2 to 6.5 TB/s read and written.
 #include "common.cuh"
 #include "q8.cuh"
 #include "umma.cuh"
