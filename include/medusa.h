@@ -312,6 +312,32 @@ int medusa_verify_accept_chain(const float* p, const float* q, const int32_t* dr
                                int32_t* out_tok, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* 4d. Tree acceptance by drawn tokens  [SD, "Faster without changing the       */
+/*     result"; MH, "Tree attention and acceptance"]                           */
+/*                                                                           */
+/* The candidates are fixed, so that the speculative rule is: draw a token     */
+/* from the target's row at the node, go on to the child that holds it (the    */
+/* lowest one), and end with the token itself where no child does.  Every token */
+/* of the round then follows the target's distribution.  The draw at depth d    */
+/* from row p with the caller's random number u = u[b,d] is the smallest v with   */
+/*   p_0 + ... + p_v > u * (p_0 + ... + p_{V-1})                                */
+/* (rows need not be normalised; entries below 0 and NaN count as 0, above 1 as 1; */
+/* sums are 64 bits wide, off by some 2^-40 of a row's total at most).  u in [0,1):   */
+/* below it counts as 0; 1 and above give the last token that has any weight.       */
+/*   probs [B,N,V] float: row u scores the token after node u; cand [B,N];          */
+/*   parent, depth [N] from the layout; u [B,Dmax+1] float                         */
+/* accept_len, best_node, path_nodes, next_tok as in 4a (next_tok: the drawn token    */
+/* that ended the walk; -1: a row without any weight).  A node whose parent is not     */
+/* below it is never reached.                                                        */
+/* Limits: N <= 512, Dmax < 512, B <= 65535, V <= 2^24.                                */
+/* ------------------------------------------------------------------------- */
+size_t medusa_verify_draw_workspace(int B, int N, int V);
+int medusa_verify_accept_tree_draw(const float* probs, const int32_t* cand, const int32_t* parent,
+                                   const int32_t* depth, const float* u, int B, int N, int V, int Dmax,
+                                   int32_t* accept_len, int32_t* best_node, int32_t* path_nodes,
+                                   int32_t* next_tok, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* 5. KV compaction  [MH, "Tree attention and acceptance": keep the longest   */
 /*    accepted branch; its last hidden state feeds the heads next round]      */
 /*                                                                           */
@@ -450,6 +476,70 @@ int medusa_kv_pages_compact(void* k_pages, void* v_pages, float* k_scale, float*
                             const int32_t* page_table, const int32_t* held, int B, int Hkv, int D, int P,
                             int n_pages, int M, int32_t* page_table_out, int32_t* new_page, int32_t* live,
                             void* ws, size_t ws_bytes, void* stream);
+
+/* 6e. Rotary positions of new rows  [MH, "Tree attention and acceptance": all    */
+/* candidates are appended at once; those of one depth stand at one position].  */
+/* Row i of sequence b stands at position kv_len[b] + depth[i] (kv_len[b] + i   */
+/* where depth is NULL).  The first 2 n_freq values of a head are pairs (i,      */
+/* n_freq + i), or (2i, 2i + 1) where interleaved != 0; pair i turns by position */
+/* * inv_freq[i]: (x, y) -> (x cos - y sin, y cos + x sin), in float32, rounded  */
+/* once; the other values are copied.  Angles are exact to 2^-30 for positions   */
+/* up to 2^20 and any frequency below 2 pi; positions count modulo 2^32.         */
+/*   q, q_out [B,T,Hq,D], k, k_out [B,T,Hkv,D] dtype; k and k_out may both be     */
+/*   NULL with Hkv = 0; q_out may be q and k_out may be k                        */
+/*   kv_len [B] int32; depth [T] int32 or NULL; inv_freq [n_freq] float, finite   */
+/* Limits: D % 16 == 0, D <= 512; n_freq % 8 == 0, 8 <= n_freq <= D / 2; at most  */
+/* 1024 heads of each kind.                                                     */
+int medusa_rope_rows(const void* q, const void* k, medusa_dtype dtype, const int32_t* kv_len,
+                     const int32_t* depth, const float* inv_freq, int B, int T, int Hq, int Hkv, int D,
+                     int n_freq, int interleaved, void* q_out, void* k_out, void* stream);
+
+/* 6f. Append rows, rotated on the way.  As 6b for K and V rows of which K is not  */
+/* rotated yet: row i turns by position kv_len[b] + i, the slot it goes to, as in  */
+/* 6e, and is rounded once, to its code.  The scale of a K page is the smallest    */
+/* power of two 2^e with |x| <= 316 * 2^e for the finite values written there,     */
+/* before they are rotated (a rotated value is at most sqrt(2) larger: 446.9), so   */
+/* that it does not depend on positions; V's and all else is as in 6b.  A pair      */
+/* with an infinity becomes what float32 makes of it: +-448 or NaN.               */
+/*   q, q_out [B,T,Hq,D] dtype, or both NULL with Hq = 0: the queries of the same   */
+/*   rows, rotated (rows must then be NULL and R = T); rows behind last[b] are      */
+/*   zero.  q_out may be q.  Queries are rotated whether or not the append is        */
+/*   refused on the device.                                                         */
+/* Limits: as 6b; n_freq as 6e; Hq <= 1024.                                         */
+int medusa_kv_append_rope_q8(const void* k_rows, const void* v_rows, medusa_dtype dtype, void* k_pages,
+                             void* v_pages, float* k_scale, float* v_scale, const int32_t* page_table,
+                             const int32_t* kv_len, const int32_t* rows, const int32_t* last,
+                             const float* inv_freq, int n_freq, int interleaved, const void* q, void* q_out,
+                             int B, int T, int R, int Hq, int Hkv, int D, int P, int n_pages, int M,
+                             const int32_t* best_node, const void* hidden_rows, void* h_next, int H,
+                             int32_t* kv_len_out, int32_t* appended, void* stream);
+
+/* 6g. Attention of a chunk of new tokens over the paged cache: a prompt, a later   */
+/* piece of one, or one decoded token (T = 1).  The rows 0..last[b] of q (all T      */
+/* where last is NULL) are those of the last n = last[b] + 1 slots that sequence b    */
+/* holds; their keys and values are in the pages (6b, 6f).  Row i sees the slots      */
+/* [0, kv_len[b] - n + i]:  out = softmax(scale * q.k) v.                            */
+/*   q [B,T,Hq,D] dtype; kv_len [B] with the chunk; last [B] int32 or NULL            */
+/*   out [B,T,Hq,D] dtype, rounded once from float32; not q.  Rows behind last[b] and  */
+/*   rows that see no key are zero.                                                  */
+/* Scores, softmax and sums are float32; codes enter the products exactly; bf16 q is    */
+/* exact down to 2^-13 of its row's largest |q|, 2^-21 of that below.  In the sum over   */
+/* V, dtype float32 takes the weights as they are, dtype bf16 takes weight * V scale      */
+/* rounded to 11 bits down to 2^-22 of the row's largest such product (fewer down to       */
+/* 2^-32).  A key with less than 2^-100 of that product may be left out of the row          */
+/* altogether (dtype bf16, as in 6a).                                                     */
+/* kv_len is clamped to [0, M*P], last to [-1, T-1].  Keys of a page that is not in         */
+/* [0, n_pages) or whose scale is not readable count as absent.  A row is NaN where its      */
+/* query is not finite or a key that it sees has a NaN code; what other rows see and what     */
+/* slots behind kv_len hold does not matter.                                                */
+/* Limits: Hq % Hkv == 0, Hq / Hkv <= 64, T <= 2^20; scale > 0 and scale * log2(e) finite;    */
+/* scores within float32's range.                                                           */
+size_t medusa_chunk_attention_q8_workspace(int B, int T, int Hq, int Hkv, int D, medusa_dtype dtype);
+int medusa_chunk_attention_q8(const void* q, medusa_dtype dtype, const void* k_pages, const void* v_pages,
+                              const float* k_scale, const float* v_scale, const int32_t* page_table,
+                              const int32_t* kv_len, const int32_t* last, int B, int T, int Hq, int Hkv,
+                              int D, int P, int n_pages, int M, float scale, void* out, void* ws,
+                              size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -29,6 +29,9 @@ EXPORTS = (
     "medusa_tree_attention_q8_workspace", "medusa_tree_attention_q8", "medusa_kv_append_q8",
     "medusa_kv_pages_fork_workspace", "medusa_kv_pages_fork",
     "medusa_kv_pages_compact_workspace", "medusa_kv_pages_compact",
+    "medusa_rope_rows", "medusa_kv_append_rope_q8",
+    "medusa_chunk_attention_q8_workspace", "medusa_chunk_attention_q8",
+    "medusa_verify_draw_workspace", "medusa_verify_accept_tree_draw",
 )
 
 
@@ -93,6 +96,14 @@ def lib() -> C.CDLL:
     L.medusa_kv_pages_compact_workspace.argtypes = [i32]
     L.medusa_kv_pages_compact_workspace.restype = sz
     L.medusa_kv_pages_compact.argtypes = [P] * 6 + [i32] * 6 + [P] * 4 + [sz, P]
+    L.medusa_rope_rows.argtypes = [P, P, i32, P, P, P] + [i32] * 7 + [P, P, P]
+    L.medusa_kv_append_rope_q8.argtypes = [P, P, i32] + [P] * 9 + [i32, i32, P, P] + [i32] * 9 + [P, P, P, i32, P, P, P]
+    L.medusa_chunk_attention_q8_workspace.argtypes = [i32] * 6
+    L.medusa_chunk_attention_q8_workspace.restype = sz
+    L.medusa_chunk_attention_q8.argtypes = [P, i32] + [P] * 7 + [i32] * 8 + [f32, P, P, sz, P]
+    L.medusa_verify_draw_workspace.argtypes = [i32] * 3
+    L.medusa_verify_draw_workspace.restype = sz
+    L.medusa_verify_accept_tree_draw.argtypes = [P] * 5 + [i32] * 4 + [P] * 5 + [sz, P]
     _lib = L
     return L
 

@@ -341,6 +341,48 @@ def verify_accept_chain(p, q, draft, seed, round_, out=None, ws=None, stream=Non
     return n_acc, out_tok
 
 
+def verify_draw_workspace(B, N, V):
+    return int(lib().medusa_verify_draw_workspace(B, N, V))
+
+
+@_in_stream
+def verify_accept_tree_draw(probs, cand, parent, depth, u, max_depth, out=None, ws=None, stream=None):
+    """Acceptance by drawn tokens: at each node of the path the token that u[b, depth]
+    in [0, 1) picks from row probs[b, node] (the smallest v with p_0 + .. + p_v above u
+    times the row's sum); the child that holds it is accepted, else it is next_tok.
+    probs [B,N,V] float32, u [B, max_depth + 1] float32."""
+    if probs is None or probs.dim() != 3:
+        raise ValueError("probs must be [B, N, V]")
+    _need(probs, "probs", torch.float32)
+    B, N, V = probs.shape
+    dev = probs.get_device()
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev):
+            return verify_accept_tree_draw(probs, cand, parent, depth, u, max_depth, out, ws, stream)
+    _need_shape(cand, "cand", (B, N), _I32, dev)
+    _need_shape(parent, "parent", (N,), _I32, dev)
+    _need_shape(depth, "depth", (N,), _I32, dev)
+    _need_shape(u, "u", (B, max_depth + 1), _F32, dev)
+    if out is None:
+        out = dict(accept_len=torch.empty(B, dtype=_I32, device=probs.device),
+                   best_node=torch.empty(B, dtype=_I32, device=probs.device),
+                   path_nodes=torch.empty((B, max_depth + 1), dtype=_I32, device=probs.device),
+                   next_tok=torch.empty(B, dtype=_I32, device=probs.device))
+    else:
+        for n, shape in (("accept_len", (B,)), ("best_node", (B,)), ("path_nodes", (B, max_depth + 1)), ("next_tok", (B,))):
+            _need_shape(out[n], f"out {n}", shape, _I32, dev)
+    if ws is None:
+        ws = torch.empty(_draw_bytes(B, N, V), dtype=torch.uint8, device=probs.device)
+    else:
+        _need_ws(ws, dev)
+    check(lib().medusa_verify_accept_tree_draw(probs.data_ptr(), cand.data_ptr(), parent.data_ptr(), depth.data_ptr(),
+                                               u.data_ptr(), B, N, V, max_depth, out["accept_len"].data_ptr(),
+                                               out["best_node"].data_ptr(), out["path_nodes"].data_ptr(),
+                                               out["next_tok"].data_ptr(), ws.data_ptr(), ws.numel(),
+                                               _raw_stream(stream, dev)))
+    return out
+
+
 # ----------------------------------------------------------------------------
 @_in_stream
 def kv_compact(k_cache, v_cache, kv_len, path_nodes, accept_len, best_node, N, max_depth,
@@ -426,6 +468,16 @@ def _raw_stream(stream, dev):
 @functools.lru_cache(maxsize=256)
 def _attention_q8_bytes(dev, B, N, Hq, Hkv, D, dtype):
     return max(16, lib().medusa_tree_attention_q8_workspace(B, N, Hq, Hkv, D, dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _chunk_q8_bytes(dev, B, T, Hq, Hkv, D, dtype):
+    return max(16, lib().medusa_chunk_attention_q8_workspace(B, T, Hq, Hkv, D, dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _draw_bytes(B, N, V):
+    return max(16, verify_draw_workspace(B, N, V))
 
 
 @functools.lru_cache(maxsize=256)
@@ -521,6 +573,144 @@ def kv_append_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table,
                                     _ptr(hidden_rows), out["h_next"].data_ptr() if H else None, H,
                                     out["kv_len"].data_ptr(), _ptr(out.get("appended")), _raw_stream(stream, dev)))
     return out
+
+
+def _need_freqs(inv_freq, D, dev):
+    if inv_freq is None or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [n_freq]")
+    _need_shape(inv_freq, "inv_freq", inv_freq.shape, _F32, dev)
+    return inv_freq.shape[0]
+
+
+@_in_stream
+def rope_rows(q, k, kv_len, inv_freq, depth=None, interleaved=False, out=None, stream=None):
+    """Rotary positions: row i of q [B,T,Hq,D] and k [B,T,Hkv,D] (k may be None) turns by
+    the angles (kv_len[b] + depth[i]) * inv_freq (i where depth is None), in pairs
+    (j, n_freq + j), or (2j, 2j + 1) where interleaved.  Returns (q, k) rotated; `out`
+    may be (q, k) itself."""
+    if q is None or q.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D]")
+    _need(q, "q")
+    B, T, Hq, D = q.shape
+    dev, code = q.get_device(), _dtype_of(q)
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev):
+            return rope_rows(q, k, kv_len, inv_freq, depth, interleaved, out, stream)
+    Hkv = 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError(f"k must be [{B}, {T}, Hkv, {D}]")
+        Hkv = k.shape[2]
+        _need_shape(k, "k", (B, T, Hkv, D), q.dtype, dev)
+    _need_shape(kv_len, "kv_len", (B,), _I32, dev)
+    n_freq = _need_freqs(inv_freq, D, dev)
+    if depth is not None:
+        _need_shape(depth, "depth", (T,), _I32, dev)
+    if out is None:
+        out = torch.empty_like(q), torch.empty_like(k) if Hkv else None
+    else:
+        _need_shape(out[0], "out q", q.shape, q.dtype, dev)
+        if Hkv:
+            _need_shape(out[1], "out k", k.shape, q.dtype, dev)
+    check(lib().medusa_rope_rows(q.data_ptr(), _ptr(k), code, kv_len.data_ptr(), _ptr(depth), inv_freq.data_ptr(), B, T, Hq,
+                                 Hkv, D, n_freq, bool(interleaved), out[0].data_ptr(), out[1].data_ptr() if Hkv else None,
+                                 _raw_stream(stream, dev)))
+    return out
+
+
+@_in_stream
+def kv_append_rope_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, inv_freq, rows=None, last=None,
+                      q=None, interleaved=False, best_node=None, hidden_rows=None, out=None, stream=None):
+    """kv_append_q8 of K rows that are not rotated yet: row i turns by the position of its
+    slot, kv_len[b] + i, on its way into the pages, and so do the queries q [B,T,Hq,D] of
+    the same rows, where given (rows then has to be None).  Returns dict(kv_len, appended,
+    h_next, q); rows of q behind last[b] are zero; the pools change in place."""
+    B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev):
+            return kv_append_rope_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, inv_freq, rows,
+                                     last, q, interleaved, best_node, hidden_rows, out, stream)
+    if k_rows is None or k_rows.dim() != 4:
+        raise ValueError(f"k_rows must be [{B}, T, {Hkv}, {D}]")
+    T, dtype = k_rows.shape[1], k_rows.dtype
+    code = _dtype_of(k_rows)
+    _need_shape(k_rows, "k_rows", (B, T, Hkv, D), dtype, dev)
+    _need_shape(v_rows, "v_rows", (B, T, Hkv, D), dtype, dev)
+    n_freq = _need_freqs(inv_freq, D, dev)
+    R = T
+    if rows is not None:
+        if rows.dim() != 2:
+            raise ValueError("rows must be [B, R]")
+        R = rows.shape[1]
+        _need_shape(rows, "rows", (B, R), _I32, dev)
+    if last is not None:
+        _need_shape(last, "last", (B,), _I32, dev)
+    Hq = 0
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError(f"q must be [{B}, {T}, Hq, {D}]")
+        Hq = q.shape[2]
+        _need_shape(q, "q", (B, T, Hq, D), dtype, dev)
+    if (hidden_rows is None) != (best_node is None):
+        raise ValueError("best_node and hidden_rows go together")
+    H = 0
+    if hidden_rows is not None:
+        H = hidden_rows.shape[-1]
+        _need_shape(hidden_rows, "hidden_rows", (B, T, H), dtype, dev)
+        _need_shape(best_node, "best_node", (B,), _I32, dev)
+    if out is None:
+        out = dict(kv_len=torch.empty_like(kv_len), appended=torch.empty_like(kv_len),
+                   h_next=torch.empty((B, H), dtype=dtype, device=kv_len.device) if H else None,
+                   q=torch.empty_like(q) if Hq else None)
+    else:
+        _need_shape(out["kv_len"], "out kv_len", (B,), _I32, dev)
+        if out.get("appended") is not None:
+            _need_shape(out["appended"], "out appended", (B,), _I32, dev)
+        if H:
+            _need_shape(out["h_next"], "out h_next", (B, H), dtype, dev)
+        if Hq:
+            _need_shape(out["q"], "out q", q.shape, dtype, dev)
+    check(lib().medusa_kv_append_rope_q8(k_rows.data_ptr(), v_rows.data_ptr(), code, k_pages.data_ptr(), v_pages.data_ptr(),
+                                         k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
+                                         _ptr(rows), _ptr(last), inv_freq.data_ptr(), n_freq, bool(interleaved), _ptr(q),
+                                         out["q"].data_ptr() if Hq else None, B, T, R, Hq, Hkv, D, P, n_pages, M,
+                                         _ptr(best_node), _ptr(hidden_rows), out["h_next"].data_ptr() if H else None, H,
+                                         out["kv_len"].data_ptr(), _ptr(out.get("appended")), _raw_stream(stream, dev)))
+    return out
+
+
+def chunk_attention_q8_workspace(B, T, Hq, Hkv, D, dtype=torch.bfloat16):
+    return int(lib().medusa_chunk_attention_q8_workspace(B, T, Hq, Hkv, D, _DT[dtype]))
+
+
+@_in_stream
+def chunk_attention_q8(q, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, scale, last=None, out=None, ws=None,
+                       stream=None):
+    """Attention of new tokens over the 8-bit paged cache that holds their keys already: row
+    i of the last[b] + 1 rows of q [B,T,Hq,D] (all T where last is None) is that of slot
+    kv_len[b] - last[b] - 1 + i and sees the slots up to it.  Returns out [B,T,Hq,D] in q's
+    type; rows behind last[b] are zero.  T = 1 is plain decoding."""
+    B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev):
+            return chunk_attention_q8(q, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, scale, last, out, ws, stream)
+    if q is None or q.dim() != 4:
+        raise ValueError(f"q must be [{B}, T, Hq, {D}]")
+    T, Hq, dtype = q.shape[1], q.shape[2], q.dtype
+    code = _dtype_of(q)
+    _need_shape(q, "q", (B, T, Hq, D), dtype, dev)
+    if last is not None:
+        _need_shape(last, "last", (B,), _I32, dev)
+    o = torch.empty_like(q) if out is None else _need_shape(out, "out", q.shape, dtype, dev)
+    if ws is None:
+        ws = torch.empty(_chunk_q8_bytes(dev, B, T, Hq, Hkv, D, code), dtype=torch.uint8, device=q.device)
+    else:
+        _need_ws(ws, dev)
+    check(lib().medusa_chunk_attention_q8(q.data_ptr(), code, k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                                          v_scale.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), _ptr(last), B, T, Hq,
+                                          Hkv, D, P, n_pages, M, scale, o.data_ptr(), ws.data_ptr(), ws.numel(),
+                                          _raw_stream(stream, dev)))
+    return o
 
 
 def kv_pages_fork_workspace(B, n_pages):

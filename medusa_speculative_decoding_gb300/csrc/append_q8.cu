@@ -21,10 +21,12 @@
 // and codes written.
 #include <algorithm>
 
+#include "append.cuh"
 #include "common.cuh"
 #include "q8.cuh"
 
 namespace medusa {
+using namespace append;
 namespace {
 
 struct AppendArgs {
@@ -42,84 +44,6 @@ struct AppendArgs {
     int32_t* appended;
     int B, T, R, Hkv, P, M, n_pages, h16, per_cta;
 };
-
-// Eight neighbouring elements of a row, as they were loaded.
-struct Bf16x8 {
-    uint4 w;
-    __device__ __forceinline__ void load(const uint16_t* p) { w = ld_stream16(p); }
-    __device__ __forceinline__ void unpack(float (&x)[8]) const {
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { x[2 * i] = bf16_lo(v[i]); x[2 * i + 1] = bf16_hi(v[i]); }
-    }
-    // largest |x|, NaN left out
-    __device__ __forceinline__ float top() const {
-        const uint32_t m = max_abs2(max_abs2(w.x, w.y), max_abs2(w.z, w.w));
-        return fmaxf(fmaxf(fabsf(bf16_lo(m)), fabsf(bf16_hi(m))), 0.f);
-    }
-    // the larger of the magnitudes, pair by pair, under some sign
-    static __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-};
-struct F32x8 {
-    uint4 w[2];
-    __device__ __forceinline__ void load(const float* p) { w[0] = ld_stream16(p); w[1] = ld_stream16(p + 4); }
-    __device__ __forceinline__ void unpack(float (&x)[8]) const {
-        const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
-    }
-    __device__ __forceinline__ float top() const {
-        float x[8], m = 0.f;
-        unpack(x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-        return m;
-    }
-};
-template <typename T> struct Raw8;
-template <> struct Raw8<uint16_t> { using type = Bf16x8; };
-template <> struct Raw8<float> { using type = F32x8; };
-
-// the smallest 2^e with top <= 448 * 2^e, e held to [-64, 64]
-__device__ __forceinline__ float page_scale(float top) {
-    if (!(top > 0.f)) return q8::kMinScale;
-    const uint32_t u = __float_as_uint(top);
-    // 448 = 1.75 * 2^8
-    int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    if ((u >> 23) == 0) e = -64;  // subnormal
-    e = q8::clamp_int(e, -64, 64);
-    return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
-// q is a quotient or product rounded to float32, r what the exact one lies above it: the
-// exact one's neighbour with an odd last bit (or itself).  The middle of two codes ends in
-// zeros, so rounding the result to a code is rounding the exact value.
-__device__ __forceinline__ float to_odd(float q, float r) {
-    uint32_t u = __float_as_uint(q);
-    if (r != 0.f) {
-        if ((r < 0.f) != (q < 0.f)) u -= 1;  // towards zero first
-        u |= 1;
-    }
-    return __uint_as_float(u);
-}
-__device__ __forceinline__ float divide_to_odd(float x, float s) {
-    const float q = x / s;
-    // (below, the code is zero whatever the bits; above, it is held at 448)
-    return fabsf(q) > 0x1p-12f && fabsf(q) < 1024.f ? to_odd(q, fmaf(-q, s, x)) : q;
-}
-__device__ __forceinline__ float multiply_to_odd(float x, float s) {
-    const float p = x * s;
-    return to_odd(p, fmaf(x, s, -p));
-}
-// top <= 448 * s, of the exact product
-__device__ __forceinline__ bool fits(float top, float s) {
-    const float p = q8::kE4m3Max * s;
-    return top < p || (top == p && fmaf(q8::kE4m3Max, s, -p) >= 0.f);
-}
 
 // THREADS * CHUNKS pieces of eight elements make a page of one head.
 template <typename T, int D, int THREADS, int CHUNKS>
@@ -228,8 +152,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_q8_kernel(cons
         for (int i = 0; i < THREADS / 32; ++i) top = fmaxf(top, s_top[id & 1][i]);
 
         const bool readable = !had || q8::scale_ok(s0);  // an unreadable page stays one
-        const bool keep = had && (!readable || fits(top, s0));
-        const float s1 = keep ? s0 : page_scale(top);
+        const bool keep = had && (!readable || fits<448>(top, s0));
+        const float s1 = keep ? s0 : page_scale<448>(top);
         if (tid == 0 && !keep) a.scale[kv][unit] = s1;
         if (readable) {
             // 1 / s1 is exact for the powers of two written here; a caller's own scale is divided by

@@ -1,0 +1,323 @@
+// verify_draw.cu -- acceptance of a tree by tokens drawn from the target's probabilities
+// with given random numbers ("Giai ma dau co" page, "Faster without changing the result";
+// "Medusa Heads" glossary page, "Tree attention and acceptance").
+//
+// The candidates are fixed before the target is asked, so the draft is a point mass on each
+// of them and the speculative rule becomes: draw a token from the target's row, accept the
+// child that holds it, and end with the token itself where no child does.  Every token of the
+// round then follows the target's distribution.  The draw at depth d is the smallest v with
+//   p_0 + ... + p_v > u_d * (p_0 + ... + p_{V-1}).
+//
+// A row has V boundaries, each of which could fall next to u: sums in float32 would pick
+// another token in V * 2^-23 of the draws, 1.5% at V = 128256.  So sums are 64 bits wide where
+// they meet: a thread adds 32 values as two float32 sums, of their multiples of 2^-18 (exact)
+// and of what is left (below 2^-14, off by 2^-34 of its terms), and everything from there on
+// is in double; 64-bit additions of every value would take an SM, which does two a cycle,
+// longer than reading them.
+//
+// A cluster of CTAs draws from one row: each CTA sums a contiguous slice, the totals are
+// pushed to every CTA, and the one whose slice holds the number finds the token in it.
+//   draw_walk_kernel  a cluster per sequence walks down the tree, a row per level: reads
+//                     only the rows that it visits, one level after the other
+//   draw_rows_kernel  a cluster per row draws from all rows at once, and walk_kernel follows
+//                     the children: fewer steps in a row where there are few rows
+#include <algorithm>
+
+#include "common.cuh"
+#include "umma.cuh"
+
+namespace medusa {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBatch = 8;         // float4 of a thread with their loads in flight
+constexpr int kMaxCluster = 8;
+constexpr int kSlice = 8192;      // values of a CTA, where the cluster can be that large
+constexpr int kMaxNodes = 512;
+// Bytes of rows up to which drawing from all of them beats walking.
+constexpr long long kAllRows = 48ll << 20;
+
+struct DrawArgs {
+    const float *probs, *u;
+    const int32_t *cand, *parent, *depth;
+    int32_t* drawn;  // ws [B][N]
+    int32_t *accept_len, *best_node, *path_nodes, *next_tok;
+    int B, N, V, Dmax, slice;  // slice: values of a CTA, a multiple of 128 * kWarps
+};
+
+struct DrawSmem {
+    double total[kMaxCluster];  // of every CTA of the cluster
+    double warp_total[kWarps];
+    int token;
+};
+
+// probabilities: negative ones and NaN count as 0, those above 1 as 1
+__device__ __forceinline__ float clean(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
+
+__device__ __forceinline__ double shfl_up_d(double v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
+
+__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// four values from v on; behind `end` zero
+__device__ __forceinline__ float4 values4(const float* row, int v, int end, bool aligned) {
+    if (aligned && v + 4 <= end) {
+        const uint4 r = ld_stream16(row + v);
+        return make_float4(clean(__uint_as_float(r.x)), clean(__uint_as_float(r.y)), clean(__uint_as_float(r.z)), clean(__uint_as_float(r.w)));
+    }
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v + i < end ? clean(__ldg(row + v + i)) : 0.f;
+    return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// The token drawn from row[0 .. V) with u, for all threads of the cluster (-1: the row has no
+// weight).  Called by every thread of the cluster's CTAs, which arrived at the cluster's barrier before
+// the first call.
+__device__ __forceinline__ int draw(const DrawArgs& a, const float* row, float u, DrawSmem& s, int rank, int ctas, bool first) {
+    using namespace umma;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool aligned = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+    const int per_warp = a.slice / kWarps;  // a multiple of 128
+    const int begin = min(a.V, rank * a.slice + warp * per_warp), end = min(a.V, begin + per_warp);
+    double sum = 0.;
+    for (int v0 = begin; v0 < end; v0 += 128 * kBatch) {
+        float4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int v = v0 + 128 * k + 4 * lane;
+            x[k] = v < end ? values4(row, v, end, aligned) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float hi = 0.f, lo = 0.f;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float h = __fsub_rn(__fadd_rn(y[i], 48.f), 48.f);  // to a multiple of 2^-18
+                hi += h;
+                lo += y[i] - h;
+            }
+        }
+        sum += (double)hi + (double)lo;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s.warp_total[warp] = sum;
+    __syncthreads();
+    if (first) cluster_wait();  // every CTA of the cluster runs: its shared memory can be written
+    if (warp == 0) {
+        double t = 0.;
+        for (int w = 0; w < kWarps; ++w) t += s.warp_total[w];
+        if (lane < ctas) st_cluster_f64(cluster_map(smem_addr(&s.total[rank]), lane), t);
+    }
+    cluster_sync();
+    double all = 0.;
+    for (int c = 0; c < ctas; ++c) all += s.total[c];
+    const double target = fmax((double)u * all, 0.);
+    // The part that holds the number: the first whose end lies behind it, the last with any
+    // weight where rounding leaves none.  The same in every CTA.
+    double at = 0., base = 0.;
+    int winner = -1;
+    for (int c = 0; c < ctas; ++c) {
+        const double t = s.total[c];
+        if (!(t > 0.)) continue;
+        winner = c;
+        base = at;
+        at += t;
+        if (at > target) break;
+    }
+    if (rank == max(winner, 0) && warp == 0) {
+        int token = -1;
+        if (winner >= 0) {
+            int w_at = 0;
+            at = base;
+            for (int w = 0; w < kWarps; ++w) {
+                const double t = s.warp_total[w];
+                if (!(t > 0.)) continue;
+                w_at = w;
+                base = at;
+                at += t;
+                if (at > target) break;
+            }
+            const int b0 = min(a.V, rank * a.slice + w_at * per_warp), b1 = min(a.V, b0 + per_warp);
+            at = base;
+            int last = -1;
+            for (int v0 = b0; v0 < b1; v0 += 128 * kBatch) {
+                float4 x[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int v = v0 + 128 * k + 4 * lane;
+                    x[k] = v < b1 ? values4(row, v, b1, aligned) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                    double mine = 0., upto;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mine += (double)y[i];
+                    upto = mine;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const double t = shfl_up_d(upto, o);
+                        if (lane >= o) upto += t;
+                    }
+                    double c = at + (upto - mine);
+                    int found = -1, behind = -1;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        c += (double)y[i];
+                        const int v = v0 + 128 * k + 4 * lane + i;
+                        if (y[i] > 0.f) {
+                            behind = v;
+                            if (found < 0 && c > target) found = v;
+                        }
+                    }
+                    const unsigned hit = __ballot_sync(0xffffffffu, found >= 0), any = __ballot_sync(0xffffffffu, behind >= 0);
+                    if (hit && token < 0) token = __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
+                    if (any) last = __shfl_sync(0xffffffffu, behind, 31 - __clz(any));
+                    at += __shfl_sync(0xffffffffu, upto, 31);
+                }
+                if (token >= 0) break;
+            }
+            if (token < 0) token = last;
+        }
+        if (lane < ctas) st_cluster_s32(cluster_map(smem_addr(&s.token), lane), token);
+    }
+    cluster_sync();
+    return s.token;
+}
+
+// The child of `node` that holds token t, the lowest one; N: none.  Called by the whole block.
+__device__ __forceinline__ int child_of(const int* parent, const int* cand, int N, int node, int t, int* s_child) {
+    if (threadIdx.x == 0) *s_child = N;
+    __syncthreads();
+    if (t >= 0)
+        for (int j = threadIdx.x; j < N; j += blockDim.x)
+            if (j > node && parent[j] == node && cand[j] == t) atomicMin(s_child, j);
+    __syncthreads();
+    return *s_child;
+}
+
+// path: how the round went, written by the block's threads
+__device__ __forceinline__ void finish(const DrawArgs& a, int b, int steps, int node, int token, const int* path) {
+    for (int i = threadIdx.x; i <= a.Dmax; i += blockDim.x) a.path_nodes[(size_t)b * (a.Dmax + 1) + i] = i <= steps ? path[i] : -1;
+    if (threadIdx.x == 0) {
+        a.accept_len[b] = steps;
+        a.best_node[b] = node;
+        a.next_tok[b] = token;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) draw_walk_kernel(const DrawArgs a) {
+    __shared__ DrawSmem s;
+    __shared__ int s_parent[kMaxNodes], s_cand[kMaxNodes], s_path[kMaxNodes], s_child;
+    const int ctas = gridDim.x, rank = blockIdx.x, b = blockIdx.y;
+    umma::cluster_arrive_relaxed();
+    pdl_wait();
+    pdl_trigger();
+    for (int i = threadIdx.x; i < a.N; i += kThreads) {
+        s_parent[i] = a.parent[i];
+        s_cand[i] = a.cand[(size_t)b * a.N + i];
+    }
+    int node = 0, token = -1, steps = 0;
+    if (threadIdx.x == 0) s_path[0] = 0;
+    for (;;) {
+        token = draw(a, a.probs + ((size_t)b * a.N + node) * a.V, a.u[(size_t)b * (a.Dmax + 1) + steps], s, rank, ctas, steps == 0);
+        if (steps == a.Dmax) break;
+        const int child = child_of(s_parent, s_cand, a.N, node, token, &s_child);
+        if (child == a.N) break;
+        node = child;
+        ++steps;
+        if (threadIdx.x == 0) s_path[steps] = node;
+        __syncthreads();  // s_child is set anew
+    }
+    __syncthreads();
+    if (rank == 0) finish(a, b, steps, node, token, s_path);
+}
+
+__global__ void __launch_bounds__(kThreads) draw_rows_kernel(const DrawArgs a) {
+    __shared__ DrawSmem s;
+    const int ctas = gridDim.x, rank = blockIdx.x, node = blockIdx.y, b = blockIdx.z;
+    umma::cluster_arrive_relaxed();
+    pdl_wait();
+    pdl_trigger();
+    const int d = min(max(a.depth[node], 0), a.Dmax);
+    const int token = draw(a, a.probs + ((size_t)b * a.N + node) * a.V, a.u[(size_t)b * (a.Dmax + 1) + d], s, rank, ctas, true);
+    if (rank == 0 && threadIdx.x == 0) a.drawn[(size_t)b * a.N + node] = token;
+}
+
+__global__ void __launch_bounds__(256) walk_kernel(const DrawArgs a) {
+    __shared__ int s_parent[kMaxNodes], s_cand[kMaxNodes], s_drawn[kMaxNodes], s_path[kMaxNodes], s_child;
+    const int b = blockIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    for (int i = threadIdx.x; i < a.N; i += blockDim.x) {
+        s_parent[i] = a.parent[i];
+        s_cand[i] = a.cand[(size_t)b * a.N + i];
+        s_drawn[i] = a.drawn[(size_t)b * a.N + i];
+    }
+    if (threadIdx.x == 0) s_path[0] = 0;
+    __syncthreads();
+    int node = 0, steps = 0;
+    while (steps < a.Dmax) {
+        const int child = child_of(s_parent, s_cand, a.N, node, s_drawn[node], &s_child);
+        if (child == a.N) break;
+        node = child;
+        ++steps;
+        if (threadIdx.x == 0) s_path[steps] = node;
+        __syncthreads();
+    }
+    __syncthreads();
+    finish(a, b, steps, node, s_drawn[node], s_path);
+}
+
+int check_draw(int B, int N, int V, int Dmax) {
+    if (B < 1 || N < 1 || V < 1 || Dmax < 0)
+        return fail(MEDUSA_ERR_INVALID_ARG, "verify_accept_tree_draw: sizes must be positive");
+    if (N > kMaxNodes || Dmax >= kMaxNodes || B > 65535 || V > 1 << 24)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "verify_accept_tree_draw: at most %d nodes, 65535 sequences and 2^24 tokens", kMaxNodes);
+    return MEDUSA_OK;
+}
+
+}  // namespace
+}  // namespace medusa
+
+using namespace medusa;
+
+extern "C" size_t medusa_verify_draw_workspace(int B, int N, int V) {
+    (void)V;
+    return B < 1 || N < 1 ? 0 : (size_t)B * N * sizeof(int32_t);
+}
+
+extern "C" int medusa_verify_accept_tree_draw(const float* probs, const int32_t* cand, const int32_t* parent,
+                                              const int32_t* depth, const float* u, int B, int N, int V, int Dmax,
+                                              int32_t* accept_len, int32_t* best_node, int32_t* path_nodes,
+                                              int32_t* next_tok, void* ws, size_t ws_bytes, void* stream) {
+    if (int rc = check_draw(B, N, V, Dmax)) return rc;
+    if (!probs || !cand || !parent || !depth || !u || !accept_len || !best_node || !path_nodes || !next_tok)
+        return fail(MEDUSA_ERR_INVALID_ARG, "verify_accept_tree_draw: null pointer");
+    const size_t need = medusa_verify_draw_workspace(B, N, V);
+    if (!ws || ws_bytes < need)
+        return fail(MEDUSA_ERR_WORKSPACE, "verify_accept_tree_draw: workspace of %zu bytes needed", need);
+    if (reinterpret_cast<uintptr_t>(ws) & 3u)
+        return fail(MEDUSA_ERR_INVALID_ARG, "verify_accept_tree_draw: ws must be 4-byte aligned");
+    DrawArgs a{probs, u, cand, parent, depth, (int32_t*)ws, accept_len, best_node, path_nodes, next_tok, B, N, V, Dmax, 0};
+    const int ctas = std::min(kMaxCluster, (V + kSlice - 1) / kSlice), unit = 128 * kWarps;
+    a.slice = (int)(((long long)(V + ctas - 1) / ctas + unit - 1) / unit * unit);
+    cudaStream_t st = as_stream(stream);
+    cudaError_t e;
+    if ((long long)B * N * V * 4 <= kAllRows || N == 1) {
+        e = launch_cluster(draw_rows_kernel, dim3(ctas, N, B), dim3(kThreads), 0, st, ctas, a);
+        if (e == cudaSuccess) e = launch(walk_kernel, dim3(B), dim3(256), 0, st, a);
+    } else {
+        e = launch_cluster(draw_walk_kernel, dim3(ctas, B), dim3(kThreads), 0, st, ctas, a);
+    }
+    if (e != cudaSuccess)
+        return fail(MEDUSA_ERR_CUDA, "verify_accept_tree_draw: launch failed: %s", cudaGetErrorString(e));
+    return MEDUSA_OK;
+}
