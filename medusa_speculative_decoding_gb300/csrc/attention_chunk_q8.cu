@@ -58,7 +58,7 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // ---------------------------------------------------------------------------
 // tcgen05 kernel (bf16 queries).
 //
-// Queries in the TMEM lanes, a softmax thread per query row.
+// Queries in the TMEM lanes; two softmax threads per query row, 64 keys of a tile each.
 //   scores  K's codes enter the product as they are.  A bf16 value has eight significant bits:
 //           q = q_hi + q_lo, an e4m3 and an e5m2 plane under one power of two per row.  What
 //           q_hi leaves of a value has three bits, which e5m2 holds down to 2^-16: the sum is
@@ -76,7 +76,7 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // Scales are those of a page: 16 neighbouring keys share theirs, so they cost a thread one
 // load and two instructions per 16 scores.
 //
-// Two streams per CTA (a softmax warpgroup each), each with its own S and O in TMEM, so that
+// Two streams per CTA (two softmax warpgroups each, one per 64 keys of a tile), each with its own S and O in TMEM, so that
 // one stream's softmax runs while the tensor core works for the other:
 //   PAIR = true   blocks of 256 rows, 128 a stream; both use every tile
 //   PAIR = false  blocks of up to 128 rows (plain decoding, short chunks): the streams take
@@ -84,8 +84,8 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // Steps x = 0, 1, 2, ...: stream x & 1, tile x / 2 (or x).  The MMA warp issues PV(x), then
 // S(x + 2), so that a stream's scores being in also says that its last PV is done.
 //
-// Warps 0-3, 4-7 softmax, 8-11 conversion of V, 12 MMA, 13 pages, scales and TMA, 14 and 15
-// idle (registers are handed over by groups of four warps).
+// Warps 0-7, 8-15 softmax of stream 0, 1, 16-19 conversion of V, 20 MMA, 21 pages, scales and TMA,
+// 22 and 23 idle (registers are handed over by groups of four warps).
 //
 // V codes that are NaN would spoil rows that do not see them (0 * NaN), and the slots behind a
 // sequence's length hold anything: the conversion writes zero for them and notes the key, and
@@ -94,27 +94,29 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // Every wait is bounded; a CTA that gives up marks its results NaN.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128, kRows = 128;  // keys of a tile, rows of a stream
-constexpr int kThreads = 512, kConvWarp = 8, kMmaWarp = 12, kTmaWarp = 13;
-constexpr int kScaleRing = 16;
+constexpr int kHalf = kTile / 2;           // keys whose weights are handed over together
+constexpr int kThreads = 480, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kTmaWarp = 14;  // an MMA warp per stream
 constexpr int kGroups = kTile / 16;  // keys that share a scale
 constexpr float kLift = 8.f, kMove = 7.f;
 constexpr int kSetup = 3;
-constexpr long long kDrainCycles = kDefaultWaitCycles;
+constexpr uint32_t kDrainCycles = (uint32_t)kDefaultWaitCycles;
 
 template <int D, bool PAIR>
 struct USmem {
     static constexpr int KR = (PAIR ? 3 : 4) * (128 / D), VR = (PAIR ? 2 : 3) * (128 / D);
+    static constexpr int kScaleRing = 1024 / D;  // tiles whose scales are held
     static constexpr int kCodes = kTile * D;  // K or V of a tile, or a plane of q
     static constexpr int kOffK = (PAIR ? 4 : 2) * kCodes;
     static constexpr int kOffV = kOffK + KR * kCodes;
     static constexpr int kOffV16 = kOffV + VR * kCodes;
     static constexpr int kOffScale = kOffV16 + 2 * kCodes * 2;  // float4 [kScaleRing][kGroups]
     static constexpr int kOffNan = kOffScale + kScaleRing * kGroups * 16;  // uint32 [2][4]
-    static constexpr int kOffX = kOffNan + 32;                             // float2 [2][128]
-    static constexpr int kOffCursor = kOffX + 2 * kRows * 8;
+    static constexpr int kOffQf = kOffNan + 32;  // float [2][256]: the rows' factors
+    static constexpr int kOffX = kOffQf + 2 * 2 * kRows * 4;  // float2 [2][128]: the streams' references and sums (split)
+    static constexpr int kOffCursor = kOffX + (PAIR ? 0 : 2 * kRows * 8);
     static constexpr int kOffBar = kOffCursor + 32;
-    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull pfull odone qfull [2], xfull xdone, scfull, drain
-    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 8 + 2 + kScaleRing + 1;
+    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull [2], pfull odone [2][2], qfull qfree xfull xdone drain [2], scfull
+    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 10 + 6 + kScaleRing;
     static constexpr int kOffMisc = kOffBar + kBars * 8;  // TMEM slot, flag
     static constexpr int kOffTables = kOffMisc + 8;
     static constexpr int bytes(int B) { return kOffTables + chunks::table_bytes(B) + 1024; }  // + alignment
@@ -166,14 +168,27 @@ __device__ __forceinline__ void mma_f16_ta_warp(uint32_t d_tmem, uint32_t a_tmem
         : "memory");
 }
 
-// A wait by a whole warp: true if the phase completed for every lane.  (A suspended lane comes
-// back late: limits that are shorter than that, set to make waits run out, are kept by polling.)
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long lim) {
+// One try that suspends the thread until the phase completes, or for about a tenth of a
+// millisecond: a warp that polls takes issue slots from those that work (without the hint a
+// wait came back at once, and waiting took half of all instructions).
+__device__ __forceinline__ bool mbar_try_long(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity), "r"(100000u)
+        : "memory");
+    return done != 0;
+}
+// A wait by a whole warp: true if the phase completed for every lane.  (Limits that are shorter
+// than a suspended try, set to make waits run out, are kept by polling.)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t lim) {
     bool done = umma::mbar_test(bar, parity);
     if (!done) {
-        const long long t0 = clock64();
-        do done = lim < 65536 ? umma::mbar_test(bar, parity) : umma::mbar_try(bar, parity);
-        while (!done && clock64() - t0 <= lim);
+        const uint32_t t0 = (uint32_t)clock();
+        do done = lim < 65536 ? umma::mbar_test(bar, parity) : mbar_try_long(bar, parity);
+        while (!done && (uint32_t)clock() - t0 <= lim);
     }
     return __all_sync(0xffffffffu, done);
 }
@@ -191,54 +206,74 @@ __device__ __forceinline__ uint64_t code_desc(uint32_t addr) {
     else return umma::desc_sw64(addr, 16, 512);
 }
 
-// Writes half (or all) of a query row's two planes and returns what its scores have to be
-// multiplied with (NaN where the row is not finite).  c0, c1: its 16-element chunks to write.
-template <int D>
-__device__ __forceinline__ float write_planes(const uint16_t* q, uint8_t* hi, uint8_t* lo, int r, int c0, int c1) {
-    constexpr int W = D / 8;
-    uint4 w[W];
-    uint32_t m = 0;
+// Eight values of a query row as two planes; f: the row's power of two.
+__device__ __forceinline__ void split_planes(const uint4& x, float f, uint2& hi, uint2& lo) {
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+    uint16_t h[4], l[4];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        w[i] = q ? *reinterpret_cast<const uint4*>(q + 8 * i) : make_uint4(0, 0, 0, 0);
-        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = max(m, max(v[e] & 0x7fffu, v[e] >> 16 & 0x7fffu));
+    for (int i = 0; i < 4; ++i) {
+        const float a = bf16_lo(v[i]) * f, b = bf16_hi(v[i]) * f;
+        h[i] = q8::float2_to_e4m3x2(a, b);
+        const float2 g = q8::e4m3x2_to_float2(h[i]);
+        l[i] = to_e5m2x2(a - g.x, b - g.y);
     }
-    if (m >= 0x7f80u) {  // an infinity or NaN: the row's results are NaN
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    hi = make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16);
+    lo = make_uint2((uint32_t)l[0] | (uint32_t)l[1] << 16, (uint32_t)l[2] | (uint32_t)l[3] << 16);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 32 bytes, both 16-byte halves at once where the address allows
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&w)[8], bool aligned) {
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                     "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    // largest |q| in [2^e, 2^(e + 1)) goes to [2^7, 2^8)
-    const int e = max((int)(m >> 7) - 127, -119);
-    const float f = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+}
+
+// What a score is multiplied with; never 0, so that a masked one stays -inf (NaN stays NaN).
+__device__ __forceinline__ float factor(float k, float qf) { return max_nan(k * qf, FLT_MIN); }
+
+__device__ __forceinline__ float max16(const float (&v)[16]) {
+    float m0 = v[0], m1 = v[1];
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-        if (c < c0 || c >= c1) continue;
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint4 x = w[2 * c + k];
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                uint16_t hc[2], lc[2];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const float a = bf16_lo(v[2 * p + s]) * f, b = bf16_hi(v[2 * p + s]) * f;
-                    hc[s] = q8::float2_to_e4m3x2(a, b);
-                    const float2 g = q8::e4m3x2_to_float2(hc[s]);
-                    lc[s] = to_e5m2x2(a - g.x, b - g.y);
-                }
-                h[2 * k + p] = (uint32_t)hc[0] | (uint32_t)hc[1] << 16;
-                l[2 * k + p] = (uint32_t)lc[0] | (uint32_t)lc[1] << 16;
-            }
-        }
-        const uint32_t o = code_offset<D>(r, c);
-        *reinterpret_cast<uint4*>(hi + o) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
+    for (int e = 2; e < 14; e += 4) {
+        m0 = max3(m0, v[e], v[e + 1]);
+        m1 = max3(m1, v[e + 2], v[e + 3]);
     }
-    return m >= 0x7f80u ? NAN : __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+    return max3(m0, m1, fmaxf(v[14], v[15]));
+}
+
+// Weights of 16 scores of one page, 2^(v * kc + off), as f16; their sum / vs added to l.
+__device__ __forceinline__ void row_weights(const float (&v)[16], float kc, float off, float per_vs, uint32_t* p, float& l) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        float x0, x1;
+        fma2(x0, x1, v[e], v[e + 1], kc, off);
+        x0 = umma::exp2_approx(x0);
+        x1 = umma::exp2_approx(x1);
+        add2(s0, s1, x0, x1);
+        p[e / 2] = pack_f16(x0, x1);
+    }
+    l = fmaf(s0 + s1, per_vs, l);
+}
+
+// a pair of f16 times a power of two
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t x, float f) {
+    uint32_t r;
+    asm("{\n.reg .f16 a, b;\n.reg .f32 u, v;\nmov.b32 {a, b}, %1;\ncvt.f32.f16 u, a;\ncvt.f32.f16 v, b;\nmul.f32 u, u, %2;\nmul.f32 v, v, %2;\n"
+        "cvt.rn.f16x2.f32 %0, v, u;\n}"
+        : "=r"(r) : "r"(x), "f"(f));
+    return r;
 }
 
 template <int D, bool PAIR>
@@ -247,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                                                                          const ChunkArgs a) {
     using namespace umma;
     using L = USmem<D, PAIR>;
-    constexpr int KR = L::KR, VR = L::VR;
+    constexpr int KR = L::KR, VR = L::VR, kScaleRing = L::kScaleRing;
     constexpr uint32_t kOCol = 128, kSCol = 256, kCols = 512;  // O_s at 128 s, S_s at 256 + 128 s
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -255,26 +290,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
     const uint32_t base_a = smem_addr(base);
     const uint32_t bar = base_a + L::kOffBar;
     const uint32_t kfull = bar, kempty = kfull + 8 * KR, vfull = kempty + 8 * KR, vempty = vfull + 8 * VR, wfull = vempty + 8 * VR,
-                   wempty = wfull + 16, sfull = wempty + 16, pfull = sfull + 16, odone = pfull + 16, qfull = odone + 16,
-                   xfull = qfull + 16, xdone = xfull + 8, scfull = xdone + 8, drain = scfull + 8 * kScaleRing;
+                   wempty = wfull + 16, sfull = wempty + 16, pfull = sfull + 16, odone = pfull + 32, qfull = odone + 32, qfree = qfull + 8,
+                   xfull = qfree + 8, xdone = xfull + 8, drain = xdone + 8, scfull = drain + 16;
     float4* s_scale = reinterpret_cast<float4*>(base + L::kOffScale);
     uint32_t* s_nan = reinterpret_cast<uint32_t*>(base + L::kOffNan);
-    float2* s_x = reinterpret_cast<float2*>(base + L::kOffX);
+    float* s_qf = reinterpret_cast<float*>(base + L::kOffQf);
     int* s_cursor = reinterpret_cast<int*>(base + L::kOffCursor);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::kOffMisc);
     volatile int* flag = reinterpret_cast<volatile int*>(base + L::kOffMisc + 4);
     const chunks::Work& w = a.work;
     const chunks::Tables tab(base + L::kOffTables, w.B);
-    const long long lim = g_wait_limit;
+    const uint32_t lim = (uint32_t)min(g_wait_limit, kDefaultWaitCycles);
 
     if (warp == kTmaWarp && lane == 0) {
         for (int i = 0; i < L::kBars; ++i) mbar_init(bar + 8 * i, 1);
-        for (int i = 0; i < VR; ++i) mbar_init(vempty + 8 * i, 4);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(wfull + 8 * i, 4);
-            mbar_init(pfull + 8 * i, 4);
-            mbar_init(qfull + 8 * i, PAIR ? 4 : 8);
+        for (int i = 0; i < VR; ++i) mbar_init(vempty + 8 * i, kConvWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(wfull + 8 * i, kConvWarps);
+        if (PAIR) {  // both streams' products are done with a tile
+            for (int i = 0; i < KR; ++i) mbar_init(kempty + 8 * i, 2);
+            for (int i = 0; i < 2; ++i) mbar_init(wempty + 8 * i, 2);
         }
+        mbar_init(qfree, 2);
+        for (int i = 0; i < 4; ++i) mbar_init(pfull + 8 * i, 4);
+        mbar_init(qfull, kConvWarps);
         mbar_init(xfull, 8);
         mbar_init(xdone, 8);
         mbar_init_fence();
@@ -298,153 +336,194 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    chunks::Cursor at;
-    at.b = at.j = at.h = 0;
-    at.begin = g1;
-    at.L = at.n = at.tiles = 0;
-    if (g0 < g1) {
-        at.b = s_cursor[0]; at.j = s_cursor[1]; at.h = s_cursor[2];
-        at.begin = (uint32_t)s_cursor[3];
-        at.set(w, tab);
-    }
-    const chunks::Cursor start = at;
+    auto first_unit = [&] {
+        chunks::Cursor c;
+        c.b = c.j = c.h = c.L = c.n = c.tiles = 0;
+        c.begin = g1;
+        if (g0 < g1) {
+            c.b = s_cursor[0]; c.j = s_cursor[1]; c.h = s_cursor[2];
+            c.begin = (uint32_t)s_cursor[3];
+            c.set(w, tab);
+        }
+        return c;
+    };
+    chunks::Cursor at = first_unit();
+    const uint32_t g_magic = (65536u + a.G - 1) / a.G;  // r / G for r < 256, G <= 64
+    auto token_of = [&](int r) { return (int)((uint32_t)r * g_magic >> 16); };
     int issued_k = 0, issued_v = 0;  // tiles requested
     bool ok = true;
 
-    if (warp >= kMmaWarp) {
-        if (warp == kMmaWarp) {
-            // -------------------------------- MMA --------------------------------
-            constexpr uint32_t idesc_hi = idesc_f8(kRows, kTile, 0, 0, 0, 0), idesc_lo = idesc_f8(kRows, kTile, 1, 0, 0, 0);
-            constexpr uint32_t idesc_pv = idesc_f16(kRows, D);
-            const uint64_t dq = code_desc<D>(base_a), dk = code_desc<D>(base_a + L::kOffK);
-            const uint64_t dv = desc_sw128(base_a + L::kOffV16, kTile * 128, 1024);
-            uint32_t kt = 0, vt = 0;         // K tiles whose first S, V tiles whose first PV is issued
-            uint32_t steps[2] = {0, 0};      // P phases consumed
-            uint32_t segments = 0;
-            for (; ok && at.begin < g1; at.next(w, tab)) {
-                const int nt = at.end_tile(w, g1) - at.first_tile(w, g0);
-                if (nt <= 0) continue;
-                const int X = PAIR ? 2 * nt : nt;
-                const uint32_t k0 = kt, v0 = vt;
-                auto issue_s = [&](int x) {
-                    const int s = x & 1;
-                    const uint32_t tile = k0 + (PAIR ? x >> 1 : x), slot = tile % KR;
-                    if ((!PAIR || s == 0) && !warp_wait(kfull + 8 * slot, (tile / KR) & 1, lim)) return false;
-                    const uint64_t k = dk + (uint64_t)((slot * L::kCodes) >> 4);
-                    const uint64_t q = dq + (uint64_t)(((PAIR ? 2 * s : 0) * L::kCodes) >> 4);
-                    const uint32_t d = tmem + kSCol + s * 128;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) mma_f8_warp(d, q + 2 * i, k + 2 * i, idesc_hi, i > 0);
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) mma_f8_warp(d, q + (L::kCodes >> 4) + 2 * i, k + 2 * i, idesc_lo, 1);
-                    commit_warp(sfull + 8 * s);
-                    if (!PAIR || s == 1) commit_warp(kempty + 8 * slot);
-                    return true;
-                };
-                // (Q's barriers complete once a segment)
-                for (int x = 0; x < 2 && x < X && ok; ++x) {
-                    if (PAIR || x == 0) ok = warp_wait(qfull + 8 * x, segments & 1, lim);
-                    fence_after_sync();
-                    ok = ok && issue_s(x);
-                }
-                for (int x = 0; x < X && ok; ++x) {
-                    const int s = x & 1;
-                    const uint32_t tile = v0 + (PAIR ? x >> 1 : x), slot = tile & 1;
-                    ok = warp_wait(pfull + 8 * s, steps[s] & 1, lim);
-                    ++steps[s];
-                    if (ok && (!PAIR || s == 0)) ok = warp_wait(wfull + 8 * slot, (tile >> 1) & 1, lim);
-                    if (!ok) break;
-                    fence_after_sync();
-                    const uint64_t v = dv + (uint64_t)((slot * L::kCodes * 2) >> 4);
-                    const uint32_t p = tmem + kSCol + s * 128;
-#pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i)
-                        mma_f16_ta_warp(tmem + s * kOCol, p + 8 * i, v + ((i * 2048) >> 4), idesc_pv, (x > 1 || i > 0) ? 1u : 0u);
-                    if (x + 2 >= X) commit_warp(odone + 8 * s);  // the stream's last
-                    if (!PAIR || s == 1) commit_warp(wempty + 8 * slot);
-                    if (x + 2 < X) ok = issue_s(x + 2);
-                }
-                kt += nt;
-                vt += nt;
-                ++segments;
-            }
-            if (!ok) *flag = 1;
-        } else if (warp == kTmaWarp) {
-            // ------------------------- pages, scales, TMA -------------------------
-            const int ppt = kTile / a.P;  // pages of a tile
-            const int nowhere = a.n_pages * a.Hkv * a.P;  // rows behind the pool read zero
-            for (; ok && at.begin < g1; at.next(w, tab)) {
-                const int t0 = at.first_tile(w, g0), t1 = at.end_tile(w, g1);
-                if (t1 <= t0) continue;
-                const int32_t* table = a.page_table + (size_t)at.b * a.M;
-                const int pages = (at.L + a.P - 1) / a.P, p0 = t0 * ppt;
-                auto page_of = [&](int i) { return i < pages ? table[i] : -1; };
-                auto scales_of = [&](int page, float& ks, float& vs) {
-                    ks = vs = 0.f;  // not readable
-                    if (page < 0 || page >= a.n_pages) return;
-                    ks = a.k_scale[(size_t)page * a.Hkv + at.h];
-                    vs = a.v_scale[(size_t)page * a.Hkv + at.h];
-                };
-                // 32 pages at a time, one a lane: the next ones' scales and the page numbers behind
-                // those are on their way
-                int page = page_of(p0 + lane), page1 = page_of(p0 + 32 + lane);
-                float ks, vs, ks1, vs1;
-                scales_of(page, ks, vs);
-                int at_page = 0;
-                float4 sc;
-                int row;
-                auto take = [&] {
-                    const bool there = q8::scale_ok(ks) && q8::scale_ok(vs);
-                    const uint32_t u = __float_as_uint(vs);
-                    const float lg = (u & 0x7fffffu) ? log2f(vs) : (float)((int)(u >> 23) - 127);
-                    sc = there ? make_float4(ks * a.scale_log2, lg, 1.f / vs, 0.f) : make_float4(0.f, -INFINITY, 0.f, 0.f);
-                    row = there ? (page * a.Hkv + at.h) * a.P : nowhere;
-                };
-                scales_of(page1, ks1, vs1);
-                int page2 = page_of(p0 + 64 + lane);
-                take();
-                for (int t = t0; t < t1 && ok; ++t) {
-                    const uint32_t kslot = (uint32_t)issued_k % KR, vslot = (uint32_t)issued_v % VR;
-                    const int i = lane - at_page;  // page of the tile
-                    const bool mine = i >= 0 && i < ppt;
-                    if (issued_k >= KR) ok = warp_wait(kempty + 8 * kslot, (uint32_t)(issued_k / KR - 1) & 1, lim);
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(kfull + 8 * kslot, L::kCodes);
-                    __syncwarp();
-                    if (mine) tma_load_2d(base_a + L::kOffK + kslot * L::kCodes + i * a.P * D, &tmk, 0, row, kfull + 8 * kslot);
-                    const uint32_t sslot = (uint32_t)issued_k % kScaleRing;
-                    ++issued_k;
-                    if (mine)
-                        for (int g = 0; g < a.P / 16; ++g) s_scale[sslot * kGroups + i * (a.P / 16) + g] = sc;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(scfull + 8 * sslot);
-                    if (issued_v >= VR) ok = warp_wait(vempty + 8 * vslot, (uint32_t)(issued_v / VR - 1) & 1, lim);
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(vfull + 8 * vslot, L::kCodes);
-                    __syncwarp();
-                    if (mine) tma_load_2d(base_a + L::kOffV + vslot * L::kCodes + i * a.P * D, &tmv, 0, row, vfull + 8 * vslot);
-                    ++issued_v;
-                    at_page += ppt;
-                    if (at_page == 32 && t + 1 < t1) {
-                        at_page = 0;
-                        const int next = p0 + (t + 1 - t0) * ppt;
-                        page = page1; ks = ks1; vs = vs1;
-                        page1 = page2;
-                        scales_of(page1, ks1, vs1);
-                        page2 = page_of(next + 64 + lane);
-                        take();
-                    }
-                }
-            }
-            if (!ok) *flag = 1;
-        }
-    } else if (warp >= kConvWarp) {
-        // ------------------------- V codes to f16 -------------------------
-        const int ct = tid - kConvWarp * 32;
-        uint32_t tile = 0;
+    if (warp >= kMmaWarp && warp < kTmaWarp) {
+        // -------------------------------- MMA --------------------------------
+        constexpr uint32_t idesc_hi = idesc_f8(kRows, kTile, 0, 0, 0, 0), idesc_lo = idesc_f8(kRows, kTile, 1, 0, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_f16(kRows, D);
+        const int s = warp - kMmaWarp;
+        const uint64_t dq = code_desc<D>(base_a + (PAIR ? 2 * s : 0) * L::kCodes), dk = code_desc<D>(base_a + L::kOffK);
+        const uint64_t dv = desc_sw128(base_a + L::kOffV16, kTile * 128, 1024);
+        const uint32_t tO = tmem + s * kOCol, tS = tmem + kSCol + s * 128;
+        uint32_t first = 0, segments = 0, had = 0;  // tiles before the segment, the stream's among them
         for (; ok && at.begin < g1; at.next(w, tab)) {
             const int nt = at.end_tile(w, g1) - at.first_tile(w, g0);
-            for (int t = 0; t < nt && ok; ++t, ++tile) {
+            if (nt <= 0) continue;
+            const int ns = PAIR ? nt : (nt + 1 - s) / 2;  // tiles of the stream
+            auto tile_of = [&](int i) { return first + (PAIR ? i : 2 * i + s); };
+            auto issue_s = [&](int i) {
+                const uint32_t tile = tile_of(i), slot = tile % KR;
+                if (!warp_wait(kfull + 8 * slot, (tile / KR) & 1, lim)) return false;
+                const uint64_t k = dk + (uint64_t)((slot * L::kCodes) >> 4);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) mma_f8_warp(tS, dq + 2 * c, k + 2 * c, idesc_hi, c > 0);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) mma_f8_warp(tS, dq + (L::kCodes >> 4) + 2 * c, k + 2 * c, idesc_lo, 1);
+                commit_warp(sfull + 8 * s);
+                commit_warp(kempty + 8 * slot);
+                if (i + 1 == ns) commit_warp(qfree);
+                return true;
+            };
+            ok = warp_wait(qfull, segments & 1, lim);
+            fence_after_sync();
+            if (ns) ok = ok && issue_s(0);
+            else if (lane == 0) mbar_arrive(qfree);
+            for (int i = 0; i < ns && ok; ++i) {
+                const uint32_t tile = tile_of(i), slot = tile & 1;
+                const uint64_t v = dv + (uint64_t)((slot * L::kCodes * 2) >> 4);
+                ok = warp_wait(wfull + 8 * slot, (tile >> 1) & 1, lim);
+                for (int h = 0; h < 2 && ok; ++h) {
+                    ok = warp_wait(pfull + 8 * (2 * s + h), (had + i) & 1, lim);
+                    if (!ok) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < kHalf / 16; ++k)
+                        mma_f16_ta_warp(tO, tS + 32 * h + 8 * k, v + (((4 * h + k) * 2048) >> 4), idesc_pv, (i > 0 || h > 0 || k > 0) ? 1u : 0u);
+                    commit_warp(odone + 8 * (2 * s + h));
+                }
+                if (!ok) break;
+                commit_warp(wempty + 8 * slot);
+                if (i + 1 < ns) ok = issue_s(i + 1);
+            }
+            first += nt;
+            had += ns;
+            ++segments;
+        }
+        if (!ok) *flag = 1;
+    } else if (warp == kTmaWarp) {
+        // ------------------------- pages, scales, TMA -------------------------
+        const int ppt = kTile / a.P;  // pages of a tile
+        const int nowhere = a.n_pages * a.Hkv * a.P;  // rows behind the pool read zero
+        for (; ok && at.begin < g1; at.next(w, tab)) {
+            const int t0 = at.first_tile(w, g0), t1 = at.end_tile(w, g1);
+            if (t1 <= t0) continue;
+            const int32_t* table = a.page_table + (size_t)at.b * a.M;
+            const int pages = (at.L + a.P - 1) / a.P, p0 = t0 * ppt;
+            auto page_of = [&](int i) { return i < pages ? table[i] : -1; };
+            auto scales_of = [&](int page, float& ks, float& vs) {
+                ks = vs = 0.f;  // not readable
+                if (page < 0 || page >= a.n_pages) return;
+                ks = a.k_scale[(size_t)page * a.Hkv + at.h];
+                vs = a.v_scale[(size_t)page * a.Hkv + at.h];
+            };
+            // 32 pages at a time, one a lane: the next ones' scales and the page numbers behind
+            // those are on their way
+            int page = page_of(p0 + lane), page1 = page_of(p0 + 32 + lane);
+            float ks, vs, ks1, vs1;
+            scales_of(page, ks, vs);
+            int at_page = 0;
+            float4 sc;
+            int row;
+            auto take = [&] {
+                const bool there = q8::scale_ok(ks) && q8::scale_ok(vs);
+                const uint32_t u = __float_as_uint(vs);
+                const float lg = (u & 0x7fffffu) ? log2f(vs) : (float)((int)(u >> 23) - 127);
+                sc = there ? make_float4(ks * a.scale_log2, lg, 1.f / vs, 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
+                row = there ? (page * a.Hkv + at.h) * a.P : nowhere;
+            };
+            scales_of(page1, ks1, vs1);
+            int page2 = page_of(p0 + 64 + lane);
+            take();
+            for (int t = t0; t < t1 && ok; ++t) {
+                const uint32_t kslot = (uint32_t)issued_k % KR, vslot = (uint32_t)issued_v % VR;
+                const int i = lane - at_page;  // page of the tile
+                const bool mine = i >= 0 && i < ppt;
+                if (issued_k >= KR) ok = warp_wait(kempty + 8 * kslot, (uint32_t)(issued_k / KR - 1) & 1, lim);
+                if (!ok) break;
+                if (lane == 0) mbar_expect_tx(kfull + 8 * kslot, L::kCodes);
+                __syncwarp();
+                if (mine) tma_load_2d(base_a + L::kOffK + kslot * L::kCodes + i * a.P * D, &tmk, 0, row, kfull + 8 * kslot);
+                const uint32_t sslot = (uint32_t)issued_k % kScaleRing;
+                ++issued_k;
+                if (mine)
+                    for (int g = 0; g < a.P / 16; ++g) s_scale[sslot * kGroups + i * (a.P / 16) + g] = sc;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(scfull + 8 * sslot);
+                if (issued_v >= VR) ok = warp_wait(vempty + 8 * vslot, (uint32_t)(issued_v / VR - 1) & 1, lim);
+                if (!ok) break;
+                if (lane == 0) mbar_expect_tx(vfull + 8 * vslot, L::kCodes);
+                __syncwarp();
+                if (mine) tma_load_2d(base_a + L::kOffV + vslot * L::kCodes + i * a.P * D, &tmv, 0, row, vfull + 8 * vslot);
+                ++issued_v;
+                at_page += ppt;
+                if (at_page == 32 && t + 1 < t1) {
+                    at_page = 0;
+                    const int next = p0 + (t + 1 - t0) * ppt;
+                    page = page1; ks = ks1; vs = vs1;
+                    page1 = page2;
+                    scales_of(page1, ks1, vs1);
+                    page2 = page_of(next + 64 + lane);
+                    take();
+                }
+            }
+        }
+        if (!ok) *flag = 1;
+    } else if (warp >= kConvWarp) {
+        // ---------------- queries to planes, V codes to f16 ----------------
+        const int cw = warp - kConvWarp;
+        uint32_t tile = 0, segments = 0;
+        for (; ok && at.begin < g1; at.next(w, tab)) {
+            const int nt = at.end_tile(w, g1) - at.first_tile(w, g0);
+            if (nt <= 0) continue;
+            {
+                // Rows two by two (D = 128) or four by four, sixteen bytes a lane: a row's largest value
+                // by shuffles, four loads in flight.
+                constexpr int W = D / 8, PER = 32 / W, ROWS = (PAIR ? 2 : 1) * kRows / kConvWarps, B = 4;
+                const uint16_t* q = static_cast<const uint16_t*>(a.q) + (((size_t)at.b * w.T + at.j * w.tb) * a.Hq + at.h * a.G) * D + lane % W * 8;
+                const int see0 = at.L - at.n + at.j * w.tb, left = min(w.tb, at.n - at.j * w.tb);
+                for (int p = 0; p < ROWS / PER && ok; p += B) {
+                    uint4 x[B];
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {
+                        const int r = cw * ROWS + (p + k) * PER + lane / W, t = token_of(r);
+                        x[k] = make_uint4(0, 0, 0, 0);
+                        if (t < left && see0 + t >= 0) x[k] = *reinterpret_cast<const uint4*>(q + ((size_t)t * a.Hq + (r - t * a.G)) * D);
+                    }
+                    if (p == 0 && segments) ok = warp_wait(qfree, (segments - 1) & 1, lim);
+                    if (!ok) break;
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {
+                        const int r = cw * ROWS + (p + k) * PER + lane / W;
+                        const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m = max(m, max(v[e] & 0x7fffu, v[e] >> 16 & 0x7fffu));
+#pragma unroll
+                        for (int o = W / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        const bool finite = m < 0x7f80u;  // otherwise the row's results are NaN
+                        // largest |q| in [2^e, 2^(e + 1)) goes to [2^7, 2^8)
+                        const int e = max((int)(m >> 7) - 127, -119);
+                        uint2 hi = make_uint2(0, 0), lo = hi;
+                        if (finite) split_planes(x[k], __uint_as_float((uint32_t)(7 - e + 127) << 23), hi, lo);
+                        uint8_t* to = base + (PAIR ? 2 * (r >> 7) * L::kCodes : 0) + code_offset<D>(r & 127, lane % W >> 1) + (lane & 1) * 8;
+                        *reinterpret_cast<uint2*>(to) = hi;
+                        *reinterpret_cast<uint2*>(to + L::kCodes) = lo;
+                        if (lane % W == 0) s_qf[(segments & 1) * 2 * kRows + r] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : NAN;
+                    }
+                }
+                if (!ok) break;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfull);
+                ++segments;
+            }
+            for (int t = 0; t < nt; ++t, ++tile) {
                 const uint32_t vslot = tile % VR, slot = tile & 1;
                 ok = warp_wait(vfull + 8 * vslot, (tile / VR) & 1, lim);
                 if (ok && tile >= 2) ok = warp_wait(wempty + 8 * slot, ((tile >> 1) - 1) & 1, lim);
@@ -454,11 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                 constexpr int C = D / 16;  // 16-code chunks of a key
                 // each warp has 32 keys; their NaN codes are gathered in one word
                 uint32_t nan_keys = 0;
-                constexpr int per = 32 * C / 32;
 #pragma unroll 4
-                for (int i = 0; i < per; ++i) {
-                    const int x = i * 32 + lane, key = (ct >> 5) * 32 + x / C, c = x % C;
-                    uint4 v = *reinterpret_cast<const uint4*>(from + key * D + c * 16);
+                for (int i = 0; i < C; ++i) {
+                    const int x = i * 32 + lane, key = cw * 32 + x / C, c = x % C;
+                    const uint4 v = *reinterpret_cast<const uint4*>(from + key * D + c * 16);
                     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
                     uint32_t bad = 0, o[8];
 #pragma unroll
@@ -481,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     *reinterpret_cast<uint4*>(to + sw128_offset(key, 2 * c + 1 - swap, kTile)) = swap ? h0 : h1;
                 }
                 nan_keys = __reduce_or_sync(0xffffffffu, nan_keys);
-                if (lane == 0) s_nan[slot * 4 + (ct >> 5)] = nan_keys;
+                if (lane == 0) s_nan[slot * 4 + cw] = nan_keys;
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -489,216 +567,196 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     mbar_arrive(wfull + 8 * slot);
                 }
             }
+            if (!ok) break;
         }
         if (!ok) *flag = 1;
     } else {
         // ------------------------------ softmax ------------------------------
-        const int s = warp >> 2, r = tid & 127;
+        const int s = warp >> 2, r = tid & 127, row = PAIR ? tid : r;  // row of the unit
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + kSCol + s * 128, tO = tmem + lane_off + s * kOCol;
-        const int row = PAIR ? s * kRows + r : r;  // of the unit
-        uint32_t tile = 0, mine = 0, done[2] = {0, 0}, segments = 0;  // tiles before the segment, this stream's steps, segments with an O
-        const uint16_t* q = static_cast<const uint16_t*>(a.q);
-        uint16_t* out = static_cast<uint16_t*>(a.out);
-        const int token_in = row / a.G, head_in = row % a.G;
+        const int token_in = token_of(row), head_in = row - token_in * a.G;
+        uint32_t tile = 0, segments = 0, had[2] = {0, 0};  // tiles before the segment: all, the streams'
         for (; ok && at.begin < g1; at.next(w, tab)) {
-            const int t0 = at.first_tile(w, g0), t1 = at.end_tile(w, g1), nt = t1 - t0;
+            const int t0 = at.first_tile(w, g0), nt = at.end_tile(w, g1) - t0;
             const int token = at.j * w.tb + token_in;
             const bool real = token_in < w.tb && token < w.T;
-            const size_t place = (((size_t)at.b * w.T + token) * a.Hq + at.h * a.G + head_in) * D;
+            uint16_t* out = static_cast<uint16_t*>(a.out) + (((size_t)at.b * w.T + token) * a.Hq + at.h * a.G + head_in) * D;
             if (nt <= 0) {
                 // rows that see nothing: zero, by the share that the unit begins in
                 if (at.tiles == 0 && g0 <= at.begin && real && (PAIR || s == 0))
-                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + place + c) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
                 continue;
             }
             const int limit = real && token < at.n ? at.L - at.n + token : -1;  // the last slot that the row sees
-            // ---- q ----
-            uint8_t* planes = base + (PAIR ? 2 * s * L::kCodes : 0);
-            constexpr int C = D / 16;
-            const float qf = write_planes<D>(limit >= 0 ? q + place : nullptr, planes, planes + L::kCodes, r, PAIR || s == 0 ? 0 : C / 2,
-                                             PAIR || s == 1 ? C : C / 2);
-            fence_async_smem();
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(PAIR ? qfull + 8 * s : qfull);
             const bool any = __any_sync(0xffffffffu, limit >= 0);
+            ok = warp_wait(qfull, segments & 1, lim);
+            if (!ok) break;
+            const float qf = s_qf[(segments & 1) * 2 * kRows + row];
             // ---- tiles ----
             float ref = -INFINITY, l = 0.f;
             const int ns = PAIR ? nt : (nt + 1 - s) / 2;
-            for (int i = 0; i < ns; ++i, ++mine) {
+            for (int i = 0; i < ns && ok; ++i) {
                 const int x = PAIR ? i : 2 * i + s;  // tile of the segment
-                const uint32_t n_tile = tile + x, sslot = n_tile % kScaleRing;
-                ok = warp_wait(sfull + 8 * s, mine & 1, lim);
-                if (ok) ok = warp_wait(scfull + 8 * sslot, (n_tile / kScaleRing) & 1, lim);
+                const uint32_t n_tile = tile + x, n_mine = had[s] + i;
+                ok = warp_wait(scfull + 8 * (n_tile % kScaleRing), (n_tile / kScaleRing) & 1, lim);
+                ok = ok && warp_wait(sfull + 8 * s, n_mine & 1, lim);
                 if (!ok) break;
+                if (!any) {
+                    if (lane == 0) {
+                        mbar_arrive(pfull + 16 * s);
+                        mbar_arrive(pfull + 16 * s + 8);
+                    }
+                    continue;
+                }
                 fence_after_sync();
-                if (any) {
-                    const float4* sc = s_scale + sslot * kGroups;
-                    const int k0 = (t0 + x) * kTile;
-                    const bool plain = __all_sync(0xffffffffu, k0 + kTile - 1 <= limit);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        tmem_ld32(tS + 32 * c, v);
-                        tmem_wait_ld();
-                        if (!plain) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = k0 + 32 * c + e <= limit ? v[e] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                m0 = max3(m0, v[16 * g + e], v[16 * g + e + 1]);
-                                m1 = max3(m1, v[16 * g + e + 2], v[16 * g + e + 3]);
-                            }
-                            const float4 f = sc[2 * c + g];
-                            top = fmaxf(top, fmaf(fmaxf(m0, m1), f.x * qf, f.y));  // (-inf times an absent page's 0 is NaN: left out)
-                        }
-                    }
-                    float corr = 1.f;
-                    bool move = false;
-                    if (top > -INFINITY && !(top <= ref + kMove)) {
-                        move = ref > -INFINITY;
-                        corr = move ? exp2_approx(ref - top) : 0.f;
-                        ref = top;
-                        l *= corr;
-                    }
-                    if (__any_sync(0xffffffffu, move)) {
-                        // O holds this stream's PV of the step before: its commit came with the scores
+                const float4* sc = s_scale + (n_tile % kScaleRing) * kGroups;
+                // the last key of the tile that the row sees (rows that see nothing: what they sum up is not used)
+                const int seen = limit < 0 ? kTile : limit - (t0 + x) * kTile;
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            tmem_ld32(tO + 32 * c, o);
-                            tmem_wait_ld();
+                for (int c = 0; c < 4; ++c) {
+                    float v[2][16];
+                    tmem_ld16(tS + 32 * c, v[0]);
+                    tmem_ld16(tS + 32 * c + 16, v[1]);
+                    const float4 f0 = sc[2 * c], f1 = sc[2 * c + 1];
+                    const float kc0 = factor(f0.x, qf), kc1 = factor(f1.x, qf);
+                    tmem_wait_ld();
+                    if (!__all_sync(0xffffffffu, seen >= 32 * c + 31)) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= move ? corr : 1.f;
-                            tmem_st32(tO + 32 * c, o);
+                        for (int e = 0; e < 32; ++e) v[e >> 4][e & 15] = 32 * c + e <= seen ? v[e >> 4][e & 15] : -INFINITY;
+                    }
+                    const float top = fmaxf(fmaf(max16(v[0]), kc0, f0.y), fmaf(max16(v[1]), kc1, f1.y));
+                    const bool up = top > -INFINITY && !(top <= ref + kMove);
+                    if (__any_sync(0xffffffffu, up)) {
+                        // The reference moves to a whole number, so that what is scaled keeps its bits.
+                        const float to = up ? ceilf(top) : ref;
+                        const float corr = up && ref > -INFINITY ? exp2_approx(ref - to) : 1.f;
+                        if (__any_sync(0xffffffffu, corr != 1.f)) {
+                            // all products so far, then the weights of this half that are not handed over yet
+                            if (c >= 2) ok = warp_wait(odone + 16 * s, n_mine & 1, lim);
+                            if (!ok) break;
+                            fence_after_sync();
+#pragma unroll 1
+                            for (int k = 0; k < D / 16; ++k) {
+                                float o[16];
+                                if (i == 0 && c < 2) break;  // O is not there yet
+                                tmem_ld16(tO + 16 * k, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] *= corr;
+                                tmem_st16(tO + 16 * k, o);
+                            }
+                            if (c & 1) {
+                                float p[16];
+                                tmem_ld16(tS + 16 * (c - 1), p);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) p[e] = __uint_as_float(scale_f16x2(__float_as_uint(p[e]), corr));
+                                tmem_st16(tS + 16 * (c - 1), p);
+                            }
+                            l *= corr;
                         }
+                        ref = to;
                     }
                     const float shift = kLift - (ref == -INFINITY ? 0.f : ref);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        tmem_ld32(tS + 32 * c, v);
-                        tmem_wait_ld();
-                        uint32_t p[16];
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float4 f = sc[2 * c + g];
-                            const float kc = f.x * qf, off = f.y + shift;
-                            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                float x0, x1;
-                                fma2(x0, x1, v[16 * g + e], v[16 * g + e + 1], kc, off);
-                                if (!plain) {
-                                    x0 = k0 + 32 * c + 16 * g + e <= limit ? x0 : -INFINITY;
-                                    x1 = k0 + 32 * c + 16 * g + e + 1 <= limit ? x1 : -INFINITY;
-                                }
-                                x0 = exp2_approx(x0);
-                                x1 = exp2_approx(x1);
-                                add2(s0, s1, x0, x1);
-                                p[8 * g + e / 2] = pack_f16(x0, x1);
-                            }
-                            l = fmaf(s0 + s1, f.z, l);
+                    uint32_t p[16];
+                    row_weights(v[0], kc0, f0.y + shift, f0.z, p, l);
+                    row_weights(v[1], kc1, f1.y + shift, f1.z, p + 8, l);
+                    tmem_st16u(tS + 16 * c, p);
+                    if (c & 1) {
+                        const int h = c >> 1;
+                        tmem_wait_st();
+                        // keys whose V has a NaN code: rows that see one are NaN
+                        const uint32_t slot = n_tile & 1;
+                        if (!h) ok = warp_wait(wfull + 8 * slot, (n_tile >> 1) & 1, lim);
+                        if (!ok) break;
+                        const uint2 bad = *reinterpret_cast<const uint2*>(s_nan + 4 * slot + 2 * h);
+                        if (bad.x | bad.y) {
+                            const int see = seen - kHalf * h;
+                            const uint32_t m0 = see < 0 ? 0u : see >= 31 ? ~0u : (2u << see) - 1u;
+                            const uint32_t m1 = see < 32 ? 0u : see >= 63 ? ~0u : (2u << (see - 32)) - 1u;
+                            if ((bad.x & m0) | (bad.y & m1)) l = NAN;
                         }
-                        tmem_st16u(tS + 16 * c, p);
-                    }
-                    tmem_wait_st();
-                    // keys whose V has a NaN code: rows that see one are NaN
-                    const uint32_t slot = n_tile & 1;
-                    ok = warp_wait(wfull + 8 * slot, (n_tile >> 1) & 1, lim);
-                    if (!ok) break;
-                    const uint4 bad = *reinterpret_cast<const uint4*>(s_nan + 4 * slot);
-                    if (bad.x | bad.y | bad.z | bad.w) {
-                        const uint32_t word[4] = {bad.x, bad.y, bad.z, bad.w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int sees = limit - (k0 + 32 * c) + 1;  // keys of the word that the row sees
-                            const uint32_t m = sees <= 0 ? 0u : sees >= 32 ? ~0u : (1u << sees) - 1u;
-                            if (word[c] & m) l = NAN;
-                        }
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pfull + 8 * (2 * s + h));
                     }
                 }
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pfull + 8 * s);
             }
             if (!ok) break;
             tile += nt;
+            had[0] += PAIR ? nt : (nt + 1) / 2;
+            had[1] += PAIR ? nt : nt / 2;
             // ---- results ----
             const bool whole = nt == at.tiles;
-            float c0 = 1.f, c1 = 0.f, m_out = ref, l_out = l;  // factors of this stream's O and, split, of both streams'
-            bool has1 = false;
-            if constexpr (PAIR) {
-                ok = warp_wait(odone + 8 * s, done[s] & 1, lim);
-                ++done[s];
-            } else {
-                has1 = nt > 1;
+            const bool split = !PAIR && nt > 1;  // both streams have an O
+            if (limit < 0) { ref = -INFINITY; l = 0.f; }
+            float m_out = ref, l_out = l, f0 = 1.f, f1 = 0.f;  // f: factors of this stream's O, or of both streams'
+            if constexpr (!PAIR) {
+                float2* s_x = reinterpret_cast<float2*>(base + L::kOffX);
                 s_x[s * kRows + r] = make_float2(ref, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(xfull);
                 ok = warp_wait(xfull, segments & 1, lim);
-                if (ok) ok = warp_wait(odone, done[0] & 1, lim);
-                ++done[0];
-                if (ok && has1) ok = warp_wait(odone + 8, done[1] & 1, lim);
-                if (has1) ++done[1];
+                if (!ok) break;
                 const float2 A = s_x[r], B = s_x[kRows + r];
                 m_out = fmaxf(A.x, B.x);
                 const float z = m_out == -INFINITY ? 0.f : m_out;
-                c0 = exp2f(A.x - z);
-                c1 = exp2f(B.x - z);
-                l_out = A.y * c0 + B.y * c1;
+                f0 = exp2f(A.x - z);
+                f1 = exp2f(B.x - z);
+                l_out = A.y * f0 + B.y * f1;
             }
+            // (a commit comes with all products before it)
+            if (PAIR || s == 0 || split) ok = warp_wait(odone + 8 * (2 * s + 1), (had[s] - 1) & 1, lim);
+            if (!PAIR && ok && (s == 1 || split)) ok = warp_wait(odone + 8 * (2 * (s ^ 1) + 1), (had[s ^ 1] - 1) & 1, lim);
             if (!ok) break;
             fence_after_sync();
-            if (any || !PAIR) {
-                const float inv = l_out == 0.f ? 0.f : 1.f / l_out;
-                const float f0 = whole ? c0 * inv : c0, f1 = whole ? c1 * inv : c1;
-                const size_t part = ((size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * a.rows + row);
-                const bool zero = whole && l_out == 0.f;
-                constexpr int CB = PAIR ? 0 : 1;  // split: each stream writes half of the columns
+            const size_t part = (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * a.rows + row;
+            const bool zero = whole && l_out == 0.f;
+            if (whole) {
+                const float inv = zero ? 0.f : 1.f / l_out;
+                f0 *= inv;
+                f1 *= inv;
+            } else if (real && (PAIR || s == 0)) {
+                a.part_ml[part] = make_float2(m_out, l_out);
+            }
+            constexpr int WC = D / (PAIR ? 1 : 2);  // columns of a warpgroup
+            const int col0 = PAIR ? 0 : s * WC;
+            const uint32_t from = tmem + lane_off + (PAIR ? s * kOCol : 0) + col0;
+            const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+            if (any) {
 #pragma unroll 1
-                for (int c = 0; c < (PAIR ? D / 32 : D / 64); ++c) {
-                    const int col = 32 * c + (CB ? s * (D / 2) : 0);
+                for (int c = 0; c < WC; c += 32) {
                     float o[32];
-                    if constexpr (PAIR) {
-                        tmem_ld32(tO + col, o);
+                    tmem_ld32(from + c, o);
+                    if (split) {
+                        float o1[32];
+                        tmem_ld32(from + kOCol + c, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+                    } else {
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] *= f0;
-                    } else {
-                        float o1[32];
-                        tmem_ld32(tmem + lane_off + col, o);
-                        if (has1) tmem_ld32(tmem + lane_off + kOCol + col, o1);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + (has1 ? o1[e] * f1 : 0.f);
                     }
                     if (!real) continue;
                     if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(out + place + col + e) =
-                                zero ? make_uint4(0, 0, 0, 0)
-                                     : make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
-                                                  pack_bf16(o[e + 6], o[e + 7]));
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t b[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) b[k] = zero ? 0u : pack_bf16(o[e + 2 * k], o[e + 2 * k + 1]);
+                            store32(out + col0 + c + e, b, aligned);
+                        }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(a.part_o + part * D + col + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(a.part_o + part * D + col0 + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
-                if (!whole && real && (PAIR || s == 0)) a.part_ml[part] = make_float2(m_out, l_out);
-            } else if (real) {  // a warp without rows that see anything
-                if (whole) {
-                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + place + c) = make_uint4(0, 0, 0, 0);
-                } else {
-                    a.part_ml[(size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * a.rows + row] = make_float2(-INFINITY, 0.f);
-                }
+            } else if (real && whole) {  // a warp without rows that see anything
+                for (int c = 0; c < WC; c += 8) *reinterpret_cast<uint4*>(out + col0 + c) = make_uint4(0, 0, 0, 0);
             }
             if constexpr (!PAIR) {
                 // the other stream has read both O and the exchanged sums
@@ -716,16 +774,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
     if (bad) {
         // Gave up: let everything this CTA started complete before its tensor memory is freed
         // and it leaves (default-limit waits), and mark what it owns.
-        if (warp == kMmaWarp) {
-            commit_warp(drain);
-            warp_wait(drain, 0, kDrainCycles);
+        if (warp >= kMmaWarp && warp < kTmaWarp) {
+            commit_warp(drain + 8 * (warp - kMmaWarp));
+            warp_wait(drain + 8 * (warp - kMmaWarp), 0, kDrainCycles);
         }
         if (warp == kTmaWarp) {
             for (int u = max(0, issued_k - KR); u < issued_k; ++u) warp_wait(kfull + 8 * (u % KR), (uint32_t)(u / KR) & 1, kDrainCycles);
             for (int u = max(0, issued_v - VR); u < issued_v; ++u) warp_wait(vfull + 8 * (u % VR), (uint32_t)(u / VR) & 1, kDrainCycles);
         }
         if (tid == 0) atomicExch(&g_wait_gave_up, 1);
-        for (chunks::Cursor c = start; c.begin < g1; c.next(w, tab)) {
+        for (chunks::Cursor c = first_unit(); c.begin < g1; c.next(w, tab)) {
             const int t0 = c.first_tile(w, g0), nt = c.end_tile(w, g1) - t0;
             if (nt <= 0) continue;
             for (int i = tid; i < a.rows; i += kThreads) {
