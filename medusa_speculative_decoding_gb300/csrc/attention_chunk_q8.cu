@@ -115,8 +115,8 @@ struct USmem {
     static constexpr int kOffX = kOffQf + 2 * 2 * kRows * 4;  // float2 [2][128]: the streams' references and sums (split)
     static constexpr int kOffCursor = kOffX + (PAIR ? 0 : 2 * kRows * 8);
     static constexpr int kOffBar = kOffCursor + 32;
-    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull [2], pfull odone [2][2], qfull qfree xfull xdone drain [2], scfull
-    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 10 + 6 + kScaleRing;
+    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull [2], pfull odone [2][2], qfull qfree xfull xdone stagger drain [2], scfull
+    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 10 + 7 + kScaleRing;
     static constexpr int kOffMisc = kOffBar + kBars * 8;  // TMEM slot, flag
     static constexpr int kOffTables = kOffMisc + 8;
     static constexpr int bytes(int B) { return kOffTables + chunks::table_bytes(B) + 1024; }  // + alignment
@@ -168,27 +168,14 @@ __device__ __forceinline__ void mma_f16_ta_warp(uint32_t d_tmem, uint32_t a_tmem
         : "memory");
 }
 
-// One try that suspends the thread until the phase completes, or for about a tenth of a
-// millisecond: a warp that polls takes issue slots from those that work (without the hint a
-// wait came back at once, and waiting took half of all instructions).
-__device__ __forceinline__ bool mbar_try_long(uint32_t mbar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(mbar), "r"(parity), "r"(100000u)
-        : "memory");
-    return done != 0;
-}
-// A wait by a whole warp: true if the phase completed for every lane.  (Limits that are shorter
-// than a suspended try, set to make waits run out, are kept by polling.)
+// A wait by a whole warp: true if the phase completed for every lane.  (A suspended try comes back
+// late: limits that are shorter than that, set to make waits run out, are kept by polling.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t lim) {
     bool done = umma::mbar_test(bar, parity);
     if (!done) {
-        const uint32_t t0 = (uint32_t)clock();
-        do done = lim < 65536 ? umma::mbar_test(bar, parity) : mbar_try_long(bar, parity);
-        while (!done && (uint32_t)clock() - t0 <= lim);
+        const uint32_t t0 = (uint32_t)clock64();
+        do done = lim < 65536 ? umma::mbar_test(bar, parity) : umma::mbar_try(bar, parity);
+        while (!done && (uint32_t)clock64() - t0 <= lim);
     }
     return __all_sync(0xffffffffu, done);
 }
@@ -267,15 +254,6 @@ __device__ __forceinline__ void row_weights(const float (&v)[16], float kc, floa
     l = fmaf(s0 + s1, per_vs, l);
 }
 
-// a pair of f16 times a power of two
-__device__ __forceinline__ uint32_t scale_f16x2(uint32_t x, float f) {
-    uint32_t r;
-    asm("{\n.reg .f16 a, b;\n.reg .f32 u, v;\nmov.b32 {a, b}, %1;\ncvt.f32.f16 u, a;\ncvt.f32.f16 v, b;\nmul.f32 u, u, %2;\nmul.f32 v, v, %2;\n"
-        "cvt.rn.f16x2.f32 %0, v, u;\n}"
-        : "=r"(r) : "r"(x), "f"(f));
-    return r;
-}
-
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const __grid_constant__ CUtensorMap tmk,
                                                                          const __grid_constant__ CUtensorMap tmv,
@@ -291,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
     const uint32_t bar = base_a + L::kOffBar;
     const uint32_t kfull = bar, kempty = kfull + 8 * KR, vfull = kempty + 8 * KR, vempty = vfull + 8 * VR, wfull = vempty + 8 * VR,
                    wempty = wfull + 16, sfull = wempty + 16, pfull = sfull + 16, odone = pfull + 32, qfull = odone + 32, qfree = qfull + 8,
-                   xfull = qfree + 8, xdone = xfull + 8, drain = xdone + 8, scfull = drain + 16;
+                   xfull = qfree + 8, xdone = xfull + 8, stagger = xdone + 8, drain = stagger + 8, scfull = drain + 16;
     float4* s_scale = reinterpret_cast<float4*>(base + L::kOffScale);
     uint32_t* s_nan = reinterpret_cast<uint32_t*>(base + L::kOffNan);
     float* s_qf = reinterpret_cast<float*>(base + L::kOffQf);
@@ -382,6 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             };
             ok = warp_wait(qfull, segments & 1, lim);
             fence_after_sync();
+            // The streams half a tile apart: one's weights are formed while the other's products run.
+            if (PAIR && s == 1 && ok) ok = warp_wait(stagger, segments & 1, lim);
             if (ns) ok = ok && issue_s(0);
             else if (lane == 0) mbar_arrive(qfree);
             for (int i = 0; i < ns && ok; ++i) {
@@ -396,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     for (int k = 0; k < kHalf / 16; ++k)
                         mma_f16_ta_warp(tO, tS + 32 * h + 8 * k, v + (((4 * h + k) * 2048) >> 4), idesc_pv, (i > 0 || h > 0 || k > 0) ? 1u : 0u);
                     commit_warp(odone + 8 * (2 * s + h));
+                    if (PAIR && s == 0 && i == 0 && h == 0 && lane == 0) mbar_arrive(stagger);
                 }
                 if (!ok) break;
                 commit_warp(wempty + 8 * slot);
@@ -483,20 +464,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             if (nt <= 0) continue;
             {
                 // Rows two by two (D = 128) or four by four, sixteen bytes a lane: a row's largest value
-                // by shuffles, four loads in flight.
-                constexpr int W = D / 8, PER = 32 / W, ROWS = (PAIR ? 2 : 1) * kRows / kConvWarps, B = 4;
+                // by shuffles; the next eight loads are on their way meanwhile.
+                constexpr int W = D / 8, PER = 32 / W, ROWS = (PAIR ? 2 : 1) * kRows / kConvWarps, PASSES = ROWS / PER, B = PASSES < 8 ? PASSES : 8;
                 const uint16_t* q = static_cast<const uint16_t*>(a.q) + (((size_t)at.b * w.T + at.j * w.tb) * a.Hq + at.h * a.G) * D + lane % W * 8;
                 const int see0 = at.L - at.n + at.j * w.tb, left = min(w.tb, at.n - at.j * w.tb);
-                for (int p = 0; p < ROWS / PER && ok; p += B) {
-                    uint4 x[B];
+                auto load = [&](int p, uint4 (&x)[B]) {
 #pragma unroll
                     for (int k = 0; k < B; ++k) {
                         const int r = cw * ROWS + (p + k) * PER + lane / W, t = token_of(r);
                         x[k] = make_uint4(0, 0, 0, 0);
                         if (t < left && see0 + t >= 0) x[k] = *reinterpret_cast<const uint4*>(q + ((size_t)t * a.Hq + (r - t * a.G)) * D);
                     }
-                    if (p == 0 && segments) ok = warp_wait(qfree, (segments - 1) & 1, lim);
-                    if (!ok) break;
+                };
+                uint4 x[B];
+                load(0, x);
+                if (segments) ok = warp_wait(qfree, (segments - 1) & 1, lim);
+                if (!ok) break;
+#pragma unroll 1
+                for (int p = 0; p < PASSES; p += B) {
+                    uint4 ahead[B];
+                    if (p + B < PASSES) load(p + B, ahead);
 #pragma unroll
                     for (int k = 0; k < B; ++k) {
                         const int r = cw * ROWS + (p + k) * PER + lane / W;
@@ -509,19 +496,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                         const bool finite = m < 0x7f80u;  // otherwise the row's results are NaN
                         // largest |q| in [2^e, 2^(e + 1)) goes to [2^7, 2^8)
                         const int e = max((int)(m >> 7) - 127, -119);
-                        uint2 hi = make_uint2(0, 0), lo = hi;
-                        if (finite) split_planes(x[k], __uint_as_float((uint32_t)(7 - e + 127) << 23), hi, lo);
+                        uint2 hi, lo;
+                        split_planes(finite ? x[k] : make_uint4(0, 0, 0, 0), __uint_as_float((uint32_t)(7 - e + 127) << 23), hi, lo);
                         uint8_t* to = base + (PAIR ? 2 * (r >> 7) * L::kCodes : 0) + code_offset<D>(r & 127, lane % W >> 1) + (lane & 1) * 8;
                         *reinterpret_cast<uint2*>(to) = hi;
                         *reinterpret_cast<uint2*>(to + L::kCodes) = lo;
                         if (lane % W == 0) s_qf[(segments & 1) * 2 * kRows + r] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : NAN;
                     }
+#pragma unroll
+                    for (int k = 0; k < B; ++k) x[k] = ahead[k];
                 }
                 if (!ok) break;
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(qfull);
                 ++segments;
+                // the next unit's queries into L2: 128 bytes a lane
+                chunks::Cursor n = at;
+                n.next(w, tab);
+                if (n.begin < g1) {
+                    const int rows = (PAIR ? 2 : 1) * kRows, tokens = min(w.tb, n.n - n.j * w.tb);
+                    for (int i = cw * 32 + lane; i < rows * D / 64; i += kConvWarps * 32) {
+                        const int r = i / (D / 64), t = token_of(r);
+                        if (t < tokens)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t*>(a.q) +
+                                (((size_t)n.b * w.T + n.j * w.tb + t) * a.Hq + n.h * a.G + r - t * a.G) * D + i % (D / 64) * 64));
+                    }
+                }
             }
             for (int t = 0; t < nt; ++t, ++tile) {
                 const uint32_t vslot = tile % VR, slot = tile & 1;
@@ -531,34 +532,47 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                 const uint8_t* from = base + L::kOffV + vslot * L::kCodes;
                 uint8_t* to = base + L::kOffV16 + slot * L::kCodes * 2;
                 constexpr int C = D / 16;  // 16-code chunks of a key
-                // each warp has 32 keys; their NaN codes are gathered in one word
-                uint32_t nan_keys = 0;
-#pragma unroll 4
-                for (int i = 0; i < C; ++i) {
-                    const int x = i * 32 + lane, key = cw * 32 + x / C, c = x % C;
-                    const uint4 v = *reinterpret_cast<const uint4*>(from + key * D + c * 16);
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t bad = 0, o[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) bad |= (in[e] & 0x7f7f7f7fu) + 0x01010101u;
-                    if (bad & 0x80808080u) {
-                        nan_keys |= 1u << (key & 31);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t n = ((in[e] & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u;
-                            codes_to_f16(in[e] & ~(n * 0xffu), o[2 * e], o[2 * e + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) codes_to_f16(in[e], o[2 * e], o[2 * e + 1]);
-                    }
+                // each warp has 32 keys
+                uint32_t bad = 0;
+                auto place = [&](int key, int c, const uint32_t (&o)[8]) {
                     // (the two halves in an order that spreads a quarter warp over all banks)
                     const uint4 h0 = make_uint4(o[0], o[1], o[2], o[3]), h1 = make_uint4(o[4], o[5], o[6], o[7]);
                     const int swap = (c >> 2) & 1;
                     *reinterpret_cast<uint4*>(to + sw128_offset(key, 2 * c + swap, kTile)) = swap ? h1 : h0;
                     *reinterpret_cast<uint4*>(to + sw128_offset(key, 2 * c + 1 - swap, kTile)) = swap ? h0 : h1;
+                };
+#pragma unroll 4
+                for (int i = 0; i < C; ++i) {
+                    const int x = i * 32 + lane, key = cw * 32 + x / C, c = x % C;
+                    const uint4 v = *reinterpret_cast<const uint4*>(from + key * D + c * 16);
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        bad |= (in[e] & 0x7f7f7f7fu) + 0x01010101u;
+                        codes_to_f16(in[e], o[2 * e], o[2 * e + 1]);
+                    }
+                    place(key, c, o);
                 }
-                nan_keys = __reduce_or_sync(0xffffffffu, nan_keys);
+                uint32_t nan_keys = 0;
+                if (__any_sync(0xffffffffu, bad & 0x80808080u)) {  // once more, with zeros for NaN codes
+#pragma unroll 1
+                    for (int i = 0; i < C; ++i) {
+                        const int x = i * 32 + lane, key = cw * 32 + x / C, c = x % C;
+                        const uint4 v = *reinterpret_cast<const uint4*>(from + key * D + c * 16);
+                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t o[8], any = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t n = ((in[e] & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u;
+                            any |= n;
+                            codes_to_f16(in[e] & ~(n * 0xffu), o[2 * e], o[2 * e + 1]);
+                        }
+                        if (any) nan_keys |= 1u << (key & 31);
+                        place(key, c, o);
+                    }
+                    nan_keys = __reduce_or_sync(0xffffffffu, nan_keys);
+                }
                 if (lane == 0) s_nan[slot * 4 + cw] = nan_keys;
                 fence_async_smem();
                 __syncwarp();
@@ -600,7 +614,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                 const int x = PAIR ? i : 2 * i + s;  // tile of the segment
                 const uint32_t n_tile = tile + x, n_mine = had[s] + i;
                 ok = warp_wait(scfull + 8 * (n_tile % kScaleRing), (n_tile / kScaleRing) & 1, lim);
-                ok = ok && warp_wait(sfull + 8 * s, n_mine & 1, lim);
+                if (!ok) break;
+                const float4* sc = s_scale + (n_tile % kScaleRing) * kGroups;
+                float kc[4], off[4], per_vs[4];
+                auto scales = [&](int h) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float4 f = sc[4 * h + g];
+                        kc[g] = factor(f.x, qf);
+                        off[g] = f.y;
+                        per_vs[g] = f.z;
+                    }
+                };
+                scales(0);
+                ok = warp_wait(sfull + 8 * s, n_mine & 1, lim);
                 if (!ok) break;
                 if (!any) {
                     if (lane == 0) {
@@ -610,77 +637,80 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     continue;
                 }
                 fence_after_sync();
-                const float4* sc = s_scale + (n_tile % kScaleRing) * kGroups;
                 // the last key of the tile that the row sees (rows that see nothing: what they sum up is not used)
                 const int seen = limit < 0 ? kTile : limit - (t0 + x) * kTile;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float v[2][16];
-                    tmem_ld16(tS + 32 * c, v[0]);
-                    tmem_ld16(tS + 32 * c + 16, v[1]);
-                    const float4 f0 = sc[2 * c], f1 = sc[2 * c + 1];
-                    const float kc0 = factor(f0.x, qf), kc1 = factor(f1.x, qf);
-                    tmem_wait_ld();
-                    if (!__all_sync(0xffffffffu, seen >= 32 * c + 31)) {
+                for (int h = 0; h < 2; ++h) {
+                    float v[4][16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e >> 4][e & 15] = 32 * c + e <= seen ? v[e >> 4][e & 15] : -INFINITY;
+                    for (int g = 0; g < 4; ++g) tmem_ld16(tS + kHalf * h + 16 * g, v[g]);
+                    const int see = seen - kHalf * h;
+                    const bool plain = __all_sync(0xffffffffu, see >= kHalf - 1);
+                    tmem_wait_ld();
+                    if (!plain) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (!__all_sync(0xffffffffu, see >= 16 * g + 15)) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) v[g][e] = 16 * g + e <= see ? v[g][e] : -INFINITY;
+                            }
                     }
-                    const float top = fmaxf(fmaf(max16(v[0]), kc0, f0.y), fmaf(max16(v[1]), kc1, f1.y));
+                    // Weights on the reference so far; formed anew where it turns out that it has to move.
+                    float sum = 0.f;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) top = fmaxf(top, fmaf(max16(v[g]), kc[g], off[g]));
                     const bool up = top > -INFINITY && !(top <= ref + kMove);
                     if (__any_sync(0xffffffffu, up)) {
                         // The reference moves to a whole number, so that what is scaled keeps its bits.
                         const float to = up ? ceilf(top) : ref;
                         const float corr = up && ref > -INFINITY ? exp2_approx(ref - to) : 1.f;
-                        if (__any_sync(0xffffffffu, corr != 1.f)) {
-                            // all products so far, then the weights of this half that are not handed over yet
-                            if (c >= 2) ok = warp_wait(odone + 16 * s, n_mine & 1, lim);
+                        ref = to;
+                        l *= corr;
+                        if (__any_sync(0xffffffffu, corr != 1.f) && (i || h)) {  // (else there is no O yet)
+                            if (h) ok = warp_wait(odone + 16 * s, n_mine & 1, lim);  // the products of the half before
                             if (!ok) break;
                             fence_after_sync();
 #pragma unroll 1
                             for (int k = 0; k < D / 16; ++k) {
                                 float o[16];
-                                if (i == 0 && c < 2) break;  // O is not there yet
                                 tmem_ld16(tO + 16 * k, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) o[e] *= corr;
                                 tmem_st16(tO + 16 * k, o);
                             }
-                            if (c & 1) {
-                                float p[16];
-                                tmem_ld16(tS + 16 * (c - 1), p);
-                                tmem_wait_ld();
+                        }
+                    }
+                    {
+                        const float shift = kLift - (ref == -INFINITY ? 0.f : ref);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) p[e] = __uint_as_float(scale_f16x2(__float_as_uint(p[e]), corr));
-                                tmem_st16(tS + 16 * (c - 1), p);
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int g = 2 * c + k;
+                                row_weights(v[g], kc[g], off[g] + shift, per_vs[g], p + 8 * k, sum);
                             }
-                            l *= corr;
+                            tmem_st16u(tS + 32 * h + 16 * c, p);
                         }
-                        ref = to;
                     }
-                    const float shift = kLift - (ref == -INFINITY ? 0.f : ref);
-                    uint32_t p[16];
-                    row_weights(v[0], kc0, f0.y + shift, f0.z, p, l);
-                    row_weights(v[1], kc1, f1.y + shift, f1.z, p + 8, l);
-                    tmem_st16u(tS + 16 * c, p);
-                    if (c & 1) {
-                        const int h = c >> 1;
-                        tmem_wait_st();
-                        // keys whose V has a NaN code: rows that see one are NaN
-                        const uint32_t slot = n_tile & 1;
-                        if (!h) ok = warp_wait(wfull + 8 * slot, (n_tile >> 1) & 1, lim);
-                        if (!ok) break;
-                        const uint2 bad = *reinterpret_cast<const uint2*>(s_nan + 4 * slot + 2 * h);
-                        if (bad.x | bad.y) {
-                            const int see = seen - kHalf * h;
-                            const uint32_t m0 = see < 0 ? 0u : see >= 31 ? ~0u : (2u << see) - 1u;
-                            const uint32_t m1 = see < 32 ? 0u : see >= 63 ? ~0u : (2u << (see - 32)) - 1u;
-                            if ((bad.x & m0) | (bad.y & m1)) l = NAN;
-                        }
-                        fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(pfull + 8 * (2 * s + h));
+                    l += sum;
+                    tmem_wait_st();
+                    // keys whose V has a NaN code: rows that see one are NaN
+                    const uint32_t slot = n_tile & 1;
+                    if (ok && !h) ok = warp_wait(wfull + 8 * slot, (n_tile >> 1) & 1, lim);
+                    if (!ok) break;
+                    const uint2 bad = *reinterpret_cast<const uint2*>(s_nan + 4 * slot + 2 * h);
+                    if (bad.x | bad.y) {
+                        const uint32_t m0 = see < 0 ? 0u : see >= 31 ? ~0u : (2u << see) - 1u;
+                        const uint32_t m1 = see < 32 ? 0u : see >= 63 ? ~0u : (2u << (see - 32)) - 1u;
+                        if ((bad.x & m0) | (bad.y & m1)) l = NAN;
                     }
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pfull + 8 * (2 * s + h));
+                    if (!h) scales(1);
                 }
             }
             if (!ok) break;
