@@ -57,20 +57,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_rope_q8_kernel
     __shared__ float s_top[2][THREADS / 32];
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.z, tid = threadIdx.x, n_freq = a.f.n;
+    const int b = blockIdx.z, tid = threadIdx.x;
     const int L = a.kv_len[b], last = a.last ? a.last[b] : a.R - 1;
     const int n = last + 1, P = a.P;
     const int x_block = blockIdx.x;
-    const rope::Item at = rope::item_at(a.f, tid % C16);  // THREADS is a multiple of C16: the same for all items of a thread
-
-    // position of the table's first row, and its rows first .. first + count - 1
-    auto fill_table = [&](int pos0, int first, int count) {
-        for (int i = tid; i < n_freq * (THREADS / n_freq); i += THREADS) {
-            const uint64_t turn = rope::turn(a.f.inv_freq[i % n_freq]);
-            for (int r = first + i / n_freq; r < first + count; r += THREADS / n_freq)
-                s_cs[r * n_freq + i % n_freq] = rope::cos_sin(turn, (int)((uint32_t)pos0 + (uint32_t)r));
-        }
-    };
+    const rope::Item at = rope::item_at(a.f, tid % C16, D);  // THREADS is a multiple of C16: the same for all items of a thread
 
     if (x_block > 2 * a.groups) {  // queries: rows blockIdx.y * P on, zero behind `last`
         const int t0 = blockIdx.y * P, rows = min(P, a.T - t0), real = min(rows, min(max(n, 0), a.T) - t0);
@@ -91,7 +82,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_rope_q8_kernel
         };
         Raw x[ITEMS][2];
         load(h0, x);
-        fill_table(L + t0, 0, real);
+        rope::fill_table(a.f, s_cs, 0, real, [&](int r) { return (int)((uint32_t)L + (uint32_t)(t0 + r)); });
         __syncthreads();
 #pragma unroll 1
         for (int h = h0; h < h1; ++h) {
@@ -105,7 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_rope_q8_kernel
                 if (r < real) {
                     x[k][0].unpack(u);
                     x[k][1].unpack(v);
-                    if (at.freq >= 0) rope::rotate(u, v, s_cs + r * n_freq + at.freq, a.f.interleaved);
+                    if (at.turns >= 0) rope::rotate(a.f, u, v, reinterpret_cast<const float4*>(s_cs + r * a.f.n) + at.turns);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) u[e] = v[e] = 0.f;
@@ -131,8 +122,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_rope_q8_kernel
     const int kv = x_block >= a.groups;
     const int first = (w0 + (int)blockIdx.y) * P - L;  // new row that the page's slot 0 takes
     const size_t row_stride = (size_t)a.Hkv * D;
-    // V is not rotated: its pieces are neighbours
-    const int e0 = kv ? tid % C16 * 16 : at.first, e1 = kv ? e0 + 8 : at.second;
+    const int e0 = kv ? tid % C16 * 8 : at.first, e1 = kv ? D / 2 + e0 : at.second;
     int row[ITEMS];  // the row that each of this thread's items comes from, -1: none
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
@@ -188,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_rope_q8_kernel
     if (!ok || !rows_cta) return;
     if (!kv) {
         const int from = max(0, -first);
-        fill_table(L + first, from, min(P, n - first) - from);  // slot s holds position L + first + s
+        rope::fill_table(a.f, s_cs, from, min(P, n - first) - from, [&](int slot) { return L + first + slot; });
     }
 
     const size_t page = table[w0 + blockIdx.y];
@@ -245,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_rope_q8_kernel
                 } else {
                     x[k][0].unpack(y[0]);
                     x[k][1].unpack(y[1]);
-                    if (!kv && at.freq >= 0) rope::rotate(y[0], y[1], s_cs + slot * n_freq + at.freq, a.f.interleaved);
+                    if (!kv && at.turns >= 0) rope::rotate(a.f, y[0], y[1], reinterpret_cast<const float4*>(s_cs + slot * a.f.n) + at.turns);
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {

@@ -17,7 +17,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 16;  // rows of a block
-constexpr int kBatch = 4;     // items of a thread with their loads in flight
+
+// items of a thread with their loads in flight: 128 bytes
+template <typename T> constexpr int kBatch = 8 / sizeof(T);
 
 struct RopeArgs {
     const void* in[2];  // q, k
@@ -25,52 +27,56 @@ struct RopeArgs {
     const int32_t *kv_len, *depth;
     rope::Freqs f;
     int T, D, heads[2], rows, per_block;  // rows, heads of a block
+    uint32_t items_magic, heads_magic;    // 2^32 / items of a head, / heads of a block, rounded up
 };
 
+// i / d with d's magic, for i * d < 2^32
+__device__ __forceinline__ int divide(int i, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)i, magic) : i; }
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) rope_rows_kernel(const RopeArgs a) {
     extern __shared__ __align__(16) float2 s_cs[];  // [rows][n]
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.z, t0 = blockIdx.x * a.rows, rows = min(a.rows, a.T - t0);
     const int base = a.kv_len[b];
-    for (int i = threadIdx.x; i < a.f.n; i += kThreads) {
-        const uint64_t turn = rope::turn(a.f.inv_freq[i]);
-        for (int r = 0; r < rows; ++r)
-            s_cs[r * a.f.n + i] = rope::cos_sin(turn, (int)((uint32_t)base + (uint32_t)(a.depth ? a.depth[t0 + r] : t0 + r)));
-    }
-    __syncthreads();
     const int all = a.heads[0] + a.heads[1], items = a.D / 16;
     const int h0 = blockIdx.y * a.per_block, nh = min(a.per_block, all - h0);
-    const int count = rows * nh * items;
+    const int count = rows * a.per_block * items;  // (heads behind the last are left out below)
     using Raw = typename append::Raw8<T>::type;
-    for (int first = threadIdx.x; first < count; first += kBatch * kThreads) {
-        Raw x[kBatch], y[kBatch];
-        T* out[kBatch];
-        int row[kBatch];
-        rope::Item at[kBatch];
+    Raw x[kBatch<T>], y[kBatch<T>];
+    T* out[kBatch<T>];
+    int row[kBatch<T>];
+    rope::Item at[kBatch<T>];
+    auto load = [&](int first) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kBatch<T>; ++k) {
             const int i = first + k * kThreads;
             row[k] = -1;
-            if (i >= count) continue;
-            const int h = h0 + i / items % nh;
-            row[k] = i / items / nh;
-            at[k] = rope::item_at(a.f, i % items);
-            const int which = h >= a.heads[0];
-            const size_t o = (((size_t)b * a.T + t0 + row[k]) * a.heads[which] + (which ? h - a.heads[0] : h)) * a.D;
-            const T* in = static_cast<const T*>(a.in[which]) + o;
-            out[k] = static_cast<T*>(a.out[which]) + o;
+            const int j = divide(i, a.items_magic), r = divide(j, a.heads_magic), h = h0 + j - r * a.per_block;
+            if (i >= count || h >= h0 + nh) continue;
+            row[k] = r;
+            at[k] = rope::item_at(a.f, i - j * items, a.D);
+            const bool key = h >= a.heads[0];
+            const size_t o = (((size_t)b * a.T + t0 + r) * (key ? a.heads[1] : a.heads[0]) + (key ? h - a.heads[0] : h)) * a.D;
+            const T* in = static_cast<const T*>(key ? a.in[1] : a.in[0]) + o;
+            out[k] = static_cast<T*>(key ? a.out[1] : a.out[0]) + o;
             x[k].load_plain(in + at[k].first);
             y[k].load_plain(in + at[k].second);
         }
+    };
+    load(threadIdx.x);  // on their way while the table is filled
+    rope::fill_table(a.f, s_cs, 0, rows, [&](int r) { return (int)((uint32_t)base + (uint32_t)(a.depth ? a.depth[t0 + r] : t0 + r)); });
+    __syncthreads();
+    for (int first = threadIdx.x; first < count; first += kBatch<T> * kThreads) {
+        if (first != (int)threadIdx.x) load(first);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kBatch<T>; ++k) {
             if (row[k] < 0) continue;
             float u[8], v[8];
             x[k].unpack(u);
             y[k].unpack(v);
-            if (at[k].freq >= 0) rope::rotate(u, v, s_cs + row[k] * a.f.n + at[k].freq, a.f.interleaved);
+            if (at[k].turns >= 0) rope::rotate(a.f, u, v, reinterpret_cast<const float4*>(s_cs + row[k] * a.f.n) + at[k].turns);
             rope::store8(out[k] + at[k].first, u);
             rope::store8(out[k] + at[k].second, v);
         }
@@ -104,14 +110,17 @@ extern "C" int medusa_rope_rows(const void* q, const void* k, medusa_dtype dtype
     a.kv_len = kv_len; a.depth = depth;
     a.f = rope::Freqs{inv_freq, n_freq, interleaved != 0};
     a.T = T; a.D = D; a.heads[0] = Hq; a.heads[1] = Hkv;
-    // Blocks of about four batches a thread; where that leaves SMs without a block, of fewer
+    // Blocks of about sixteen items a thread; where that leaves SMs without a block, of fewer
     // rows, then of fewer heads.
     const int all = Hq + Hkv, items = D / 16, sms = sm_count();
-    a.rows = std::clamp(4 * kBatch * kThreads / (all * items), 1, kMaxRows);
+    a.rows = std::clamp(16 * kThreads / (all * items), 1, kMaxRows);
     while (a.rows > 1 && (long long)B * ((T + a.rows - 1) / a.rows) < 2 * sms) a.rows /= 2;
     a.per_block = all;
     while (a.per_block > 16 && (long long)B * ((T + a.rows - 1) / a.rows) * ((all + a.per_block - 1) / a.per_block) < sms)
         a.per_block = (a.per_block + 1) / 2;
+    auto magic = [](int d) { return d == 1 ? 0u : (uint32_t)(((1ull << 32) + d - 1) / d); };
+    a.items_magic = magic(items);
+    a.heads_magic = magic(a.per_block);
     const dim3 grid((T + a.rows - 1) / a.rows, (all + a.per_block - 1) / a.per_block, B);
     const size_t smem = (size_t)a.rows * n_freq * sizeof(float2);  // at most 16 * 256 * 8 bytes
     cudaStream_t st = as_stream(stream);

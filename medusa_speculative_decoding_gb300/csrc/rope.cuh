@@ -31,39 +31,62 @@ __device__ __forceinline__ uint64_t turn(float inv_freq) {
     return __double2ull_rn(t * 18446744073709551616.0);
 }
 
-// (cos, sin) of p turns
+// (cos, sin) of p turns.  Within an eighth of a revolution of a multiple of a quarter, the series
+// of sine and cosine to the 9th and 10th power are off by 2^-29 and 2^-33 (the next terms, x^11 /
+// 11! and x^12 / 12!); what is left is the rounding of the angle and of the sums, 2^-24 each.
 __device__ __forceinline__ float2 cos_sin(uint64_t turn, int p) {
     const uint32_t w = (uint32_t)((turn * (uint64_t)(int64_t)p) >> 32);  // units of 2^-32 revolutions
     const uint32_t quarter = (w + (1u << 29)) >> 30;
-    const float x = (float)(int32_t)(w - (quarter << 30)) * 0x1p-31f;  // half turns, within a quarter
-    float s, c;
-    sincospif(x, &s, &c);
+    const float x = (float)(int32_t)(w - (quarter << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+    const float z = x * x;
+    const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
     const float cs = quarter & 1 ? s : c, sn = quarter & 1 ? c : s;
     return make_float2((quarter + 1) & 2 ? -cs : cs, quarter & 2 ? -sn : sn);
 }
 
-// The sixteen values that a thread works on: eight pairs in two pieces of eight values, or
-// sixteen values behind the pairs.  item = 0 .. D / 16 - 1 of a head.
+// The sixteen values that a thread works on, item = 0 .. D / 16 - 1 of a head: eight pairs, or
+// sixteen values behind the pairs, in two pieces of eight that lie as far apart as they can, so that
+// neighbouring threads read neighbouring pieces.
 struct Item {
     int first, second;  // where the two pieces begin
-    int freq;           // of the first pair, -1: not rotated
+    int turns;          // its place in a row of the table, -1: not rotated
 };
-__device__ __forceinline__ Item item_at(const Freqs& f, int item) {
+__device__ __forceinline__ Item item_at(const Freqs& f, int item, int D) {
     const int i = item * 8;
-    if (i >= f.n) return Item{2 * i, 2 * i + 8, -1};
-    return f.interleaved ? Item{2 * i, 2 * i + 8, i} : Item{i, f.n + i, i};
+    return i < f.n ? Item{i, f.n + i, item} : Item{f.n + i, (D - 2 * f.n) / 2 + f.n + i, -1};
 }
 
-// a, b: the two pieces; cs: (cos, sin) of the eight pairs
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float2* cs, bool interleaved) {
+// A row's cosines and sines in shared memory, [4][n / 8] float4 of two pairs each: the threads of
+// neighbouring items read side by side (sixteen bytes of every 64 took four times as long).
+// Entry e of n: frequency freq_at(e) at float2 number place(e).
+__device__ __forceinline__ int freq_at(const Freqs& f, int e) {  // the pair that an item's k-th is, e = 8 * item + k
+    const int item = e >> 3, k = e & 7;
+    return !f.interleaved ? e : k < 4 ? item * 4 + k : f.n / 2 + item * 4 + k - 4;
+}
+__device__ __forceinline__ int place(const Freqs& f, int e) { return ((e & 7) >> 1) * (f.n / 4) + (e >> 3) * 2 + (e & 1); }
+
+// The rows first .. first + count - 1 of the table; row r stands at position pos(r).  Called by
+// every thread of the block.
+template <typename Pos>
+__device__ __forceinline__ void fill_table(const Freqs& f, float2* table, int first, int count, Pos pos) {
+    const int per = blockDim.x / f.n, e = threadIdx.x % f.n;  // threads per entry
+    if ((int)threadIdx.x >= per * f.n) return;
+    const uint64_t step = turn(f.inv_freq[freq_at(f, e)]);
+    const int at = place(f, e);
+    for (int r = first + threadIdx.x / f.n; r < first + count; r += per) table[r * f.n + at] = cos_sin(step, pos(r));
+}
+
+// a, b: the two pieces; turns: the item's first float4 of the row's table
+__device__ __forceinline__ void rotate(const Freqs& f, float (&a)[8], float (&b)[8], const float4* turns) {
     float2 t[8];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float4 v = *reinterpret_cast<const float4*>(cs + i);
-        t[i] = make_float2(v.x, v.y);
-        t[i + 1] = make_float2(v.z, v.w);
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = turns[i * (f.n / 8)];
+        t[2 * i] = make_float2(v.x, v.y);
+        t[2 * i + 1] = make_float2(v.z, v.w);
     }
-    if (interleaved) {
+    if (f.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], w = b[2 * i + 1];

@@ -9,11 +9,11 @@
 //   p_0 + ... + p_v > u_d * (p_0 + ... + p_{V-1}).
 //
 // A row has V boundaries, each of which could fall next to u: sums in float32 would pick
-// another token in V * 2^-23 of the draws, 1.5% at V = 128256.  So sums are 64 bits wide where
-// they meet: a thread adds 32 values as two float32 sums, of their multiples of 2^-18 (exact)
-// and of what is left (below 2^-14, off by 2^-34 of its terms), and everything from there on
-// is in double; 64-bit additions of every value would take an SM, which does two a cycle,
-// longer than reading them.
+// another token in V * 2^-23 of the draws, 1.5% at V = 128256.  So sums have 48 bits where they
+// meet: a thread adds sixteen values as two float32 sums, of their multiples of 2^-18 (exact) and
+// of what is left (below 2^-15, off by 2^-35 of its terms at most), and everything from there on is
+// a pair of float32, high and low part (in double, of which an SM adds two a cycle, the draws of
+// 64 rows of 32000 took 40 us instead of 6).
 //
 // A cluster of CTAs draws from one row: each CTA sums a contiguous slice, the totals are
 // pushed to every CTA, and the one whose slice holds the number finds the token in it.
@@ -30,7 +30,7 @@ namespace medusa {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBatch = 8;         // float4 of a thread with their loads in flight
+constexpr int kBatch = 4;         // float4 of a thread with their loads in flight
 constexpr int kMaxCluster = 8;
 constexpr int kSlice = 8192;      // values of a CTA, where the cluster can be that large
 constexpr int kMaxNodes = 512;
@@ -46,19 +46,55 @@ struct DrawArgs {
 };
 
 struct DrawSmem {
-    double total[kMaxCluster];  // of every CTA of the cluster
-    double warp_total[kWarps];
+    float2 total[kMaxCluster];  // of every CTA of the cluster
+    float2 warp_total[kWarps];
     int token;
 };
 
 // probabilities: negative ones and NaN count as 0, those above 1 as 1
 __device__ __forceinline__ float clean(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
 
-__device__ __forceinline__ double shfl_up_d(double v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
-
-__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+// Sums of two float32: x + y exactly, |y| at most half of x's last place.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
 }
+__device__ __forceinline__ float2 add(float2 a, float2 b) {
+    const float2 s = two_sum(a.x, b.x);
+    return two_sum(s.x, __fadd_rn(s.y, __fadd_rn(a.y, b.y)));
+}
+__device__ __forceinline__ bool greater(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
+__device__ __forceinline__ bool positive(float2 a) { return a.x > 0.f; }
+__device__ __forceinline__ float2 shfl_up2(float2 v, int o) {
+    return make_float2(__shfl_up_sync(0xffffffffu, v.x, o), __shfl_up_sync(0xffffffffu, v.y, o));
+}
+__device__ __forceinline__ float2 shfl2(float2 v, int l) {
+    return make_float2(__shfl_sync(0xffffffffu, v.x, l), __shfl_sync(0xffffffffu, v.y, l));
+}
+// inclusive sums over the lanes
+__device__ __forceinline__ float2 scan(float2 v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float2 u = shfl_up2(v, o);
+        if (lane >= o) v = add(u, v);
+    }
+    return v;
+}
+// The lane whose part holds `target`, the parts laid end to end behind `base`: the first whose
+// end lies behind it, the last with any weight where rounding leaves none, -1 where all are
+// empty.  base becomes what lies before that part (behind all of them where over is false).
+__device__ __forceinline__ int part_of(float2 mine, float2 target, float2& base, bool& over) {
+    const float2 upto = add(base, scan(mine));
+    const unsigned some = __ballot_sync(0xffffffffu, positive(mine)), behind = __ballot_sync(0xffffffffu, positive(mine) && greater(upto, target));
+    over = behind != 0;
+    if (!some) return -1;
+    const int at = behind ? __ffs(behind) - 1 : 31 - __clz(some);
+    const float2 before = shfl_up2(upto, 1), end = shfl2(upto, 31);
+    base = behind ? (at ? shfl2(before, at) : base) : end;
+    return at;
+}
+
 __device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -84,7 +120,7 @@ __device__ __forceinline__ int draw(const DrawArgs& a, const float* row, float u
     const bool aligned = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
     const int per_warp = a.slice / kWarps;  // a multiple of 128
     const int begin = min(a.V, rank * a.slice + warp * per_warp), end = min(a.V, begin + per_warp);
-    double sum = 0.;
+    float2 sum = make_float2(0.f, 0.f);
     for (int v0 = begin; v0 < end; v0 += 128 * kBatch) {
         float4 x[kBatch];
 #pragma unroll
@@ -99,94 +135,66 @@ __device__ __forceinline__ int draw(const DrawArgs& a, const float* row, float u
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float h = __fsub_rn(__fadd_rn(y[i], 48.f), 48.f);  // to a multiple of 2^-18
-                hi += h;
-                lo += y[i] - h;
+                hi = __fadd_rn(hi, h);
+                lo = __fadd_rn(lo, __fsub_rn(y[i], h));
             }
         }
-        sum += (double)hi + (double)lo;
+        sum = add(sum, two_sum(hi, lo));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1)
+        sum = add(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
     if (lane == 0) s.warp_total[warp] = sum;
     __syncthreads();
     if (first) cluster_wait();  // every CTA of the cluster runs: its shared memory can be written
+    const float2 none = make_float2(0.f, 0.f);
     if (warp == 0) {
-        double t = 0.;
-        for (int w = 0; w < kWarps; ++w) t += s.warp_total[w];
-        if (lane < ctas) st_cluster_f64(cluster_map(smem_addr(&s.total[rank]), lane), t);
+        float2 t = lane < kWarps ? s.warp_total[lane] : none;
+        t = shfl2(scan(t), 31);
+        if (lane < ctas) st_cluster_f32x2(cluster_map(smem_addr(&s.total[rank]), lane), t.x, t.y);
     }
     cluster_sync();
-    double all = 0.;
-    for (int c = 0; c < ctas; ++c) all += s.total[c];
-    const double target = fmax((double)u * all, 0.);
-    // The part that holds the number: the first whose end lies behind it, the last with any
-    // weight where rounding leaves none.  The same in every CTA.
-    double at = 0., base = 0.;
-    int winner = -1;
-    for (int c = 0; c < ctas; ++c) {
-        const double t = s.total[c];
-        if (!(t > 0.)) continue;
-        winner = c;
-        base = at;
-        at += t;
-        if (at > target) break;
-    }
-    if (rank == max(winner, 0) && warp == 0) {
-        int token = -1;
-        if (winner >= 0) {
-            int w_at = 0;
-            at = base;
-            for (int w = 0; w < kWarps; ++w) {
-                const double t = s.warp_total[w];
-                if (!(t > 0.)) continue;
-                w_at = w;
-                base = at;
-                at += t;
-                if (at > target) break;
-            }
-            const int b0 = min(a.V, rank * a.slice + w_at * per_warp), b1 = min(a.V, b0 + per_warp);
-            at = base;
-            int last = -1;
-            for (int v0 = b0; v0 < b1; v0 += 128 * kBatch) {
-                float4 x[kBatch];
+    if (warp == 0) {
+        // Every CTA finds the same CTA of the cluster, and that one the warp's part and the token.
+        const float2 part = lane < ctas ? s.total[lane] : none;
+        const float2 all = shfl2(scan(part), 31);
+        const float un = fmaxf(u, 0.f), ph = __fmul_rn(un, all.x);
+        const float2 target = two_sum(ph, __fadd_rn(__fmaf_rn(un, all.x, -ph), __fmul_rn(un, all.y)));
+        float2 base = none;
+        bool over;
+        const int winner = part_of(part, target, base, over);
+        if (rank == max(winner, 0)) {
+            int token = -1;
+            if (winner >= 0) {
+                if (!over) base = none;  // (the last weight of all: every sum counts as too small)
+                const float2 goal = over ? target : make_float2(INFINITY, 0.f);
+                const int w_at = part_of(lane < kWarps ? s.warp_total[lane] : none, goal, base, over);
+                const int b0 = min(a.V, rank * a.slice + w_at * per_warp), b1 = min(a.V, b0 + per_warp);
+                // 1024 values at a time, 32 a lane, then a lane's values one a lane
+                const bool found_warp = over;
+                for (int v0 = b0; v0 < b1; v0 += 1024) {
+                    float2 mine = none;
+                    const int from = v0 + 32 * lane;
+                    float4 x[8];
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int v = v0 + 128 * k + 4 * lane;
-                    x[k] = v < b1 ? values4(row, v, b1, aligned) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+                    for (int k = 0; k < 8; ++k) x[k] = from + 4 * k < b1 ? values4(row, from + 4 * k, b1, aligned) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const float y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                    double mine = 0., upto;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mine += (double)y[i];
-                    upto = mine;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const double t = shfl_up_d(upto, o);
-                        if (lane >= o) upto += t;
+                    for (int k = 0; k < 8; ++k) {
+                        mine = add(mine, two_sum(x[k].x, x[k].y));
+                        mine = add(mine, two_sum(x[k].z, x[k].w));
                     }
-                    double c = at + (upto - mine);
-                    int found = -1, behind = -1;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        c += (double)y[i];
-                        const int v = v0 + 128 * k + 4 * lane + i;
-                        if (y[i] > 0.f) {
-                            behind = v;
-                            if (found < 0 && c > target) found = v;
-                        }
-                    }
-                    const unsigned hit = __ballot_sync(0xffffffffu, found >= 0), any = __ballot_sync(0xffffffffu, behind >= 0);
-                    if (hit && token < 0) token = __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
-                    if (any) last = __shfl_sync(0xffffffffu, behind, 31 - __clz(any));
-                    at += __shfl_sync(0xffffffffu, upto, 31);
+                    bool in_chunk, in_lane;
+                    const int l = part_of(mine, found_warp ? goal : make_float2(INFINITY, 0.f), base, in_chunk);
+                    if (l < 0) continue;
+                    const int v = v0 + 32 * l + lane;
+                    float2 before = base;
+                    const int e = part_of(make_float2(v < b1 ? clean(__ldg(row + v)) : 0.f, 0.f), in_chunk ? goal : make_float2(INFINITY, 0.f), before, in_lane);
+                    token = v0 + 32 * l + e;
+                    if (in_chunk) break;
                 }
-                if (token >= 0) break;
             }
-            if (token < 0) token = last;
+            if (lane < ctas) st_cluster_s32(cluster_map(smem_addr(&s.token), lane), token);
         }
-        if (lane < ctas) st_cluster_s32(cluster_map(smem_addr(&s.token), lane), token);
     }
     cluster_sync();
     return s.token;
@@ -213,7 +221,7 @@ __device__ __forceinline__ void finish(const DrawArgs& a, int b, int steps, int 
     }
 }
 
-__global__ void __launch_bounds__(kThreads) draw_walk_kernel(const DrawArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) draw_walk_kernel(const DrawArgs a) {
     __shared__ DrawSmem s;
     __shared__ int s_parent[kMaxNodes], s_cand[kMaxNodes], s_path[kMaxNodes], s_child;
     const int ctas = gridDim.x, rank = blockIdx.x, b = blockIdx.y;
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) draw_walk_kernel(const DrawArgs a) {
     if (rank == 0) finish(a, b, steps, node, token, s_path);
 }
 
-__global__ void __launch_bounds__(kThreads) draw_rows_kernel(const DrawArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) draw_rows_kernel(const DrawArgs a) {
     __shared__ DrawSmem s;
     const int ctas = gridDim.x, rank = blockIdx.x, node = blockIdx.y, b = blockIdx.z;
     umma::cluster_arrive_relaxed();
