@@ -10,7 +10,7 @@
 // positions nor on how sines are rounded, and nothing is clipped.  e4m3 is a floating type, so
 // the half bit of range that this can leave unused costs no precision but in its subnormals.
 //
-// One CTA per (page that receives rows, up to eight heads of K, of V or of the queries,
+// One CTA per (page that receives rows, up to four heads of K, of V or of the queries,
 // sequence).  The page's sines and cosines are formed once into shared memory, while the first
 // head's rows are on their way; a thread has pieces of sixteen values, both halves of eight
 // pairs, so that no value crosses threads.  Bound by HBM for prompts: rows, queries and codes
@@ -340,9 +340,9 @@ extern "C" int medusa_kv_append_rope_q8(const void* k_rows, const void* v_rows, 
     a.f = rope::Freqs{inv_freq, n_freq, interleaved != 0};
     a.B = B; a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.P = P; a.M = M; a.n_pages = n_pages;
     a.h16 = hid ? (int)((long long)H * elem / 16) : 0;
-    // A CTA takes up to eight heads one after the other, the next one's rows on their way, as
+    // A CTA takes up to four heads one after the other, the next one's rows on their way, as
     // long as that leaves four CTAs for every SM.
-    a.per_cta = (int)std::min(8ll, std::max(1ll, (2ll * Hkv + Hq) * windows * B / (4 * sm_count())));
+    a.per_cta = (int)std::min(4ll, std::max(1ll, (2ll * Hkv + Hq) * windows * B / (4 * sm_count())));
     a.groups = (Hkv + a.per_cta - 1) / a.per_cta;
     a.q_groups = (Hq + a.per_cta - 1) / a.per_cta;
     cudaStream_t st = as_stream(stream);

@@ -88,8 +88,8 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // 22 and 23 idle (registers are handed over by groups of four warps).
 //
 // V codes that are NaN would spoil rows that do not see them (0 * NaN), and the slots behind a
-// sequence's length hold anything: the conversion writes zero for them and notes the key, and
-// a row that does see one is made NaN.
+// sequence's length hold anything: the conversion writes zero for them and notes the first such
+// slot.  A row that sees it, and so all rows that see any, is made NaN when its results go out.
 //
 // Every wait is bounded; a CTA that gives up marks its results NaN.
 // ---------------------------------------------------------------------------
@@ -110,13 +110,13 @@ struct USmem {
     static constexpr int kOffV = kOffK + KR * kCodes;
     static constexpr int kOffV16 = kOffV + VR * kCodes;
     static constexpr int kOffScale = kOffV16 + 2 * kCodes * 2;  // float4 [kScaleRing][kGroups]
-    static constexpr int kOffNan = kOffScale + kScaleRing * kGroups * 16;  // uint32 [2][4]
-    static constexpr int kOffQf = kOffNan + 32;  // float [2][256]: the rows' factors
+    static constexpr int kOffNan = kOffScale + kScaleRing * kGroups * 16;  // int [4][kConvWarps]: first slot with a NaN code of V
+    static constexpr int kOffQf = kOffNan + 64;  // float [2][256]: the rows' factors
     static constexpr int kOffX = kOffQf + 2 * 2 * kRows * 4;  // float2 [2][128]: the streams' references and sums (split)
     static constexpr int kOffCursor = kOffX + (PAIR ? 0 : 2 * kRows * 8);
     static constexpr int kOffBar = kOffCursor + 32;
-    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull [2], pfull odone [2][2], qfull qfree xfull xdone stagger drain [2], scfull
-    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 10 + 7 + kScaleRing;
+    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull [2], pfull odone [2][2], qfull qfree [2], xfull xdone turn [2] drain [2], scfull
+    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 10 + 10 + kScaleRing;
     static constexpr int kOffMisc = kOffBar + kBars * 8;  // TMEM slot, flag
     static constexpr int kOffTables = kOffMisc + 8;
     static constexpr int bytes(int B) { return kOffTables + chunks::table_bytes(B) + 1024; }  // + alignment
@@ -149,12 +149,6 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
     asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
         : "=r"(lo), "=r"(hi) : "r"(c));
 }
-__device__ __forceinline__ uint16_t to_e5m2x2(float lo, float hi) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
-    return c;
-}
-
 // kind::f16 with f16 A and B, float32 D; A K-major, B MN-major
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
     return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -193,16 +187,17 @@ __device__ __forceinline__ uint64_t code_desc(uint32_t addr) {
     else return umma::desc_sw64(addr, 16, 512);
 }
 
-// Eight values of a query row as two planes; f: the row's power of two.
+// Eight values of a query row as two planes; f: the row's power of two, which brings them to
+// where f16 holds all of their bits that the planes do.
 __device__ __forceinline__ void split_planes(const uint4& x, float f, uint2& hi, uint2& lo) {
     const uint32_t v[4] = {x.x, x.y, x.z, x.w};
     uint16_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = bf16_lo(v[i]) * f, b = bf16_hi(v[i]) * f;
-        h[i] = q8::float2_to_e4m3x2(a, b);
-        const float2 g = q8::e4m3x2_to_float2(h[i]);
-        l[i] = to_e5m2x2(a - g.x, b - g.y);
+        const uint32_t q = pack_f16(bf16_lo(v[i]) * f, bf16_hi(v[i]) * f);
+        asm("{\n.reg .b32 g, r;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, %2;\ncvt.rn.f16x2.e4m3x2 g, %0;\nsub.f16x2 r, %2, g;\n"
+            "cvt.rn.satfinite.e5m2x2.f16x2 %1, r;\n}"
+            : "=&h"(h[i]), "=h"(l[i]) : "r"(q));
     }
     hi = make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16);
     lo = make_uint2((uint32_t)l[0] | (uint32_t)l[1] << 16, (uint32_t)l[2] | (uint32_t)l[3] << 16);
@@ -268,10 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
     const uint32_t base_a = smem_addr(base);
     const uint32_t bar = base_a + L::kOffBar;
     const uint32_t kfull = bar, kempty = kfull + 8 * KR, vfull = kempty + 8 * KR, vempty = vfull + 8 * VR, wfull = vempty + 8 * VR,
-                   wempty = wfull + 16, sfull = wempty + 16, pfull = sfull + 16, odone = pfull + 32, qfull = odone + 32, qfree = qfull + 8,
-                   xfull = qfree + 8, xdone = xfull + 8, stagger = xdone + 8, drain = stagger + 8, scfull = drain + 16;
+                   wempty = wfull + 16, sfull = wempty + 16, pfull = sfull + 16, odone = pfull + 32, qfull = odone + 32, qfree = qfull + 16,
+                   xfull = qfree + 16, xdone = xfull + 8, turn = xdone + 8, drain = turn + 16, scfull = drain + 16;
     float4* s_scale = reinterpret_cast<float4*>(base + L::kOffScale);
-    uint32_t* s_nan = reinterpret_cast<uint32_t*>(base + L::kOffNan);
+    volatile int* s_nan = reinterpret_cast<volatile int*>(base + L::kOffNan);
     float* s_qf = reinterpret_cast<float*>(base + L::kOffQf);
     int* s_cursor = reinterpret_cast<int*>(base + L::kOffCursor);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::kOffMisc);
@@ -288,9 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             for (int i = 0; i < KR; ++i) mbar_init(kempty + 8 * i, 2);
             for (int i = 0; i < 2; ++i) mbar_init(wempty + 8 * i, 2);
         }
-        mbar_init(qfree, 2);
+        if (!PAIR) mbar_init(qfree, 2);  // (both streams are done with the one block of queries)
         for (int i = 0; i < 4; ++i) mbar_init(pfull + 8 * i, 4);
-        mbar_init(qfull, kConvWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(qfull + 8 * i, kConvWarps);
         mbar_init(xfull, 8);
         mbar_init(xdone, 8);
         mbar_init_fence();
@@ -355,13 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                 for (int c = 0; c < D / 32; ++c) mma_f8_warp(tS, dq + (L::kCodes >> 4) + 2 * c, k + 2 * c, idesc_lo, 1);
                 commit_warp(sfull + 8 * s);
                 commit_warp(kempty + 8 * slot);
-                if (i + 1 == ns) commit_warp(qfree);
+                if (i + 1 == ns) commit_warp(qfree + (PAIR ? 8 * s : 0));
                 return true;
             };
-            ok = warp_wait(qfull, segments & 1, lim);
+            ok = warp_wait(qfull + (PAIR ? 8 * s : 0), segments & 1, lim);
             fence_after_sync();
-            // The streams half a tile apart: one's weights are formed while the other's products run.
-            if (PAIR && s == 1 && ok) ok = warp_wait(stagger, segments & 1, lim);
             if (ns) ok = ok && issue_s(0);
             else if (lane == 0) mbar_arrive(qfree);
             for (int i = 0; i < ns && ok; ++i) {
@@ -370,17 +363,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                 ok = warp_wait(wfull + 8 * slot, (tile >> 1) & 1, lim);
                 for (int h = 0; h < 2 && ok; ++h) {
                     ok = warp_wait(pfull + 8 * (2 * s + h), (had + i) & 1, lim);
+                    // The streams take turns with a tile's second PV and the next scores: issued side by
+                    // side both take twice as long, and both streams wait at the same time.
+                    if (PAIR && h && ok && (s || had + i)) ok = warp_wait(turn + 8 * s, (had + i - (s ? 0 : 1)) & 1, lim);
                     if (!ok) break;
                     fence_after_sync();
 #pragma unroll
                     for (int k = 0; k < kHalf / 16; ++k)
                         mma_f16_ta_warp(tO, tS + 32 * h + 8 * k, v + (((4 * h + k) * 2048) >> 4), idesc_pv, (i > 0 || h > 0 || k > 0) ? 1u : 0u);
                     commit_warp(odone + 8 * (2 * s + h));
-                    if (PAIR && s == 0 && i == 0 && h == 0 && lane == 0) mbar_arrive(stagger);
                 }
                 if (!ok) break;
                 commit_warp(wempty + 8 * slot);
                 if (i + 1 < ns) ok = issue_s(i + 1);
+                if (PAIR && lane == 0) mbar_arrive(turn + 8 * (s ^ 1));
             }
             first += nt;
             had += ns;
@@ -460,33 +456,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
         const int cw = warp - kConvWarp;
         uint32_t tile = 0, segments = 0;
         for (; ok && at.begin < g1; at.next(w, tab)) {
-            const int nt = at.end_tile(w, g1) - at.first_tile(w, g0);
+            const int t0 = at.first_tile(w, g0), nt = at.end_tile(w, g1) - t0;
             if (nt <= 0) continue;
             {
                 // Rows two by two (D = 128) or four by four, sixteen bytes a lane: a row's largest value
                 // by shuffles; the next eight loads are on their way meanwhile.
-                constexpr int W = D / 8, PER = 32 / W, ROWS = (PAIR ? 2 : 1) * kRows / kConvWarps, PASSES = ROWS / PER, B = PASSES < 8 ? PASSES : 8;
+                // (PAIR: stream 0's rows first, so that it can go on while stream 1 still works)
+                constexpr int W = D / 8, PER = 32 / W, ROWS = kRows / kConvWarps, PASSES = ROWS / PER, B = PASSES < 8 ? PASSES : 8;
                 const uint16_t* q = static_cast<const uint16_t*>(a.q) + (((size_t)at.b * w.T + at.j * w.tb) * a.Hq + at.h * a.G) * D + lane % W * 8;
                 const int see0 = at.L - at.n + at.j * w.tb, left = min(w.tb, at.n - at.j * w.tb);
+                auto row_of = [&](int p) { return p / PASSES * kRows + cw * ROWS + p % PASSES * PER + lane / W; };
                 auto load = [&](int p, uint4 (&x)[B]) {
 #pragma unroll
                     for (int k = 0; k < B; ++k) {
-                        const int r = cw * ROWS + (p + k) * PER + lane / W, t = token_of(r);
+                        const int r = row_of(p + k), t = token_of(r);
                         x[k] = make_uint4(0, 0, 0, 0);
                         if (t < left && see0 + t >= 0) x[k] = *reinterpret_cast<const uint4*>(q + ((size_t)t * a.Hq + (r - t * a.G)) * D);
                     }
                 };
                 uint4 x[B];
                 load(0, x);
-                if (segments) ok = warp_wait(qfree, (segments - 1) & 1, lim);
-                if (!ok) break;
 #pragma unroll 1
-                for (int p = 0; p < PASSES; p += B) {
+                for (int p = 0; p < (PAIR ? 2 : 1) * PASSES; p += B) {
                     uint4 ahead[B];
-                    if (p + B < PASSES) load(p + B, ahead);
+                    if (p + B < (PAIR ? 2 : 1) * PASSES) load(p + B, ahead);
+                    if (segments && p % PASSES == 0) ok = warp_wait(qfree + 8 * (p / PASSES), (segments - 1) & 1, lim);
+                    if (!ok) break;
 #pragma unroll
                     for (int k = 0; k < B; ++k) {
-                        const int r = cw * ROWS + (p + k) * PER + lane / W;
+                        const int r = row_of(p + k);
                         const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                         uint32_t m = 0;
 #pragma unroll
@@ -498,18 +496,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                         const int e = max((int)(m >> 7) - 127, -119);
                         uint2 hi, lo;
                         split_planes(finite ? x[k] : make_uint4(0, 0, 0, 0), __uint_as_float((uint32_t)(7 - e + 127) << 23), hi, lo);
-                        uint8_t* to = base + (PAIR ? 2 * (r >> 7) * L::kCodes : 0) + code_offset<D>(r & 127, lane % W >> 1) + (lane & 1) * 8;
+                        uint8_t* to = base + 2 * (r >> 7) * L::kCodes + code_offset<D>(r & 127, lane % W >> 1) + (lane & 1) * 8;
                         *reinterpret_cast<uint2*>(to) = hi;
                         *reinterpret_cast<uint2*>(to + L::kCodes) = lo;
                         if (lane % W == 0) s_qf[(segments & 1) * 2 * kRows + r] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : NAN;
+                    }
+                    if ((p + B) % PASSES == 0) {
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(qfull + 8 * (p / PASSES));
                     }
 #pragma unroll
                     for (int k = 0; k < B; ++k) x[k] = ahead[k];
                 }
                 if (!ok) break;
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(qfull);
                 ++segments;
                 // the next unit's queries into L2: 128 bytes a lane
                 chunks::Cursor n = at;
@@ -524,6 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     }
                 }
             }
+            const int first_nan = (segments - 1) % 4 * kConvWarps + cw;
+            if (lane == 0) s_nan[first_nan] = 0x7fffffff;
             for (int t = 0; t < nt; ++t, ++tile) {
                 const uint32_t vslot = tile % VR, slot = tile & 1;
                 ok = warp_wait(vfull + 8 * vslot, (tile / VR) & 1, lim);
@@ -554,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     }
                     place(key, c, o);
                 }
-                uint32_t nan_keys = 0;
                 if (__any_sync(0xffffffffu, bad & 0x80808080u)) {  // once more, with zeros for NaN codes
+                    int nan_slot = 0x7fffffff;
 #pragma unroll 1
                     for (int i = 0; i < C; ++i) {
                         const int x = i * 32 + lane, key = cw * 32 + x / C, c = x % C;
@@ -568,12 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                             any |= n;
                             codes_to_f16(in[e] & ~(n * 0xffu), o[2 * e], o[2 * e + 1]);
                         }
-                        if (any) nan_keys |= 1u << (key & 31);
+                        if (any) nan_slot = min(nan_slot, (t0 + t) * kTile + key);
                         place(key, c, o);
                     }
-                    nan_keys = __reduce_or_sync(0xffffffffu, nan_keys);
+                    nan_slot = __reduce_min_sync(0xffffffffu, nan_slot);
+                    if (lane == 0) s_nan[first_nan] = min(s_nan[first_nan], nan_slot);
                 }
-                if (lane == 0) s_nan[slot * 4 + cw] = nan_keys;
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             }
             const int limit = real && token < at.n ? at.L - at.n + token : -1;  // the last slot that the row sees
             const bool any = __any_sync(0xffffffffu, limit >= 0);
-            ok = warp_wait(qfull, segments & 1, lim);
+            ok = warp_wait(qfull + (PAIR ? 8 * s : 0), segments & 1, lim);
             if (!ok) break;
             const float qf = s_qf[(segments & 1) * 2 * kRows + row];
             // ---- tiles ----
@@ -697,16 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     }
                     l += sum;
                     tmem_wait_st();
-                    // keys whose V has a NaN code: rows that see one are NaN
-                    const uint32_t slot = n_tile & 1;
-                    if (ok && !h) ok = warp_wait(wfull + 8 * slot, (n_tile >> 1) & 1, lim);
-                    if (!ok) break;
-                    const uint2 bad = *reinterpret_cast<const uint2*>(s_nan + 4 * slot + 2 * h);
-                    if (bad.x | bad.y) {
-                        const uint32_t m0 = see < 0 ? 0u : see >= 31 ? ~0u : (2u << see) - 1u;
-                        const uint32_t m1 = see < 32 ? 0u : see >= 63 ? ~0u : (2u << (see - 32)) - 1u;
-                        if ((bad.x & m0) | (bad.y & m1)) l = NAN;
-                    }
                     fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(pfull + 8 * (2 * s + h));
@@ -741,6 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             if (!PAIR && ok && (s == 1 || split)) ok = warp_wait(odone + 8 * (2 * (s ^ 1) + 1), (had[s ^ 1] - 1) & 1, lim);
             if (!ok) break;
             fence_after_sync();
+            {
+                int nan_slot = 0x7fffffff;
+                for (int k = 0; k < kConvWarps; ++k) nan_slot = min(nan_slot, s_nan[segments % 4 * kConvWarps + k]);
+                if (limit >= nan_slot) l_out = NAN;
+            }
             const size_t part = (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * a.rows + row;
             const bool zero = whole && l_out == 0.f;
             if (whole) {
