@@ -84,8 +84,8 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // Steps x = 0, 1, 2, ...: stream x & 1, tile x / 2 (or x).  The MMA warp issues PV(x), then
 // S(x + 2), so that a stream's scores being in also says that its last PV is done.
 //
-// Warps 0-7, 8-15 softmax of stream 0, 1, 16-19 conversion of V, 20 MMA, 21 pages, scales and TMA,
-// 22 and 23 idle (registers are handed over by groups of four warps).
+// Warps 0-3, 4-7 softmax of stream 0, 1, 8-11 queries to planes and V codes to f16, 12, 13 MMA of
+// stream 0, 1, 14 pages, scales and TMA, 15 rows of units that see nothing.
 //
 // V codes that are NaN would spoil rows that do not see them (0 * NaN), and the slots behind a
 // sequence's length hold anything: the conversion writes zero for them and notes the first such
@@ -95,10 +95,10 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128, kRows = 128;  // keys of a tile, rows of a stream
 constexpr int kHalf = kTile / 2;           // keys whose weights are handed over together
-constexpr int kThreads = 480, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kTmaWarp = 14;  // an MMA warp per stream
+constexpr int kThreads = 512, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kTmaWarp = 14, kZeroWarp = 15;  // an MMA warp per stream
 constexpr int kGroups = kTile / 16;  // keys that share a scale
 constexpr float kLift = 8.f, kMove = 7.f;
-constexpr int kSetup = 3;
+constexpr int kSetup = 4;
 constexpr uint32_t kDrainCycles = (uint32_t)kDefaultWaitCycles;
 
 template <int D, bool PAIR>
@@ -451,6 +451,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             }
         }
         if (!ok) *flag = 1;
+    } else if (warp == kZeroWarp) {
+        // Units that see nothing, by the share that they begin in: rows of zeros.  A warp of its own,
+        // 32 values of 16 bytes side by side (row by row in the softmax warps, such a unit cost as
+        // much as five tiles).
+        for (; at.begin < g1; at.next(w, tab)) {
+            if (at.tiles || at.begin < g0) continue;
+            const int tokens = min(w.tb, w.T - at.j * w.tb);
+            uint16_t* out = static_cast<uint16_t*>(a.out) + (((size_t)at.b * w.T + at.j * w.tb) * a.Hq + at.h * a.G) * D;
+            for (int i = lane; i < tokens * a.G * (D / 8); i += 32) {
+                const int r = i / (D / 8), t = token_of(r);
+                *reinterpret_cast<uint4*>(out + ((size_t)t * a.Hq + r - t * a.G) * D + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+            }
+        }
     } else if (warp >= kConvWarp) {
         // ---------------- queries to planes, V codes to f16 ----------------
         const int cw = warp - kConvWarp;
@@ -598,12 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             const int token = at.j * w.tb + token_in;
             const bool real = token_in < w.tb && token < w.T;
             uint16_t* out = static_cast<uint16_t*>(a.out) + (((size_t)at.b * w.T + token) * a.Hq + at.h * a.G + head_in) * D;
-            if (nt <= 0) {
-                // rows that see nothing: zero, by the share that the unit begins in
-                if (at.tiles == 0 && g0 <= at.begin && real && (PAIR || s == 0))
-                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
-                continue;
-            }
+            if (nt <= 0) continue;
             const int limit = real && token < at.n ? at.L - at.n + token : -1;  // the last slot that the row sees
             const bool any = __any_sync(0xffffffffu, limit >= 0);
             ok = warp_wait(qfull + (PAIR ? 8 * s : 0), segments & 1, lim);

@@ -27,7 +27,9 @@ struct Work {
         const int lim = L - n + min(lo + tb, n) - 1;  // last slot that the block's last row sees
         return lim < 0 ? 0 : lim / tile + 1;
     }
-    __device__ __forceinline__ int span(int L, int n, int j) const { return whole ? 1 : setup + tiles(L, n, j); }
+    // positions of a unit with so many tiles; one that sees nothing has its rows set to zero and no more
+    __device__ __forceinline__ int span_of(int tiles) const { return whole || !tiles ? 1 : setup + tiles; }
+    __device__ __forceinline__ int span(int L, int n, int j) const { return span_of(tiles(L, n, j)); }
     // total * c / ctas, in 32 bits
     __device__ __forceinline__ uint32_t share(uint32_t total, int c) const {
         const uint32_t q = total / (uint32_t)ctas, r = total - q * (uint32_t)ctas;
@@ -97,7 +99,7 @@ struct Cursor {
         n = t.len[b].y;
         tiles = w.tiles(L, n, j);
     }
-    __device__ __forceinline__ uint32_t end(const Work& w) const { return begin + (w.whole ? 1 : w.setup + tiles); }
+    __device__ __forceinline__ uint32_t end(const Work& w) const { return begin + w.span_of(tiles); }
     // the next unit; not called behind the last one
     __device__ __forceinline__ void next(const Work& w, const Tables& t) {
         begin = end(w);
