@@ -322,7 +322,7 @@ int medusa_verify_accept_chain(const float* p, const float* q, const int32_t* dr
 /* from row p with the caller's random number u = u[b,d] is the smallest v with   */
 /*   p_0 + ... + p_v > u * (p_0 + ... + p_{V-1})                                */
 /* (rows need not be normalised; entries below 0 and NaN count as 0, above 1 as 1; */
-/* sums are 64 bits wide, off by some 2^-40 of a row's total at most).  u in [0,1):   */
+/* sums have 48 bits, off by some 2^-35 of a row's total at most).  u in [0,1):   */
 /* below it counts as 0; 1 and above give the last token that has any weight.       */
 /*   probs [B,N,V] float: row u scores the token after node u; cand [B,N];          */
 /*   parent, depth [N] from the layout; u [B,Dmax+1] float                         */
@@ -488,8 +488,8 @@ int medusa_kv_pages_compact(void* k_pages, void* v_pages, float* k_scale, float*
 /*   q, q_out [B,T,Hq,D], k, k_out [B,T,Hkv,D] dtype; k and k_out may both be     */
 /*   NULL with Hkv = 0; q_out may be q and k_out may be k                        */
 /*   kv_len [B] int32; depth [T] int32 or NULL; inv_freq [n_freq] float, finite   */
-/* Limits: D % 16 == 0, D <= 512; n_freq % 8 == 0, 8 <= n_freq <= D / 2; at most  */
-/* 1024 heads of each kind.                                                     */
+/* Limits: D % 16 == 0, D <= 512; n_freq % 8 == 0, 8 <= n_freq <= D / 2; B <= 65535; */
+/* T <= 2^24; at most 1024 heads of each kind.                                  */
 int medusa_rope_rows(const void* q, const void* k, medusa_dtype dtype, const int32_t* kv_len,
                      const int32_t* depth, const float* inv_freq, int B, int T, int Hq, int Hkv, int D,
                      int n_freq, int interleaved, void* q_out, void* k_out, void* stream);
@@ -529,9 +529,9 @@ int medusa_kv_append_rope_q8(const void* k_rows, const void* v_rows, medusa_dtyp
 /* 2^-32).  A key with less than 2^-100 of that product may be left out of the row          */
 /* altogether (dtype bf16, as in 6a).                                                     */
 /* kv_len is clamped to [0, M*P], last to [-1, T-1].  Keys of a page that is not in         */
-/* [0, n_pages) or whose scale is not readable count as absent.  A row is NaN where its      */
-/* query is not finite or a key that it sees has a NaN code; what other rows see and what     */
-/* slots behind kv_len hold does not matter.                                                */
+/* [0, n_pages) or whose scale is not readable count as absent.  A row that sees a key is NaN */
+/* where its query is not finite or a key that it sees has a NaN code; what other rows see and */
+/* what slots behind kv_len hold does not matter.                                           */
 /* Limits: Hq % Hkv == 0, Hq / Hkv <= 64, T <= 2^20; scale > 0 and scale * log2(e) finite;    */
 /* scores within float32's range.                                                           */
 size_t medusa_chunk_attention_q8_workspace(int B, int T, int Hq, int Hkv, int D, medusa_dtype dtype);

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_rope_q8_kernel
     const rope::Item at = rope::item_at(a.f, tid % C16, D);  // THREADS is a multiple of C16: the same for all items of a thread
 
     if (x_block > 2 * a.groups) {  // queries: rows blockIdx.y * P on, zero behind `last`
-        const int t0 = blockIdx.y * P, rows = min(P, a.T - t0), real = min(rows, min(max(n, 0), a.T) - t0);
+        const int t0 = blockIdx.y * P, rows = min(P, a.T - t0), real = min(rows, (last >= a.T ? a.T : max(last, -1) + 1) - t0);
         if (rows <= 0) return;
         const int h0 = (x_block - 2 * a.groups - 1) * a.per_cta, h1 = min(h0 + a.per_cta, a.Hq);
         const size_t o = (((size_t)b * a.T + t0) * a.Hq) * D;

@@ -115,8 +115,8 @@ struct USmem {
     static constexpr int kOffX = kOffQf + 2 * 2 * kRows * 4;  // float2 [2][128]: the streams' references and sums (split)
     static constexpr int kOffCursor = kOffX + (PAIR ? 0 : 2 * kRows * 8);
     static constexpr int kOffBar = kOffCursor + 32;
-    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull [2], pfull odone [2][2], qfull qfree [2], xfull xdone turn [2] drain [2], scfull
-    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 10 + 10 + kScaleRing;
+    // kfull kempty [KR], vfull vempty [VR], wfull wempty [2], sfull [2], pfull odone [2][2], qfull qfree [2], xfull xdone turn [2] drain [2], qseen [2][4], scfull
+    static constexpr int kBars = 2 * KR + 2 * VR + 4 + 10 + 18 + kScaleRing;
     static constexpr int kOffMisc = kOffBar + kBars * 8;  // TMEM slot, flag
     static constexpr int kOffTables = kOffMisc + 8;
     static constexpr int bytes(int B) { return kOffTables + chunks::table_bytes(B) + 1024; }  // + alignment
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
     const uint32_t bar = base_a + L::kOffBar;
     const uint32_t kfull = bar, kempty = kfull + 8 * KR, vfull = kempty + 8 * KR, vempty = vfull + 8 * VR, wfull = vempty + 8 * VR,
                    wempty = wfull + 16, sfull = wempty + 16, pfull = sfull + 16, odone = pfull + 32, qfull = odone + 32, qfree = qfull + 16,
-                   xfull = qfree + 16, xdone = xfull + 8, turn = xdone + 8, drain = turn + 16, scfull = drain + 16;
+                   xfull = qfree + 16, xdone = xfull + 8, turn = xdone + 8, drain = turn + 16, qseen = drain + 16, scfull = qseen + 64;
     float4* s_scale = reinterpret_cast<float4*>(base + L::kOffScale);
     volatile int* s_nan = reinterpret_cast<volatile int*>(base + L::kOffNan);
     float* s_qf = reinterpret_cast<float*>(base + L::kOffQf);
@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
         if (!PAIR) mbar_init(qfree, 2);  // (both streams are done with the one block of queries)
         for (int i = 0; i < 4; ++i) mbar_init(pfull + 8 * i, 4);
         for (int i = 0; i < 2; ++i) mbar_init(qfull + 8 * i, kConvWarps);
+        for (int i = 0; i < 8; ++i) mbar_init(qseen + 8 * i, kConvWarps);
         mbar_init(xfull, 8);
         mbar_init(xdone, 8);
         mbar_init_fence();
@@ -517,7 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                     if ((p + B) % PASSES == 0) {
                         fence_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(qfull + 8 * (p / PASSES));
+                        if (lane == 0) {
+                            mbar_arrive(qfull + 8 * (p / PASSES));
+                            mbar_arrive(qseen + 8 * (4 * (p / PASSES) + segments % 4));
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < B; ++k) x[k] = ahead[k];
@@ -614,12 +618,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             if (nt <= 0) continue;
             const int limit = real && token < at.n ? at.L - at.n + token : -1;  // the last slot that the row sees
             const bool any = __any_sync(0xffffffffu, limit >= 0);
-            ok = warp_wait(qfull + (PAIR ? 8 * s : 0), segments & 1, lim);
-            if (!ok) break;
-            const float qf = s_qf[(segments & 1) * 2 * kRows + row];
             // ---- tiles ----
-            float ref = -INFINITY, l = 0.f;
+            float ref = -INFINITY, l = 0.f, qf = 0.f;
             const int ns = PAIR ? nt : (nt + 1 - s) / 2;
+            if (ns) {
+                // The rows' factors.  (Where segments have one tile, the queries of the next segment, and in time
+                // those behind them, can be ready before this warp has handed out the results of the last
+                // one: a barrier of two phases would be misread, so there are four, used in turn.)
+                ok = warp_wait(qseen + 8 * ((PAIR ? 4 * s : 0) + segments % 4), segments / 4 & 1, lim);
+                if (!ok) break;
+                qf = s_qf[(segments & 1) * 2 * kRows + row];
+            }
             for (int i = 0; i < ns && ok; ++i) {
                 const int x = PAIR ? i : 2 * i + s;  // tile of the segment
                 const uint32_t n_tile = tile + x, n_mine = had[s] + i;
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const float4 f = sc[4 * h + g];
-                        kc[g] = factor(f.x, qf);
+                        kc[g] = f.z == 0.f ? 1.f : factor(f.x, qf);  // (an absent page's keys stay -inf whatever q holds)
                         off[g] = f.y;
                         per_vs[g] = f.z;
                     }
@@ -915,7 +924,7 @@ struct FSmem {
     static_assert(kOffTables % 8 == 0, "alignment");
 };
 
-template <int D, int ROWS, int THREADS>
+template <int D, int ROWS, int THREADS, int RT>
 __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkArgs a) {
     using L = FSmem<D, ROWS>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -951,9 +960,9 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
         at.begin = (uint32_t)s_cursor[3];
         at.set(w, tab);
     }
-    // this thread's four rows; its KT keys, KL apart; its CP columns, CW side by side
-    constexpr int KT = ROWS * kKeys / (4 * THREADS), KL = kKeys / KT, CP = D * ROWS / (4 * THREADS), CW = CP < 4 ? CP : 4;
-    const int r0 = tid / KL * 4, kl = tid % KL;
+    // this thread's RT rows; its KT keys, KL apart; its CP columns, CW side by side
+    constexpr int KT = ROWS * kKeys / (RT * THREADS), KL = kKeys / KT, CP = D * ROWS / (RT * THREADS), CW = CP < 4 ? CP : 4;
+    const int r0 = tid / KL * RT, kl = tid % KL;
     auto column = [&](int j) { return (j / CW * KL + kl) * CW + j % CW; };
     for (; at.begin < g1; at.next(w, tab)) {
         const int t0 = at.first_tile(w, g0), t1 = at.end_tile(w, g1);
@@ -970,9 +979,9 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
             const int token = at.j * w.tb + tid / a.G;
             s_limit[tid] = real(tid) && token < at.n ? at.L - at.n + token : -1;
         }
-        float acc[4][CP];
+        float acc[RT][CP];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < CP; ++j) acc[i][j] = 0.f;
         for (int t = t0; t < t1; ++t) {
@@ -1021,20 +1030,20 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
             }
             __syncthreads();
             {
-                float z[4][KT];
+                float z[RT][KT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < RT; ++i)
 #pragma unroll
                     for (int j = 0; j < KT; ++j) z[i][j] = 0.f;
 #pragma unroll 4
                 for (int c = 0; c < D; c += 4) {
-                    float4 kx[KT], qx[4];
+                    float4 kx[KT], qx[RT];
 #pragma unroll
                     for (int j = 0; j < KT; ++j) kx[j] = *reinterpret_cast<const float4*>(sk + (kl + j * KL) * L::kStride + c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) qx[i] = *reinterpret_cast<const float4*>(sq + (r0 + i) * L::kStride + c);
+                    for (int i = 0; i < RT; ++i) qx[i] = *reinterpret_cast<const float4*>(sq + (r0 + i) * L::kStride + c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < RT; ++i)
 #pragma unroll
                         for (int j = 0; j < KT; ++j)
                             z[i][j] = fmaf(qx[i].x, kx[j].x, fmaf(qx[i].y, kx[j].y, fmaf(qx[i].z, kx[j].z, fmaf(qx[i].w, kx[j].w, z[i][j]))));
@@ -1044,7 +1053,7 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
                     const int key = kl + j * KL;
                     const bool there = s_there[key];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < RT; ++i)
                         sp[(r0 + i) * L::kStrideP + key] = there && k0 + key <= s_limit[r0 + i] ? z[i][j] * a.scale_log2 : -INFINITY;
                 }
             }
@@ -1074,16 +1083,16 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
             }
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RT; ++i) {
                 const float c = s_corr[r0 + i];
 #pragma unroll
                 for (int j = 0; j < CP; ++j) acc[i][j] *= c;
             }
 #pragma unroll 2
             for (int k = 0; k < kKeys; k += 4) {
-                float p[4][4], v[4][CP];
+                float p[RT][4], v[4][CP];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < RT; ++i)
                     *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(sp + (r0 + i) * L::kStrideP + k);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -1097,7 +1106,7 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < RT; ++i)
 #pragma unroll
                         for (int j = 0; j < CP; ++j) acc[i][j] = fmaf(p[i][e], v[e][j], acc[i][j]);
             }
@@ -1106,7 +1115,7 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
         const bool whole = t1 - t0 == at.tiles;
         const size_t part = (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * ROWS;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RT; ++i) {
             const float l = s_l[r0 + i];
             if (!real(r0 + i)) continue;
             float* out = static_cast<float*>(a.out) + place(r0 + i);
@@ -1137,7 +1146,10 @@ struct Plan {
 Plan plan_chunk(medusa_dtype dtype, int T, int G, int D) {
     const long long rows = (long long)T * G;
     const int sms = sm_count();
-    if (dtype == MEDUSA_F32) return rows <= 32 && G <= 16 ? Plan{16, kKeys, kSetupF32, 2 * sms, 2} : Plan{64, kKeys, kSetupF32, D == 64 ? 2 * sms : sms, 2};
+    if (dtype == MEDUSA_F32) {
+        if (rows <= 32 && G <= 16) return Plan{16, kKeys, kSetupF32, 2 * sms, 3};
+        return Plan{rows <= 64 ? 64 : 128, kKeys, kSetupF32, D == 64 ? 2 * sms : sms, 3};
+    }
     return rows <= kRows ? Plan{kRows, kTile, kSetup, sms, 3} : Plan{2 * kRows, kTile, kSetup, sms, 3};
 }
 
@@ -1153,9 +1165,9 @@ cudaError_t launch_merge(const ChunkArgs& a, cudaStream_t st) {
 
 // (the shared memory limit is the kernel's, not the call's, so it is always what the largest
 // batch takes: a call of few sequences on another thread must not lower it under this one)
-template <int D, int ROWS, int THREADS>
+template <int D, int ROWS, int THREADS, int RT>
 cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t st) {
-    auto kern = chunk_attn_q8_f32_kernel<D, ROWS, THREADS>;
+    auto kern = chunk_attn_q8_f32_kernel<D, ROWS, THREADS, RT>;
     constexpr int most = FSmem<D, ROWS>::bytes(q8::kMaxBatch);
     static_assert(most + 1024 <= q8::kMaxSmem, "the largest batch does not fit (1024: static arrays)");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -1244,8 +1256,14 @@ extern "C" int medusa_chunk_attention_q8(const void* q, medusa_dtype dtype, cons
     cudaStream_t st = as_stream(stream);
     cudaError_t e;
     if (dtype == MEDUSA_F32) {
-        e = p.rows == 16 ? (D == 64 ? launch_f32<64, 16, 256>(a, st) : launch_f32<128, 16, 256>(a, st))
-                         : (D == 64 ? launch_f32<64, 64, 256>(a, st) : launch_f32<128, 64, 512>(a, st));
+        if (D == 64)
+            e = p.rows == 16   ? launch_f32<64, 16, 256, 4>(a, st)
+                : p.rows == 64 ? launch_f32<64, 64, 256, 4>(a, st)
+                               : launch_f32<64, 128, 256, 8>(a, st);
+        else
+            e = p.rows == 16   ? launch_f32<128, 16, 256, 4>(a, st)
+                : p.rows == 64 ? launch_f32<128, 64, 512, 4>(a, st)
+                               : launch_f32<128, 128, 256, 8>(a, st);
     } else {
         CUtensorMap mk, mv;
         const long long rows = (long long)n_pages * Hkv * P;

@@ -95,8 +95,8 @@ extern "C" int medusa_rope_rows(const void* q, const void* k, medusa_dtype dtype
         return fail(MEDUSA_ERR_INVALID_ARG, "rope_rows: sizes must be positive");
     if (dtype != MEDUSA_F32 && dtype != MEDUSA_BF16)
         return fail(MEDUSA_ERR_UNSUPPORTED, "rope_rows: unknown dtype %d", (int)dtype);
-    if (D % 16 || D > 512 || B > 65535 || Hq > 1024 || Hkv > 1024)
-        return fail(MEDUSA_ERR_UNSUPPORTED, "rope_rows: head dim %d must be a multiple of 16 up to 512, at most 65535 sequences and 1024 heads", D);
+    if (D % 16 || D > 512 || B > 65535 || T > 1 << 24 || Hq > 1024 || Hkv > 1024)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "rope_rows: head dim %d must be a multiple of 16 up to 512, at most 65535 sequences, 2^24 rows and 1024 heads", D);
     if (int rc = rope::check_freqs("rope_rows", inv_freq, n_freq, D)) return rc;
     if (!q || !q_out || !kv_len || (Hkv > 0) != (k != nullptr) || (k != nullptr) != (k_out != nullptr))
         return fail(MEDUSA_ERR_INVALID_ARG, "rope_rows: null pointer");

@@ -241,3 +241,33 @@ def test_waits_that_run_out_are_reported_and_the_next_calls_are_correct(medusa, 
     assert np.isnan(hurt).any() and (np.isnan(hurt) | (hurt == before)).all()
     assert np.array_equal(run(), before)
     M.device_status()
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,P,hi,wide", [
+    (10, 4, 40, 40, 64, 64, 270, 0),     # two or three tiles a unit, units not cut
+    (40, 1, 20, 20, 128, 32, 100, 0),    # one tile a unit, five units a block
+    (40, 1, 20, 20, 128, 32, 300, 40),   # a wide table: units may be cut
+    (30, 20, 32, 16, 64, 16, 90, 60),
+    (8, 200, 16, 16, 128, 64, 60, 0),    # two streams' rows, one or two tiles
+])
+def test_many_short_units_with_nothing_in_the_caches(medusa, B, T, Hq, Hkv, D, P, hi, wide):
+    """A block takes up one unit after the other: their queries are made ready ahead of the softmax,
+    by one segment and, where segments have a tile, by two; cold memory changes who comes first."""
+    M, flush = medusa, torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        c = case(seed, B, T, Hq, Hkv, D, P, rng.integers(0, hi, B).tolist(), rng.integers(0, T, B).tolist(), "bf16")
+        c["table"] = np.concatenate([c["table"], np.full((B, wide), -1, np.int32)], 1)
+        args, last = tensors(c)
+        outs = []
+        for _ in range(3):
+            flush.zero_()
+            torch.cuda.synchronize()
+            outs.append(M.chunk_attention_q8(*args, last=last))
+            torch.cuda.synchronize()
+        M.device_status()
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+        if seed == 0:
+            some = slice(0, 6)
+            part = {**c, **{n: c[n][some] for n in ("q", "table", "kv_len", "last")}}
+            check(part, outs[0][some].double().cpu().numpy())
