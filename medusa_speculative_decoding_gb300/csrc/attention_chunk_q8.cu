@@ -924,7 +924,7 @@ struct FSmem {
     static_assert(kOffTables % 8 == 0, "alignment");
 };
 
-template <int D, int ROWS, int THREADS, int RT>
+template <int D, int ROWS, int THREADS>
 __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkArgs a) {
     using L = FSmem<D, ROWS>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -960,9 +960,9 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
         at.begin = (uint32_t)s_cursor[3];
         at.set(w, tab);
     }
-    // this thread's RT rows; its KT keys, KL apart; its CP columns, CW side by side
-    constexpr int KT = ROWS * kKeys / (RT * THREADS), KL = kKeys / KT, CP = D * ROWS / (RT * THREADS), CW = CP < 4 ? CP : 4;
-    const int r0 = tid / KL * RT, kl = tid % KL;
+    // this thread's four rows; its KT keys, KL apart; its CP columns, CW side by side
+    constexpr int KT = ROWS * kKeys / (4 * THREADS), KL = kKeys / KT, CP = D * ROWS / (4 * THREADS), CW = CP < 4 ? CP : 4;
+    const int r0 = tid / KL * 4, kl = tid % KL;
     auto column = [&](int j) { return (j / CW * KL + kl) * CW + j % CW; };
     for (; at.begin < g1; at.next(w, tab)) {
         const int t0 = at.first_tile(w, g0), t1 = at.end_tile(w, g1);
@@ -979,9 +979,9 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
             const int token = at.j * w.tb + tid / a.G;
             s_limit[tid] = real(tid) && token < at.n ? at.L - at.n + token : -1;
         }
-        float acc[RT][CP];
+        float acc[4][CP];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < CP; ++j) acc[i][j] = 0.f;
         for (int t = t0; t < t1; ++t) {
@@ -1030,20 +1030,20 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
             }
             __syncthreads();
             {
-                float z[RT][KT];
+                float z[4][KT];
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < KT; ++j) z[i][j] = 0.f;
 #pragma unroll 4
                 for (int c = 0; c < D; c += 4) {
-                    float4 kx[KT], qx[RT];
+                    float4 kx[KT], qx[4];
 #pragma unroll
                     for (int j = 0; j < KT; ++j) kx[j] = *reinterpret_cast<const float4*>(sk + (kl + j * KL) * L::kStride + c);
 #pragma unroll
-                    for (int i = 0; i < RT; ++i) qx[i] = *reinterpret_cast<const float4*>(sq + (r0 + i) * L::kStride + c);
+                    for (int i = 0; i < 4; ++i) qx[i] = *reinterpret_cast<const float4*>(sq + (r0 + i) * L::kStride + c);
 #pragma unroll
-                    for (int i = 0; i < RT; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int j = 0; j < KT; ++j)
                             z[i][j] = fmaf(qx[i].x, kx[j].x, fmaf(qx[i].y, kx[j].y, fmaf(qx[i].z, kx[j].z, fmaf(qx[i].w, kx[j].w, z[i][j]))));
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
                     const int key = kl + j * KL;
                     const bool there = s_there[key];
 #pragma unroll
-                    for (int i = 0; i < RT; ++i)
+                    for (int i = 0; i < 4; ++i)
                         sp[(r0 + i) * L::kStrideP + key] = there && k0 + key <= s_limit[r0 + i] ? z[i][j] * a.scale_log2 : -INFINITY;
                 }
             }
@@ -1083,16 +1083,16 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
             }
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 const float c = s_corr[r0 + i];
 #pragma unroll
                 for (int j = 0; j < CP; ++j) acc[i][j] *= c;
             }
 #pragma unroll 2
             for (int k = 0; k < kKeys; k += 4) {
-                float p[RT][4], v[4][CP];
+                float p[4][4], v[4][CP];
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
+                for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(sp + (r0 + i) * L::kStrideP + k);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -1106,7 +1106,7 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int i = 0; i < RT; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int j = 0; j < CP; ++j) acc[i][j] = fmaf(p[i][e], v[e][j], acc[i][j]);
             }
@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
         const bool whole = t1 - t0 == at.tiles;
         const size_t part = (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * ROWS;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float l = s_l[r0 + i];
             if (!real(r0 + i)) continue;
             float* out = static_cast<float*>(a.out) + place(r0 + i);
@@ -1146,10 +1146,7 @@ struct Plan {
 Plan plan_chunk(medusa_dtype dtype, int T, int G, int D) {
     const long long rows = (long long)T * G;
     const int sms = sm_count();
-    if (dtype == MEDUSA_F32) {
-        if (rows <= 32 && G <= 16) return Plan{16, kKeys, kSetupF32, 2 * sms, 3};
-        return Plan{rows <= 64 ? 64 : 128, kKeys, kSetupF32, D == 64 ? 2 * sms : sms, 3};
-    }
+    if (dtype == MEDUSA_F32) return rows <= 32 && G <= 16 ? Plan{16, kKeys, kSetupF32, 2 * sms, 2} : Plan{64, kKeys, kSetupF32, D == 64 ? 2 * sms : sms, 2};
     return rows <= kRows ? Plan{kRows, kTile, kSetup, sms, 3} : Plan{2 * kRows, kTile, kSetup, sms, 3};
 }
 
@@ -1165,9 +1162,9 @@ cudaError_t launch_merge(const ChunkArgs& a, cudaStream_t st) {
 
 // (the shared memory limit is the kernel's, not the call's, so it is always what the largest
 // batch takes: a call of few sequences on another thread must not lower it under this one)
-template <int D, int ROWS, int THREADS, int RT>
+template <int D, int ROWS, int THREADS>
 cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t st) {
-    auto kern = chunk_attn_q8_f32_kernel<D, ROWS, THREADS, RT>;
+    auto kern = chunk_attn_q8_f32_kernel<D, ROWS, THREADS>;
     constexpr int most = FSmem<D, ROWS>::bytes(q8::kMaxBatch);
     static_assert(most + 1024 <= q8::kMaxSmem, "the largest batch does not fit (1024: static arrays)");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -1256,14 +1253,8 @@ extern "C" int medusa_chunk_attention_q8(const void* q, medusa_dtype dtype, cons
     cudaStream_t st = as_stream(stream);
     cudaError_t e;
     if (dtype == MEDUSA_F32) {
-        if (D == 64)
-            e = p.rows == 16   ? launch_f32<64, 16, 256, 4>(a, st)
-                : p.rows == 64 ? launch_f32<64, 64, 256, 4>(a, st)
-                               : launch_f32<64, 128, 256, 8>(a, st);
-        else
-            e = p.rows == 16   ? launch_f32<128, 16, 256, 4>(a, st)
-                : p.rows == 64 ? launch_f32<128, 64, 512, 4>(a, st)
-                               : launch_f32<128, 128, 256, 8>(a, st);
+        e = p.rows == 16 ? (D == 64 ? launch_f32<64, 16, 256>(a, st) : launch_f32<128, 16, 256>(a, st))
+                         : (D == 64 ? launch_f32<64, 64, 256>(a, st) : launch_f32<128, 64, 512>(a, st));
     } else {
         CUtensorMap mk, mv;
         const long long rows = (long long)n_pages * Hkv * P;
