@@ -13,8 +13,10 @@
 // One CTA per (page that receives rows, up to four heads of K, of V or of the queries,
 // sequence).  The page's sines and cosines are formed once into shared memory, while the first
 // head's rows are on their way; a thread has pieces of sixteen values, both halves of eight
-// pairs, so that no value crosses threads.  Bound by HBM for prompts: rows, queries and codes
-// each pass once.
+// pairs, so that no value crosses threads.  130 us for four prompts of 2048 to 4096 rows, 32 heads
+// (503 MB, 3.9 TB/s; without the queries 88, of which kv_append_q8 takes 63): a CTA's steps follow one
+// another, lengths, rows, turns, the largest value, codes; 5 us for a token of sixteen sequences.
+// With 2 / 4 / 8 / 16 / 32 heads a CTA: 141 / 129 / 130 / 141 / 170 us.
 #include <algorithm>
 
 #include "append.cuh"

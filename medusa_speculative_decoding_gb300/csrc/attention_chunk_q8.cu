@@ -58,31 +58,32 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // ---------------------------------------------------------------------------
 // tcgen05 kernel (bf16 queries).
 //
-// Queries in the TMEM lanes; two softmax threads per query row, 64 keys of a tile each.
+// Queries in the TMEM lanes, a softmax thread per query row.
 //   scores  K's codes enter the product as they are.  A bf16 value has eight significant bits:
 //           q = q_hi + q_lo, an e4m3 and an e5m2 plane under one power of two per row.  What
 //           q_hi leaves of a value has three bits, which e5m2 holds down to 2^-16: the sum is
 //           exact for values down to 2^-13 of the row's largest, and off by 2^-21 of it below.
 //   output  a page's V scale (vs) enters the weights, w = 2^(x + log2 vs - m), x the score in
-//           log2 units and m the row's reference, the largest x + log2 vs when it was set: a
-//           page's scale then counts only as far as its weight does.  Weights are rounded to
-//           f16, 11 bits where the model's bf16 has 8; 2^kLift times w stays below 2^15 until
-//           references move and keeps its bits down to 2^-22 of the row's largest.  V's codes
-//           are converted to f16, exactly, by warps of their own: the tensor core multiplies
-//           types of one kind only, and three 8-bit planes of the weights would cost the
-//           softmax warps more than the whole conversion.
+//           log2 units and m the row's reference, the largest x + log2 vs when it was set (to a
+//           whole number above it, so that what moves with it keeps its bits): a page's scale then
+//           counts only as far as its weight does.  Weights are rounded to f16, 11 bits where the
+//           model's bf16 has 8; 2^kLift times w stays below 2^15 until references move and keeps
+//           its bits down to 2^-22 of the row's largest.  V's codes are converted to f16, exactly,
+//           by warps of their own: the tensor core multiplies types of one kind only, and three
+//           8-bit planes of the weights would cost the softmax warps more than the conversion.
 //   sums    of w / vs, in float32, unrounded.
 //
 // Scales are those of a page: 16 neighbouring keys share theirs, so they cost a thread one
 // load and two instructions per 16 scores.
 //
-// Two streams per CTA (two softmax warpgroups each, one per 64 keys of a tile), each with its own S and O in TMEM, so that
-// one stream's softmax runs while the tensor core works for the other:
+// Two streams per CTA (a softmax warpgroup and an MMA warp each), each with its own S and O in
+// TMEM, so that one stream's softmax runs while the tensor core works for the other:
 //   PAIR = true   blocks of 256 rows, 128 a stream; both use every tile
 //   PAIR = false  blocks of up to 128 rows (plain decoding, short chunks): the streams take
 //                 alternate tiles, each an online softmax of its own, joined at the end
-// Steps x = 0, 1, 2, ...: stream x & 1, tile x / 2 (or x).  The MMA warp issues PV(x), then
-// S(x + 2), so that a stream's scores being in also says that its last PV is done.
+// A tile: S = q K^T into TMEM; the softmax warps write the weights of its first 64 keys over S, then
+// those of the others; the MMA warp adds each half's PV to O, and forms the next S behind the second.
+// So a stream's scores being in says that its PV before are done.
 //
 // Warps 0-3, 4-7 softmax of stream 0, 1, 8-11 queries to planes and V codes to f16, 12, 13 MMA of
 // stream 0, 1, 14 pages, scales and TMA, 15 rows of units that see nothing.
@@ -92,12 +93,24 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // slot.  A row that sees it, and so all rows that see any, is made NaN when its results go out.
 //
 // Every wait is bounded; a CTA that gives up marks its results NaN.
+//
+// Measured, merge included: 486 us for four prompts of 2048 to 4096 rows, 32 heads (329 GFLOP
+// counted, 677 TFLOP/s); 168 us for one of 4096 rows, 32 / 8 heads (816 TFLOP/s); 88 us for 512 rows
+// on 8192 (808); 75 us for one token of sixteen sequences of 777 to 16384 (282 MB, 3.8 TB/s).  A
+// tile takes about 4200 cycles where its products take 2300: per stream two halves of 1300 to 1500
+// cycles (scores out of TMEM 200, their maximum 200, weights 600, handing over 150) and 1300 from
+// the last weights to the next scores, of which the other stream hides a part.  One MMA warp for
+// both streams 10% slower; scores of 64 keys, two buffers a stream, cost as many cycles an instruction
+// as those of 128 (75) and took 40% longer; two threads a row (four softmax warpgroups) 30%.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128, kRows = 128;  // keys of a tile, rows of a stream
 constexpr int kHalf = kTile / 2;           // keys whose weights are handed over together
 constexpr int kThreads = 512, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kTmaWarp = 14, kZeroWarp = 15;  // an MMA warp per stream
 constexpr int kGroups = kTile / 16;  // keys that share a scale
 constexpr float kLift = 8.f, kMove = 7.f;
+// Tiles that a unit counts more for its queries, first references and results.  Measured with 1 / 2 /
+// 4 / 6 / 8: one prompt of 4096 rows 264 / 204 / 166 / 168 / 175 us, 512 rows on 8192 91 / 90 / 87 / 87
+// / 89, sixteen sequences of one token 79 / 77 / 75 / 76 / 78.
 constexpr int kSetup = 4;
 constexpr uint32_t kDrainCycles = (uint32_t)kDefaultWaitCycles;
 
@@ -908,7 +921,9 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkA
 // float32 kernel.  A CTA works through its share of (unit, tile) pairs; a unit has ROWS query
 // rows, 16 or 64, a tile 64 keys, dequantised into shared memory once for all rows; scores,
 // softmax and sums are float32.  A thread has four rows and KT keys (then CP columns) of each
-// product.  Bound by issue and shared memory, small calls by latency.
+// product.  Bound by shared memory and issue (147 us for two chunks of 300 rows on 500, 16 / 4 heads, 22
+// TFLOP/s), small calls by latency (14 us for nine rows, four heads of 64 and 137 keys).  One token goes
+// through a block of 16 rows: 540 us for sixteen sequences of 777 to 16384 keys, 8 heads of 4 rows.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 64, kSetupF32 = 1;
 
