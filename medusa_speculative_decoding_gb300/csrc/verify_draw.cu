@@ -36,8 +36,10 @@ constexpr int kBatch = 4;         // float4 of a thread with their loads in flig
 constexpr int kMaxCluster = 8;
 constexpr int kSlice = 8192;      // values of a CTA, where the cluster can be that large
 constexpr int kMaxNodes = 512;
-// Bytes of rows up to which drawing from all of them beats walking.
-constexpr long long kAllRows = 48ll << 20;
+// Bytes of rows up to which drawing from all of them beats walking: trees of 64 nodes took 10 us against 21 at
+// 8 MB (one, V = 32000), 25 against 19 at 31 MB (one, V = 128256), 37 against 31 (four, V = 32000) and 64 against
+// 39 at 62 MB (eight).
+constexpr long long kAllRows = 16ll << 20;
 
 struct DrawArgs {
     const float *probs, *u;
