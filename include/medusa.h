@@ -526,7 +526,9 @@ int medusa_kv_append_rope_q8(const void* k_rows, const void* v_rows, medusa_dtyp
 /* exact down to 2^-13 of its row's largest |q|, 2^-21 of that below.  In the sum over   */
 /* V, dtype float32 takes the weights as they are, dtype bf16 takes weight * V scale      */
 /* rounded to 11 bits down to 2^-22 of the row's largest such product (fewer down to       */
-/* 2^-32).  A key with less than 2^-100 of that product may be left out of the row          */
+/* 2^-32).  T = 1 in bf16 with Hq/Hkv <= 16 is computed as 6a with a tree of no rows: q and     */
+/* weights are rounded as there, and a NaN code of V makes its own column of out NaN, not the     */
+/* row.  A key with less than 2^-100 of that product may be left out of the row          */
 /* altogether (dtype bf16, as in 6a).                                                     */
 /* kv_len is clamped to [0, M*P], last to [-1, T-1].  Keys of a page that is not in         */
 /* [0, n_pages) or whose scale is not readable count as absent.  A row that sees a key is NaN */

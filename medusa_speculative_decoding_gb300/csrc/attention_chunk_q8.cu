@@ -7,7 +7,8 @@
 // and values in the pages like those before them.  Row i sees the slots [0, L - n + i]:
 //   out = softmax(scale * q.k) v,   k = code * K scale, v = code * V scale
 //
-//   chunk_attn_q8_umma_kernel : bf16, on the tensor cores
+//   chunk_attn_q8_umma_kernel : bf16, on the tensor cores (single rows go to the kernel of attention_q8.cu:
+//                               single_row)
 //   chunk_attn_q8_f32_kernel  : float32, on the CUDA cores
 //   chunk_merge_kernel        : joins the partial results of units that several CTAs share
 //                               (chunks.cuh)
@@ -79,7 +80,7 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 // Two streams per CTA (a softmax warpgroup and an MMA warp each), each with its own S and O in
 // TMEM, so that one stream's softmax runs while the tensor core works for the other:
 //   PAIR = true   blocks of 256 rows, 128 a stream; both use every tile
-//   PAIR = false  blocks of up to 128 rows (plain decoding, short chunks): the streams take
+//   PAIR = false  blocks of up to 128 rows (short chunks): the streams take
 //                 alternate tiles, each an online softmax of its own, joined at the end
 // A tile: S = q K^T into TMEM; the softmax warps write the weights of its first 64 keys over S, then
 // those of the others; the MMA warp adds each half's PV to O, and forms the next S behind the second.
@@ -96,7 +97,7 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
 //
 // Measured, merge included: 486 us for four prompts of 2048 to 4096 rows, 32 heads (329 GFLOP
 // counted, 677 TFLOP/s); 168 us for one of 4096 rows, 32 / 8 heads (816 TFLOP/s); 88 us for 512 rows
-// on 8192 (808); 75 us for one token of sixteen sequences of 777 to 16384 (282 MB, 3.8 TB/s).  A
+// on 8192 (808).  A
 // tile takes about 4200 cycles where its products take 2300: per stream two halves of 1300 to 1500
 // cycles (scores out of TMEM 200, their maximum 200, weights 600, handing over 150) and 1300 from
 // the last weights to the next scores, of which the other stream hides a part.  One MMA warp for
@@ -110,7 +111,7 @@ constexpr int kGroups = kTile / 16;  // keys that share a scale
 constexpr float kLift = 8.f, kMove = 7.f;
 // Tiles that a unit counts more for its queries, first references and results.  Measured with 1 / 2 /
 // 4 / 6 / 8: one prompt of 4096 rows 264 / 204 / 166 / 168 / 175 us, 512 rows on 8192 91 / 90 / 87 / 87
-// / 89, sixteen sequences of one token 79 / 77 / 75 / 76 / 78.
+// / 89.
 constexpr int kSetup = 4;
 constexpr uint32_t kDrainCycles = (uint32_t)kDefaultWaitCycles;
 
@@ -1165,6 +1166,11 @@ Plan plan_chunk(medusa_dtype dtype, int T, int G, int D) {
     return rows <= kRows ? Plan{kRows, kTile, kSetup, sms, 3} : Plan{2 * kRows, kTile, kSetup, sms, 3};
 }
 
+// One row a sequence and at most 16 query heads a KV head: the kernel that has the keys in the TMEM
+// lanes and the rows in the columns, whose work is in proportion to 16 rows instead of 128.  One token of
+// sixteen sequences of 777 to 16384, 32 / 8 heads (282 MB): 74 us here, 54 there.
+bool single_row(medusa_dtype dtype, int T, int G) { return dtype == MEDUSA_BF16 && T == 1 && G <= 16; }
+
 size_t ws_bytes_chunk(const Plan& p, int D) { return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float) + p.ctas * sizeof(int4); }
 
 template <typename T, int D>
@@ -1221,7 +1227,7 @@ using namespace medusa;
 
 extern "C" size_t medusa_chunk_attention_q8_workspace(int B, int T, int Hq, int Hkv, int D, medusa_dtype dtype) {
     if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128)) return 0;
-    return ws_bytes_chunk(plan_chunk(dtype, T, Hq / Hkv, D), D);
+    return single_row(dtype, T, Hq / Hkv) ? row_attention_q8_workspace(Hq / Hkv, D) : ws_bytes_chunk(plan_chunk(dtype, T, Hq / Hkv, D), D);
 }
 
 extern "C" int medusa_chunk_attention_q8(const void* q, medusa_dtype dtype, const void* k_pages, const void* v_pages,
@@ -1245,9 +1251,12 @@ extern "C" int medusa_chunk_attention_q8(const void* q, medusa_dtype dtype, cons
         return fail(MEDUSA_ERR_INVALID_ARG, "%s: scale must be positive, scale * log2(e) finite", who);
     const int G = Hq / Hkv;
     const Plan p = plan_chunk(dtype, T, G, D);
-    const size_t need = ws_bytes_chunk(p, D);
+    const size_t need = medusa_chunk_attention_q8_workspace(B, T, Hq, Hkv, D, dtype);
     if (!ws || ws_bytes < need) return fail(MEDUSA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", who, need);
     if (!aligned16(ws)) return fail(MEDUSA_ERR_INVALID_ARG, "%s: ws must be 16-byte aligned", who);
+    if (single_row(dtype, T, G))
+        return row_attention_q8(who, q, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, last, B, Hq, Hkv, D, P, n_pages, M, scale, out,
+                                ws, stream);
     ChunkArgs a{};
     a.q = q;
     a.k_pages = (const uint8_t*)k_pages; a.v_pages = (const uint8_t*)v_pages;

@@ -34,8 +34,8 @@ struct AttnQ8Args {
     const void *q, *k_tree, *v_tree;
     const uint8_t *k_pages, *v_pages;
     const float *k_scale, *v_scale;
-    const int32_t *page_table, *kv_len;
-    const uint64_t* mask;
+    const int32_t *page_table, *kv_len, *last;  // last: NULL, or negative where a sequence counts as empty
+    const uint64_t* mask;                       // NULL: no row sees a tree row
     void* out;
     float* part_o;   // ws [2 * ctas][rows][D]: sums relative to the row's reference
     float2* part_ml;  // ws [2 * ctas][rows]: (reference in log2 units, sum)
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
     if (warp == 0) tmem_alloc(tmem_slot, kCols);
     pdl_wait();
     pdl_trigger();
-    q8::tile_offsets(w, a.kv_len, first);
+    q8::tile_offsets(w, a.kv_len, first, a.last);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(kUThreads, 1) tree_attn_q8_umma_kernel(
                 const uint32_t* mask = reinterpret_cast<const uint32_t*>(a.mask);
                 for (int i = tid; i < L::kRowsBlock * 16; i += kUSoftmax) {
                     const int r = i >> 4, word = i & 15;
-                    if (word < 2 * a.W) s_mask[i] = r < nrows ? __ldg(mask + (size_t)((row0 + r) / a.G) * (2 * a.W) + word) : 0u;
+                    if (word < 2 * a.W) s_mask[i] = a.mask && r < nrows ? __ldg(mask + (size_t)((row0 + r) / a.G) * (2 * a.W) + word) : 0u;
                 }
             }
         };
@@ -1491,42 +1491,17 @@ cudaError_t launch_umma(const CUtensorMap (&m)[4], AttnQ8Args& a, const Plan& p,
     return e;
 }
 
-}  // namespace
-}  // namespace medusa
-
-using namespace medusa;
-
-extern "C" size_t medusa_tree_attention_q8_workspace(int B, int N, int Hq, int Hkv, int D, medusa_dtype dtype) {
-    if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128)) return 0;
-    return ws_bytes_q8(plan_q8(dtype, N, Hq / Hkv, D), D);
-}
-
-extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype,
-                                        const void* k_pages, const void* v_pages, const float* k_scale,
-                                        const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
-                                        const uint64_t* mask, int B, int N, int Hq, int Hkv, int D, int P,
-                                        int n_pages, int M, float scale, void* out, void* ws, size_t ws_bytes,
-                                        void* stream) {
-    if (int rc = check_attn_q8(B, N, Hq, Hkv, D, P, n_pages, M)) return rc;
-    if (dtype != MEDUSA_F32 && dtype != MEDUSA_BF16)
-        return fail(MEDUSA_ERR_UNSUPPORTED, "tree_attention_q8: unknown dtype %d", (int)dtype);
-    if (!q || !k_tree || !v_tree || !k_pages || !v_pages || !k_scale || !v_scale || !page_table || !kv_len || !mask || !out)
-        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: null pointer");
-    if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_pages) || !aligned16(v_pages) ||
-        !aligned16(out))
-        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: q, tree rows, pages and out must be 16-byte aligned");
-    if (!(scale > 0.f) || !(scale * kLog2e <= FLT_MAX))
-        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: scale must be positive, scale * log2(e) finite");
+// Arguments checked, workspace large enough.
+int run_attn_q8(const char* who, const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype, const void* k_pages,
+                const void* v_pages, const float* k_scale, const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
+                const int32_t* last, const uint64_t* mask, int B, int N, int Hq, int Hkv, int D, int P, int n_pages, int M, float scale,
+                void* out, void* ws, void* stream) {
     const Plan p = plan_q8(dtype, N, Hq / Hkv, D);
-    const size_t need = ws_bytes_q8(p, D);
-    if (!ws || ws_bytes < need)
-        return fail(MEDUSA_ERR_WORKSPACE, "tree_attention_q8: workspace of %zu bytes needed", need);
-    if (!aligned16(ws)) return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: ws must be 16-byte aligned");
     AttnQ8Args a{};
     a.q = q; a.k_tree = k_tree; a.v_tree = v_tree;
     a.k_pages = (const uint8_t*)k_pages; a.v_pages = (const uint8_t*)v_pages;
     a.k_scale = k_scale; a.v_scale = v_scale;
-    a.page_table = page_table; a.kv_len = kv_len; a.mask = mask; a.out = out;
+    a.page_table = page_table; a.kv_len = kv_len; a.last = last; a.mask = mask; a.out = out;
     a.part_o = (float*)ws;
     a.part_ml = (float2*)((float*)ws + (size_t)2 * p.ctas * p.rows * D);
     a.plan = (int4*)(a.part_ml + (size_t)2 * p.ctas * p.rows);
@@ -1537,7 +1512,7 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
     const bool whole = tiles <= p.whole && units <= 1 << 20;  // (share_begin counts in 32 bits)
     a.work = q8::Work{B, N, Hkv * a.qblocks, p.keys, p.setup, M * P, whole && units < p.ctas ? (int)units : p.ctas, whole};
     if ((long long)B * a.work.U * (((long long)M * P + p.keys - 1) / p.keys + (N + p.keys - 1) / p.keys + p.setup) > 0x7fffffffll)
-        return fail(MEDUSA_ERR_UNSUPPORTED, "tree_attention_q8: %d sequences of up to %lld tokens are too many tiles", B,
+        return fail(MEDUSA_ERR_UNSUPPORTED, "%s: %d sequences of up to %lld tokens are too many tiles", who, B,
                     (long long)M * P);
     a.scale_log2 = scale * kLog2e;
     cudaStream_t st = as_stream(stream);
@@ -1563,6 +1538,50 @@ extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const
                                : launch_umma<128, 64, true>(m, a, p, st);
     }
     if (e != cudaSuccess)
-        return fail(MEDUSA_ERR_CUDA, "tree_attention_q8: launch failed: %s", cudaGetErrorString(e));
+        return fail(MEDUSA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return MEDUSA_OK;
+}
+}  // namespace
+
+size_t row_attention_q8_workspace(int G, int D) { return ws_bytes_q8(plan_q8(MEDUSA_BF16, 1, G, D), D); }
+
+// (The tile of tree rows that a unit has stays: no mask, so no row sees any of it, and what lies in it, here
+// the first Hkv rows of q, does not matter.)
+int row_attention_q8(const char* who, const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                     const float* v_scale, const int32_t* page_table, const int32_t* kv_len, const int32_t* last, int B, int Hq,
+                     int Hkv, int D, int P, int n_pages, int M, float scale, void* out, void* ws, void* stream) {
+    return run_attn_q8(who, q, q, q, MEDUSA_BF16, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, last, nullptr, B, 1, Hq, Hkv, D,
+                       P, n_pages, M, scale, out, ws, stream);
+}
+}  // namespace medusa
+
+using namespace medusa;
+
+extern "C" size_t medusa_tree_attention_q8_workspace(int B, int N, int Hq, int Hkv, int D, medusa_dtype dtype) {
+    if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128)) return 0;
+    return ws_bytes_q8(plan_q8(dtype, N, Hq / Hkv, D), D);
+}
+
+extern "C" int medusa_tree_attention_q8(const void* q, const void* k_tree, const void* v_tree, medusa_dtype dtype,
+                                        const void* k_pages, const void* v_pages, const float* k_scale,
+                                        const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
+                                        const uint64_t* mask, int B, int N, int Hq, int Hkv, int D, int P,
+                                        int n_pages, int M, float scale, void* out, void* ws, size_t ws_bytes,
+                                        void* stream) {
+    if (int rc = check_attn_q8(B, N, Hq, Hkv, D, P, n_pages, M)) return rc;
+    if (dtype != MEDUSA_F32 && dtype != MEDUSA_BF16)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "tree_attention_q8: unknown dtype %d", (int)dtype);
+    if (!q || !k_tree || !v_tree || !k_pages || !v_pages || !k_scale || !v_scale || !page_table || !kv_len || !mask || !out)
+        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: null pointer");
+    if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_pages) || !aligned16(v_pages) ||
+        !aligned16(out))
+        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: q, tree rows, pages and out must be 16-byte aligned");
+    if (!(scale > 0.f) || !(scale * kLog2e <= FLT_MAX))
+        return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: scale must be positive, scale * log2(e) finite");
+    const size_t need = ws_bytes_q8(plan_q8(dtype, N, Hq / Hkv, D), D);
+    if (!ws || ws_bytes < need)
+        return fail(MEDUSA_ERR_WORKSPACE, "tree_attention_q8: workspace of %zu bytes needed", need);
+    if (!aligned16(ws)) return fail(MEDUSA_ERR_INVALID_ARG, "tree_attention_q8: ws must be 16-byte aligned");
+    return run_attn_q8("tree_attention_q8", q, k_tree, v_tree, dtype, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, nullptr, mask, B,
+                       N, Hq, Hkv, D, P, n_pages, M, scale, out, ws, stream);
 }

@@ -103,10 +103,12 @@ struct Offsets {
     __device__ __forceinline__ uint32_t total(const Work& w) const { return first[w.B]; }
 };
 
-// Fills the tables; called by every thread of the block.
-__device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __restrict__ kv_len, const Offsets& t) {
+// Fills the tables; called by every thread of the block.  last, where given: a sequence whose
+// last is negative counts as one without slots.
+__device__ __forceinline__ void tile_offsets(const Work& w, const int32_t* __restrict__ kv_len, const Offsets& t,
+                                             const int32_t* __restrict__ last = nullptr) {
     for (int b = threadIdx.x; b < w.B; b += blockDim.x) {
-        const int L = w.len(kv_len, b);
+        const int L = last && last[b] < 0 ? 0 : w.len(kv_len, b);
         t.rest[b] = (uint8_t)(L ? (L - 1) % w.T : 0);
         t.first[b + 1] = (uint32_t)w.U * w.span(L);
     }
@@ -186,4 +188,11 @@ __device__ __forceinline__ bool next_segment(const Work& w, const Offsets& t, ui
 }
 
 }  // namespace q8
+
+// Attention of one row a sequence over the slots that it holds, at most 16 query heads a KV head,
+// bf16 (attention_q8.cu; the arguments are checked, the workspace is large enough).
+size_t row_attention_q8_workspace(int G, int D);
+int row_attention_q8(const char* who, const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                     const float* v_scale, const int32_t* page_table, const int32_t* kv_len, const int32_t* last, int B, int Hq,
+                     int Hkv, int D, int P, int n_pages, int M, float scale, void* out, void* ws, void* stream);
 }  // namespace medusa

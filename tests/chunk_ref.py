@@ -144,19 +144,23 @@ def attention_tolerance(q, k_pages, table, kv_len, v_scale, ref, bf16):
     magnitudes.  bf16: q enters to 2^-21 of its row's largest; weights are rounded to f16, 2^-11,
     and below its normal range to half of its least step, 2^-25, in units of which the row's
     largest weight * V scale is at least 2^8: 2^-33, times a code of at most 448 and the V scale, for
-    each key; the output rounds to bf16: 2^-8 (float32: 2^-24)."""
+    each key; the output rounds to bf16: 2^-8 (float32: 2^-24).
+    bf16, T = 1 and at most 16 query heads a KV head, which is computed as a tree of no rows: q enters to
+    2^-17 of the largest of its block (all of q here), weights have 9 bits, 2^-9, and below that half of
+    e5m2's least step, 2^-17, in planes that hold at least 2^9 for the largest weight * V scale: 2^-26."""
     out, spread, bounds = ref
+    row = bf16 and q.shape[1] == 1 and q.shape[2] <= 16 * k_pages.shape[1]
     keys = min(int(kv_len.max()), table.shape[1] * k_pages.shape[2])
     D = q.shape[3]
     e = (D + 8) * U * bounds[..., 0] + 8 * U * 128
     per = (2 * keys + 64) * U
     if bf16:
-        e = e + 2.0 ** -21 * np.abs(q).max(-1) * bounds[..., 1]
-        per = per + 2.0 ** -11
+        e = e + (2.0 ** -17 * np.abs(q).max() if row else 2.0 ** -21 * np.abs(q).max(-1)) * bounds[..., 1]
+        per = per + (2.0 ** -9 if row else 2.0 ** -11)
     tol = spread * (2.1 * e[..., None] + per)
     if bf16:
         vs = np.where(np.isfinite(v_scale), v_scale, 0)
-        tol = tol + keys * 2.0 ** -33 * 448 * vs[vs <= 2.0 ** 64].max(initial=0)
+        tol = tol + keys * (2.0 ** -26 if row else 2.0 ** -33) * 448 * vs[vs <= 2.0 ** 64].max(initial=0)
     return tol + np.abs(out) * (2.0 ** -8 if bf16 else 2.0 ** -24) + 1e-30
 
 
