@@ -9,11 +9,12 @@
 //   p_0 + ... + p_v > u_d * (p_0 + ... + p_{V-1}).
 //
 // A row has V boundaries, each of which could fall next to u: sums in float32 would pick
-// another token in V * 2^-23 of the draws, 1.5% at V = 128256.  So sums have 48 bits where they
-// meet: a thread adds sixteen values as two float32 sums, of their multiples of 2^-18 (exact) and
-// of what is left (below 2^-15, off by 2^-35 of its terms at most), and everything from there on is
-// a pair of float32, high and low part (in double, of which an SM adds two a cycle, the draws of
-// 64 rows of 32000 took 40 us instead of 6).
+// another token in V * 2^-23 of the draws, 1.5% at V = 128256.  So a sum is a pair of float32, high
+// and low part (in double, of which an SM adds two a cycle, the draws of 64 rows of 32000 took 40 us
+// instead of 6).  A thread adds sixteen values in float32 and, beside them, what each addition rounded
+// away, which is exact: 2^-24 of the sum at most, so that the sixteen of them are off by 2^-40 of it
+// whatever the values' size.  From there on pairs are added, off by 2^-46 of the result each time, at
+// most some 270 one after the other (V = 2^24): 2^-37 of a row's total in all at most.
 //
 // A cluster of CTAs draws from one row: each CTA sums a contiguous slice, the totals are
 // pushed to every CTA, and the one whose slice holds the number finds the token in it.
@@ -132,15 +133,15 @@ __device__ __forceinline__ int draw(const DrawArgs& a, const float* row, float u
             const int v = v0 + 128 * k + 4 * lane;
             x[k] = v < end ? values4(row, v, end, aligned) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float hi = 0.f, lo = 0.f;
+        float hi = 0.f, lo = 0.f;  // lo: what hi's additions rounded away
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const float y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float h = __fsub_rn(__fadd_rn(y[i], 48.f), 48.f);  // to a multiple of 2^-18
-                hi = __fadd_rn(hi, h);
-                lo = __fadd_rn(lo, __fsub_rn(y[i], h));
+                const float2 t = two_sum(hi, y[i]);
+                hi = t.x;
+                lo = __fadd_rn(lo, t.y);
             }
         }
         sum = add(sum, two_sum(hi, lo));
