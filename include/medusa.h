@@ -329,7 +329,8 @@ int medusa_verify_accept_chain(const float* p, const float* q, const int32_t* dr
 /*   parent, depth [N] from the layout; u [B,Dmax+1] float                         */
 /* accept_len, best_node, path_nodes, next_tok as in 4a (next_tok: the drawn token    */
 /* that ended the walk; -1: a row without any weight).  A node whose parent is not     */
-/* below it is never reached.                                                        */
+/* below it is never reached.  The d of a node is the number of steps from the root by   */
+/* parent; depth has to hold the same and is not looked at.                             */
 /* Limits: N <= 512, Dmax < 512, B <= 65535, V <= 2^24.                                */
 /* ------------------------------------------------------------------------- */
 size_t medusa_verify_draw_workspace(int B, int N, int V);

@@ -44,7 +44,7 @@ constexpr long long kAllRows = 16ll << 20;
 
 struct DrawArgs {
     const float *probs, *u;
-    const int32_t *cand, *parent, *depth;
+    const int32_t *cand, *parent;
     int32_t* drawn;  // ws [B][N]
     int32_t *accept_len, *best_node, *path_nodes, *next_tok;
     int B, N, V, Dmax, slice;  // slice: values of a CTA, a multiple of 128 * kWarps
@@ -116,10 +116,11 @@ __device__ __forceinline__ float4 values4(const float* row, int v, int end, bool
     return make_float4(x[0], x[1], x[2], x[3]);
 }
 
-// The token drawn from row[0 .. V) with u, for all threads of the cluster (-1: the row has no
-// weight).  Called by every thread of the cluster's CTAs, which arrived at the cluster's barrier before
-// the first call.
-__device__ __forceinline__ int draw(const DrawArgs& a, const float* row, float u, DrawSmem& s, int rank, int ctas, bool first) {
+// The token drawn from row[0 .. V) with the number that `number` gives (called by the first warp, behind
+// a barrier of the block), for all threads of the cluster (-1: the row has no weight).  Called by every
+// thread of the cluster's CTAs, which arrived at the cluster's barrier before the first call.
+template <typename Number>
+__device__ __forceinline__ int draw(const DrawArgs& a, const float* row, Number number, DrawSmem& s, int rank, int ctas, bool first) {
     using namespace umma;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool aligned = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
@@ -163,7 +164,7 @@ __device__ __forceinline__ int draw(const DrawArgs& a, const float* row, float u
         // Every CTA finds the same CTA of the cluster, and that one the warp's part and the token.
         const float2 part = lane < ctas ? s.total[lane] : none;
         const float2 all = shfl2(scan(part), 31);
-        const float un = fmaxf(u, 0.f), ph = __fmul_rn(un, all.x);
+        const float un = fmaxf(number(), 0.f), ph = __fmul_rn(un, all.x);
         const float2 target = two_sum(ph, __fadd_rn(__fmaf_rn(un, all.x, -ph), __fmul_rn(un, all.y)));
         float2 base = none;
         bool over;
@@ -240,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) draw_walk_kernel(const DrawArgs a
     int node = 0, token = -1, steps = 0;
     if (threadIdx.x == 0) s_path[0] = 0;
     for (;;) {
-        token = draw(a, a.probs + ((size_t)b * a.N + node) * a.V, a.u[(size_t)b * (a.Dmax + 1) + steps], s, rank, ctas, steps == 0);
+        const float u = a.u[(size_t)b * (a.Dmax + 1) + steps];
+        token = draw(a, a.probs + ((size_t)b * a.N + node) * a.V, [=] { return u; }, s, rank, ctas, steps == 0);
         if (steps == a.Dmax) break;
         const int child = child_of(s_parent, s_cand, a.N, node, token, &s_child);
         if (child == a.N) break;
@@ -255,12 +257,25 @@ __global__ void __launch_bounds__(kThreads, 2) draw_walk_kernel(const DrawArgs a
 
 __global__ void __launch_bounds__(kThreads, 2) draw_rows_kernel(const DrawArgs a) {
     __shared__ DrawSmem s;
-    const int ctas = gridDim.x, rank = blockIdx.x, node = blockIdx.y, b = blockIdx.z;
+    __shared__ int s_parent[kMaxNodes];
+    __shared__ float s_u[kMaxNodes];
+    static_assert(kThreads >= kMaxNodes, "one node and one number a thread");
+    const int ctas = gridDim.x, rank = blockIdx.x, node = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     umma::cluster_arrive_relaxed();
     pdl_wait();
     pdl_trigger();
-    const int d = min(max(a.depth[node], 0), a.Dmax);
-    const int token = draw(a, a.probs + ((size_t)b * a.N + node) * a.V, a.u[(size_t)b * (a.Dmax + 1) + d], s, rank, ctas, true);
+    if (tid < a.N) s_parent[tid] = a.parent[tid];
+    if (tid <= a.Dmax) s_u[tid] = a.u[(size_t)b * (a.Dmax + 1) + tid];
+    // The steps that a walk takes to this node; any number where none gets here.
+    auto number = [&] {
+        int d = 0;
+        for (int j = node; j > 0 && d < a.Dmax; ++d) {
+            const int up = s_parent[j];
+            j = up < j ? up : 0;
+        }
+        return s_u[d];
+    };
+    const int token = draw(a, a.probs + ((size_t)b * a.N + node) * a.V, number, s, rank, ctas, true);
     if (rank == 0 && threadIdx.x == 0) a.drawn[(size_t)b * a.N + node] = token;
 }
 
@@ -319,7 +334,7 @@ extern "C" int medusa_verify_accept_tree_draw(const float* probs, const int32_t*
         return fail(MEDUSA_ERR_WORKSPACE, "verify_accept_tree_draw: workspace of %zu bytes needed", need);
     if (reinterpret_cast<uintptr_t>(ws) & 3u)
         return fail(MEDUSA_ERR_INVALID_ARG, "verify_accept_tree_draw: ws must be 4-byte aligned");
-    DrawArgs a{probs, u, cand, parent, depth, (int32_t*)ws, accept_len, best_node, path_nodes, next_tok, B, N, V, Dmax, 0};
+    DrawArgs a{probs, u, cand, parent, (int32_t*)ws, accept_len, best_node, path_nodes, next_tok, B, N, V, Dmax, 0};
     const int ctas = std::min(kMaxCluster, (V + kSlice - 1) / kSlice), unit = 128 * kWarps;
     a.slice = (int)(((long long)(V + ctas - 1) / ctas + unit - 1) / unit * unit);
     cudaStream_t st = as_stream(stream);
