@@ -485,8 +485,9 @@ int medusa_kv_pages_compact(void* k_pages, void* v_pages, float* k_scale, float*
 /* where depth is NULL).  The first 2 n_freq values of a head are pairs (i,      */
 /* n_freq + i), or (2i, 2i + 1) where interleaved != 0; pair i turns by position */
 /* * inv_freq[i]: (x, y) -> (x cos - y sin, y cos + x sin), in float32, rounded  */
-/* once; the other values are copied.  Angles are exact to 2^-30 for positions   */
-/* up to 2^20 and any frequency below 2 pi; positions count modulo 2^32.         */
+/* once; the other values are copied.  An angle, whole turns taken off, is off by  */
+/* 2^-30 + |position| * (2^-52 * |inv_freq| + 2^-62) radians at most before it is     */
+/* rounded to float32.  Positions are int32 and wrap as such.                        */
 /*   q, q_out [B,T,Hq,D], k, k_out [B,T,Hkv,D] dtype; k and k_out may both be     */
 /*   NULL with Hkv = 0; q_out may be q and k_out may be k                        */
 /*   kv_len [B] int32; depth [T] int32 or NULL; inv_freq [n_freq] float, finite   */

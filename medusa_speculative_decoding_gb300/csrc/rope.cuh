@@ -8,8 +8,10 @@
 //
 // p * inv_freq in float32 is off by 2^-25 p radians: 0.03 at a million tokens.  Here a
 // frequency is a 64-bit fraction of a revolution, so that p times it modulo 2^64 is the angle
-// after whole turns, off by p * 2^-64 revolutions and the 2^-53 of the fraction itself; two
-// integer products instead of 64-bit floating ones, of which an SM does two a cycle.
+// after whole turns, two integer products instead of 64-bit floating ones, of which an SM does
+// two a cycle.  The fraction comes from a double, off by 2^-52 of inv_freq / 2 pi and by 2^-65, so that
+// the angle is off by p (2^-52 |inv_freq| + 2^-62) radians, and is then rounded to 2^-32 revolutions:
+// by 2 pi * 2^-33 < 2^-30 radians.
 #pragma once
 
 #include <stdint.h>
@@ -33,9 +35,10 @@ __device__ __forceinline__ uint64_t turn(float inv_freq) {
 
 // (cos, sin) of p turns.  Within an eighth of a revolution of a multiple of a quarter, the series
 // of sine and cosine to the 9th and 10th power are off by 2^-29 and 2^-33 (the next terms, x^11 /
-// 11! and x^12 / 12!); what is left is the rounding of the angle and of the sums, 2^-24 each.
+// 11! and x^12 / 12!); what is left is the rounding of the angle to float32 (2^-25 at an eighth of a
+// revolution) and of the sums, 2^-24 each.
 __device__ __forceinline__ float2 cos_sin(uint64_t turn, int p) {
-    const uint32_t w = (uint32_t)((turn * (uint64_t)(int64_t)p) >> 32);  // units of 2^-32 revolutions
+    const uint32_t w = (uint32_t)((turn * (uint64_t)(int64_t)p + (1ull << 31)) >> 32);  // units of 2^-32 revolutions
     const uint32_t quarter = (w + (1u << 29)) >> 30;
     const float x = (float)(int32_t)(w - (quarter << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32
     const float z = x * x;
