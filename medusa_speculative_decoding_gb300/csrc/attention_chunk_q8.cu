@@ -987,7 +987,9 @@ __global__ void __launch_bounds__(THREADS) chunk_attn_q8_f32_kernel(const ChunkA
         auto place = [&](int r) { return (((size_t)at.b * w.T + at.j * w.tb + r / a.G) * a.Hq + at.h * a.G + r % a.G) * D; };
         for (int i = tid; i < ROWS * D; i += THREADS) {
             const int r = i / D;
-            sq[r * L::kStride + i % D] = real(r) && at.j * w.tb + r / a.G < at.n ? static_cast<const float*>(a.q)[place(r) + i % D] : 0.f;
+            const float x = real(r) && at.j * w.tb + r / a.G < at.n ? static_cast<const float*>(a.q)[place(r) + i % D] : 0.f;
+            // (an infinity as NaN: scores that are all -inf would look like keys that are not there)
+            sq[r * L::kStride + i % D] = fabsf(x) < INFINITY ? x : NAN;
         }
         if (tid < ROWS) {
             s_m[tid] = -INFINITY;
