@@ -217,12 +217,6 @@ __device__ __forceinline__ void split_planes(const uint4& x, float f, uint2& hi,
     lo = make_uint2((uint32_t)l[0] | (uint32_t)l[1] << 16, (uint32_t)l[2] | (uint32_t)l[3] << 16);
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 // 32 bytes, both 16-byte halves at once where the address allows
 __device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&w)[8], bool aligned) {
     if (aligned) {
@@ -235,8 +229,8 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&w)[8], boo
     }
 }
 
-// What a score is multiplied with; never 0, so that a masked one stays -inf (NaN stays NaN).
-__device__ __forceinline__ float factor(float k, float qf) { return max_nan(k * qf, FLT_MIN); }
+// What a score is multiplied with; never 0, so that a masked one stays -inf.
+__device__ __forceinline__ float factor(float k, float qf) { return fmaxf(k * qf, FLT_MIN); }
 
 __device__ __forceinline__ float max16(const float (&v)[16]) {
     float m0 = v[0], m1 = v[1];
@@ -527,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
                         uint8_t* to = base + 2 * (r >> 7) * L::kCodes + code_offset<D>(r & 127, lane % W >> 1) + (lane & 1) * 8;
                         *reinterpret_cast<uint2*>(to) = hi;
                         *reinterpret_cast<uint2*>(to + L::kCodes) = lo;
-                        if (lane % W == 0) s_qf[(segments & 1) * 2 * kRows + r] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : NAN;
+                        if (lane % W == 0) s_qf[(segments & 1) * 2 * kRows + r] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : -1.f;
                     }
                     if ((p + B) % PASSES == 0) {
                         fence_async_smem();
@@ -633,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             const int limit = real && token < at.n ? at.L - at.n + token : -1;  // the last slot that the row sees
             const bool any = __any_sync(0xffffffffu, limit >= 0);
             // ---- tiles ----
-            float ref = -INFINITY, l = 0.f, qf = 0.f;
+            float ref = -INFINITY, l = 0.f, qf = 0.f;  // qf < 0: the row's query is not finite
             const int ns = PAIR ? nt : (nt + 1 - s) / 2;
             if (ns) {
                 // The rows' factors.  (Where segments have one tile, the queries of the next segment, and in time
@@ -654,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const float4 f = sc[4 * h + g];
-                        kc[g] = f.z == 0.f ? 1.f : factor(f.x, qf);  // (an absent page's keys stay -inf whatever q holds)
+                        kc[g] = factor(f.x, fabsf(qf));
                         off[g] = f.y;
                         per_vs[g] = f.z;
                     }
@@ -744,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_q8_umma_kernel(const _
             const bool whole = nt == at.tiles;
             const bool split = !PAIR && nt > 1;  // both streams have an O
             if (limit < 0) { ref = -INFINITY; l = 0.f; }
+            if (qf < 0.f && l != 0.f) l = NAN;  // (its planes are zero, so that l says whether it sees a key)
             float m_out = ref, l_out = l, f0 = 1.f, f1 = 0.f;  // f: factors of this stream's O, or of both streams'
             if constexpr (!PAIR) {
                 float2* s_x = reinterpret_cast<float2*>(base + L::kOffX);
