@@ -507,7 +507,9 @@ int medusa_rope_rows(const void* q, const void* k, medusa_dtype dtype, const int
 /*   q, q_out [B,T,Hq,D] dtype, or both NULL with Hq = 0: the queries of the same   */
 /*   rows, rotated (rows must then be NULL and R = T); rows behind last[b] are      */
 /*   zero.  q_out may be q.  Queries are rotated whether or not the append is        */
-/*   refused on the device.                                                         */
+/*   refused on the device: what then attends with the same last (6g) would answer   */
+/*   from the slots before the refused rows.  With last = appended - 1 (-3 where the  */
+/*   sequence was refused) its rows are zero there.                                  */
 /* Limits: as 6b; n_freq as 6e; Hq <= 1024.                                         */
 int medusa_kv_append_rope_q8(const void* k_rows, const void* v_rows, medusa_dtype dtype, void* k_pages,
                              void* v_pages, float* k_scale, float* v_scale, const int32_t* page_table,
@@ -521,7 +523,9 @@ int medusa_kv_append_rope_q8(const void* k_rows, const void* v_rows, medusa_dtyp
 /* piece of one, or one decoded token (T = 1).  The rows 0..last[b] of q (all T      */
 /* where last is NULL) are those of the last n = last[b] + 1 slots that sequence b    */
 /* holds; their keys and values are in the pages (6b, 6f).  Row i sees the slots      */
-/* [0, kv_len[b] - n + i]:  out = softmax(scale * q.k) v.                            */
+/* [0, kv_len[b] - n + i]:  out = softmax(scale * q.k) v.  Behind an append that may    */
+/* have refused a sequence, last is what it wrote, appended - 1, not what it was asked   */
+/* to: the refused rows are not among the slots, and any last below 0 gives zeros.        */
 /*   q [B,T,Hq,D] dtype; kv_len [B] with the chunk; last [B] int32 or NULL            */
 /*   out [B,T,Hq,D] dtype, rounded once from float32; not q.  Rows behind last[b] and  */
 /*   rows that see no key are zero.                                                  */

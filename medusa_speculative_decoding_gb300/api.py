@@ -624,7 +624,9 @@ def kv_append_rope_q8(k_rows, v_rows, k_pages, v_pages, k_scale, v_scale, page_t
     """kv_append_q8 of K rows that are not rotated yet: row i turns by the position of its
     slot, kv_len[b] + i, on its way into the pages, and so do the queries q [B,T,Hq,D] of
     the same rows, where given (rows then has to be None).  Returns dict(kv_len, appended,
-    h_next, q); rows of q behind last[b] are zero; the pools change in place."""
+    h_next, q); rows of q behind last[b] are zero; the pools change in place.  A sequence
+    that is refused (appended -2) keeps its kv_len and its queries are rotated all the same:
+    chunk_attention_q8(.., last=appended - 1) answers such rows with zeros."""
     B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
     if _elsewhere(dev, stream):
         with torch.cuda.device(dev):
@@ -689,7 +691,8 @@ def chunk_attention_q8(q, k_pages, v_pages, k_scale, v_scale, page_table, kv_len
     """Attention of new tokens over the 8-bit paged cache that holds their keys already: row
     i of the last[b] + 1 rows of q [B,T,Hq,D] (all T where last is None) is that of slot
     kv_len[b] - last[b] - 1 + i and sees the slots up to it.  Returns out [B,T,Hq,D] in q's
-    type; rows behind last[b] are zero.  T = 1 is plain decoding."""
+    type; rows behind last[b] are zero.  T = 1 is plain decoding.  Behind an append that may
+    have refused a sequence, last is its appended - 1."""
     B, M, n_pages, Hkv, P, D, dev = _need_pool(k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
     if _elsewhere(dev, stream):
         with torch.cuda.device(dev):
