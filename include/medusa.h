@@ -321,10 +321,11 @@ int medusa_verify_accept_chain(const float* p, const float* q, const int32_t* dr
 /* of the round then follows the target's distribution.  The draw at depth d    */
 /* from row p with the caller's random number u = u[b,d] is the smallest v with   */
 /*   p_0 + ... + p_v > u * (p_0 + ... + p_{V-1})                                */
-/* (rows need not be normalised; entries below 0 and NaN count as 0, above 1 as 1;   */
-/* sums are off by 2^-37 of a row's total at most, where that is 2^-80 or more).      */
-/* u in [0,1):                                                                       */
-/* below it counts as 0; 1 and above give the last token that has any weight.       */
+/* A row is one of probabilities: it need not sum to 1, but entries below 0 and NaN    */
+/* count as 0, above 1 as 1, so that weights such as exp(logits) or counts have to be   */
+/* scaled to [0,1] first.  Sums are off by 2^-37 of a row's total at most, where that    */
+/* is 2^-80 or more.  u in [0,1): below it counts as 0; 1 and above give the last        */
+/* token that has any weight.                                                           */
 /*   probs [B,N,V] float: row u scores the token after node u; cand [B,N];          */
 /*   parent, depth [N] from the layout; u [B,Dmax+1] float                         */
 /* accept_len, best_node, path_nodes, next_tok as in 4a (next_tok: the drawn token    */

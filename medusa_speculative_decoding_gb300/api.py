@@ -350,7 +350,8 @@ def verify_accept_tree_draw(probs, cand, parent, depth, u, max_depth, out=None, 
     """Acceptance by drawn tokens: at each node of the path the token that u[b, depth]
     in [0, 1) picks from row probs[b, node] (the smallest v with p_0 + .. + p_v above u
     times the row's sum); the child that holds it is accepted, else it is next_tok.
-    probs [B,N,V] float32, u [B, max_depth + 1] float32."""
+    probs [B,N,V] float32, u [B, max_depth + 1] float32.  A row need not sum to 1, but its
+    entries count as at most 1 (below 0 and NaN: 0): weights above 1 are not told apart."""
     if probs is None or probs.dim() != 3:
         raise ValueError("probs must be [B, N, V]")
     _need(probs, "probs", torch.float32)

@@ -105,3 +105,16 @@ def test_large_vocabularies(medusa, n):
     got = medusa.verify_accept_tree_draw(to_dev(row).expand(B, 1, n).contiguous(), zero.expand(B, 1).contiguous(), zero - 1, zero,
                                          to_dev(u[:, None]), 0)
     assert np.array_equal(got["next_tok"].cpu().numpy(), drawn(sums, u))
+
+
+@pytest.mark.parametrize("B", [1, 64])
+def test_entries_above_one_count_as_one(medusa, B):
+    """What the header says of weights that are not scaled to [0, 1]: the row clipped to it is drawn from."""
+    rng = np.random.default_rng(5)
+    counts = rng.integers(-1, 6, (B, 2, 40000)).astype(np.float32)
+    node = torch.arange(2, dtype=torch.int32, device="cuda")
+    rest = to_dev(np.full((B, 2), 40001, np.int32)), node - 1, node, to_dev(rng.random((B, 2), dtype=np.float32)), 1
+    a = medusa.verify_accept_tree_draw(to_dev(counts), *rest)
+    b = medusa.verify_accept_tree_draw(to_dev(np.clip(counts, 0, 1)), *rest)
+    for name in a:
+        assert torch.equal(a[name], b[name])
