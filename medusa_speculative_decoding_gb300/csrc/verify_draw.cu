@@ -37,10 +37,17 @@ constexpr int kBatch = 4;         // float4 of a thread with their loads in flig
 constexpr int kMaxCluster = 8;
 constexpr int kSlice = 8192;      // values of a CTA, where the cluster can be that large
 constexpr int kMaxNodes = 512;
-// Bytes of rows up to which drawing from all of them beats walking: trees of 64 nodes took 10 us against 21 at
-// 8 MB (one, V = 32000), 25 against 19 at 31 MB (one, V = 128256), 37 against 31 (four, V = 32000) and 64 against
-// 39 at 62 MB (eight).
-constexpr long long kAllRows = 16ll << 20;
+// Bytes of rows, and CTAs for them, up to which drawing from all of them beats walking.  All take some 8 us for
+// every 304 CTAs (two an SM) or 20 MB, a walk 8 to 10 us a level, whatever the rows.  Measured, us, all / walking (trees
+// x nodes x tokens):
+//   up to 304 CTAs        9 x 1000 8 / 14; 64 x 8192 10 / 19; 64 x 32000 11 / 19; 300 x 8192 12 / 21; 32 x 128256 14 / 23;
+//                         4 x 9 x 128256 (18 MB) 14 / 30
+//   up to 1024            341 x 5000 18 / 19; 8 x 64 x 8192 21 / 42; 64 x 64000 20 / 16; 24 x 25 x 8000 (18 MB) 21 / 42; 341 x
+//                         10000 27 / 22; 2 x 341 x 6000 27 / 25; 16 x 64 x 4000 33 / 35; 64 x 16 x 2000 31 / 27
+//   more                  32 x 64 x 1000 52 / 42; 64 x 64 x 1000 99 / 45
+//   more bytes            12 x 64 x 8000 (23 MB) 29 / 47; 64 x 128256 (31 MB) 25 / 16; 38 x 300000 (43 MB) 41 / 27; 8 x 64 x
+//                         32000 (62 MB) 64 / 39
+constexpr long long kAllRows = 20ll << 20, kAllBlocks = 1024;
 
 struct DrawArgs {
     const float *probs, *u;
@@ -339,7 +346,7 @@ extern "C" int medusa_verify_accept_tree_draw(const float* probs, const int32_t*
     a.slice = (int)(((long long)(V + ctas - 1) / ctas + unit - 1) / unit * unit);
     cudaStream_t st = as_stream(stream);
     cudaError_t e;
-    if ((long long)B * N * V * 4 <= kAllRows || N == 1) {
+    if (((long long)B * N * V * 4 <= kAllRows && (long long)B * N * ctas <= kAllBlocks) || N == 1) {
         e = launch_cluster(draw_rows_kernel, dim3(ctas, N, B), dim3(kThreads), 0, st, ctas, a);
         if (e == cudaSuccess) e = launch(walk_kernel, dim3(B), dim3(256), 0, st, a);
     } else {
