@@ -19,10 +19,10 @@
 // A cluster of CTAs draws from one row: each CTA sums a contiguous slice, the totals are
 // pushed to every CTA, and the one whose slice holds the number finds the token in it.
 //   draw_walk_kernel  a cluster per sequence walks down the tree, a row per level: reads
-//                     only the rows that it visits, one level after the other (53 us for 32
+//                     only the rows that it visits, one level after the other (52 us for 32
 //                     trees of 64 nodes, 128256 tokens: the longest walk, 5 us a level)
 //   draw_rows_kernel  a cluster per row draws from all rows at once, and walk_kernel follows
-//                     the children: fewer steps in a row where there are few rows (10 us for 64
+//                     the children: fewer steps in a row where there are few rows (11 us for 64
 //                     nodes, 32000 tokens)
 #include <algorithm>
 
@@ -38,7 +38,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kSlice = 8192;      // values of a CTA, where the cluster can be that large
 constexpr int kMaxNodes = 512;
 // Bytes of rows, and CTAs for them, up to which drawing from all of them beats walking.  All take some 8 us for
-// every 304 CTAs (two an SM) or 20 MB, a walk 8 to 10 us a level, whatever the rows.  Measured, us, all / walking (trees
+// every 304 CTAs (two an SM) or 20 MB, a walk 5 to 9 us a level, whatever the rows.  Measured, us, all / walking (trees
 // x nodes x tokens):
 //   up to 304 CTAs        9 x 1000 8 / 14; 64 x 8192 10 / 19; 64 x 32000 11 / 19; 300 x 8192 12 / 21; 32 x 128256 14 / 23;
 //                         4 x 9 x 128256 (18 MB) 14 / 30
