@@ -172,7 +172,8 @@ __device__ __forceinline__ int draw(const DrawArgs& a, const float* row, Number 
         const float2 part = lane < ctas ? s.total[lane] : none;
         const float2 all = shfl2(scan(part), 31);
         const float un = fmaxf(number(), 0.f), ph = __fmul_rn(un, all.x);
-        const float2 target = two_sum(ph, __fadd_rn(__fmaf_rn(un, all.x, -ph), __fmul_rn(un, all.y)));
+        // (from 1 on the last token: no sum, whatever order it was added up in, lies behind infinity)
+        const float2 target = un >= 1.f ? make_float2(INFINITY, 0.f) : two_sum(ph, __fadd_rn(__fmaf_rn(un, all.x, -ph), __fmul_rn(un, all.y)));
         float2 base = none;
         bool over;
         const int winner = part_of(part, target, base, over);

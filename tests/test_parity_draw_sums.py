@@ -118,3 +118,19 @@ def test_entries_above_one_count_as_one(medusa, B):
     b = medusa.verify_accept_tree_draw(to_dev(np.clip(counts, 0, 1)), *rest)
     for name in a:
         assert torch.equal(a[name], b[name])
+
+
+@pytest.mark.parametrize("u", [1.0, 1.0000001, 3.5, float("inf")])
+@pytest.mark.parametrize("B,N,V", [(400, 1, 1003), (400, 1, 44914), (40, 5, 44914)])
+def test_from_one_on_the_last_token_with_weight(medusa, B, N, V, u):
+    """Rows whose last weights are below what any sum of them is rounded by."""
+    rng = np.random.default_rng(V)
+    z = rng.normal(0, 12, (B, V)).astype(np.float32)
+    p = np.exp(z - z.max(1, keepdims=True))
+    p[::3, -5:] = 0
+    p[1::3, -1] = np.float32(1e-44)
+    last = V - 1 - np.argmax(p[:, ::-1] > 0, 1)
+    node = torch.arange(N, dtype=torch.int32, device="cuda")
+    got = medusa.verify_accept_tree_draw(to_dev(p).view(B, 1, V).expand(B, N, V).contiguous(), to_dev(np.full((B, N), -1, np.int32)), node - 1, node,
+                                         torch.full((B, N), u, device="cuda"), N - 1)
+    assert np.array_equal(got["next_tok"].cpu().numpy(), last)
